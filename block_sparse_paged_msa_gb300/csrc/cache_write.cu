@@ -28,10 +28,7 @@
 // largest, 6 -- and each element the E2M1 code of x / (block scale * tensor
 // scale); every step round-to-nearest-even in fp32, a block whose scale code
 // is 0 stores zero codes.  A lane holds 8 elements, so a block is a lane pair.
-#include <cuda_fp4.h>
-#include <cuda_fp8.h>
-
-#include "msa_device.cuh"
+#include "kv_quant.cuh"
 
 namespace msa {
 namespace {
@@ -44,40 +41,6 @@ __device__ __forceinline__ uint4 ld_nc(const uint4* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
-}
-
-// Two bf16 (one 32-bit word) -> two e4m3 codes of x / scale (low value in the
-// low byte).
-__device__ __forceinline__ uint32_t bf16x2_to_e4m3x2(uint32_t w, float scale) {
-  const float2 f = make_float2(__fdiv_rn(bf16lo(w), scale), __fdiv_rn(bf16hi(w), scale));
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-}
-
-// Eight bf16 (this lane's part of a 16-element block; the partner lane, lane ^ 1,
-// holds the rest) -> four bytes of E2M1 pairs (even element in the low nibble)
-// and the block's E4M3 scale code, for tensor scale g.
-__device__ __forceinline__ uint32_t nvfp4_quantize8(const uint4& x, float g, uint8_t& scale) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float f[8], amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16lo(w[i]);
-    f[2 * i + 1] = bf16hi(w[i]);
-    amax = fmaxf(amax, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-  }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  const __nv_fp8_storage_t sc =
-      __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(6.f, g)), __NV_SATFINITE, __NV_E4M3);
-  scale = (uint8_t)sc;
-  const float d = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(sc, __NV_E4M3))), g);
-  if (d == 0.f) return 0u;
-  uint32_t codes = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 u = make_float2(__fdiv_rn(f[2 * i], d), __fdiv_rn(f[2 * i + 1], d));
-    codes |= (uint32_t)__nv_cvt_float2_to_fp4x2(u, __NV_E2M1, cudaRoundNearest) << (8 * i);
-  }
-  return codes;
 }
 
 // kv: the pools' MSA_KV_* type.  The K and V pools may be one allocation (NVFP4
@@ -120,14 +83,21 @@ cache_write_kernel(WsView ws, int Hkv, int max_blocks, int64_t pool_slots, int i
     // slot 2h (keys) or 2h + 1 (values) of the page, 72-byte rows
     const int64_t r4 = ((slot / kBlock * Hkv + h) * 2 + half) * kBlock + slot % kBlock;
     uint8_t* dst = pool + r4 * kFp4Row;
+    // the lane holds half of a 16-element block, its partner (lane ^ 1) the rest
+    float f[8];
+    bf16x8_to_f32(x, f);
+    float amax = amax8(f);
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     uint8_t scale;
-    const uint32_t codes = nvfp4_quantize8(x, half ? v_scale : k_scale, scale);
+    const uint32_t codes = nvfp4_codes8(f, amax, half ? v_scale : k_scale, scale);
     reinterpret_cast<uint32_t*>(dst)[c] = codes;
     if ((c & 1) == 0) dst[kHeadDim / 2 + c / 2] = scale;
   } else {
     const float s = half ? v_scale : k_scale;
-    const uint32_t lo = bf16x2_to_e4m3x2(x.x, s) | bf16x2_to_e4m3x2(x.y, s) << 16;
-    const uint32_t hi = bf16x2_to_e4m3x2(x.z, s) | bf16x2_to_e4m3x2(x.w, s) << 16;
+    float f[8];
+    bf16x8_to_f32(x, f);
+    const uint32_t lo = e4m3x2_of(f[0], f[1], s) | e4m3x2_of(f[2], f[3], s) << 16;
+    const uint32_t hi = e4m3x2_of(f[4], f[5], s) | e4m3x2_of(f[6], f[7], s) << 16;
     reinterpret_cast<uint2*>(pool)[row * 16 + c] = make_uint2(lo, hi);
   }
   if (idx_k != nullptr && lane < idx_lanes)

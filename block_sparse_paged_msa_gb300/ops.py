@@ -22,7 +22,8 @@ KV_DTYPES = {"bf16": MSA_KV_BF16, "fp8_e4m3": MSA_KV_FP8_E4M3, "nvfp4": MSA_KV_N
 MSA_MODE_DECODE, MSA_MODE_PREFILL = 0, 1
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED",
           3: "MSA_ERR_CUDA", 4: "MSA_ERR_DEVICE_FLAG"}
-DEVERR_BITS = {1: "PAGE_RANGE", 2: "SEQ_LEN", 4: "SLOT_ALIGN", 8: "TIMEOUT", 16: "FP16_RANGE"}
+DEVERR_BITS = {1: "PAGE_RANGE", 2: "SEQ_LEN", 4: "SLOT_ALIGN", 8: "TIMEOUT", 16: "FP16_RANGE",
+               32: "POSITION"}
 
 
 class MsaError(RuntimeError):
@@ -50,6 +51,18 @@ class MsaConfig(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class MsaRope(ctypes.Structure):
+    """Mirror of ``msa_rope`` in include/msa.h (field order matters)."""
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p), ("idx_cos_sin", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32), ("idx_rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("num_positions", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("idx_q_stride", ctypes.c_int64),
+        ("idx_k_stride", ctypes.c_int64), ("idx_v_stride", ctypes.c_int64),
+    ]
+
+
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MsaConfig)
 _SIGNATURES = {
@@ -66,6 +79,9 @@ _SIGNATURES = {
                                                   ctypes.c_int32, _P, _P, _P]),
     "msa_index_score": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P]),
     "msa_cache_write": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "msa_rope_cache_write": (ctypes.c_int, [_CFG, _P, ctypes.POINTER(MsaRope)] + [_P] * 15),
+    "msa_dense_decode_scratch_bytes": (ctypes.c_size_t, [_CFG]),
+    "msa_dense_decode": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P]),
     "msa_index_attention_scratch_bytes": (ctypes.c_size_t, [_CFG]),
     "msa_index_attention": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P]),
     "msa_topk_select": (ctypes.c_int, [_CFG, _P, _P, _P, _P]),
@@ -362,6 +378,79 @@ def cache_write(cfg, ws, k, v, idx_k, k_pages, v_pages, idx_k_pages, out_cache_l
         _stream(stream)))
 
 
+def _need_rows(t, name, T, heads, width):
+    """A projection's rows [>= T, heads, width] bf16: heads contiguous, tokens
+    at any stride that is a multiple of 8.  Returns that stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the config needs "
+                         f"[{T}, {heads}, {width}]")
+    if t.shape[0] < T:
+        raise ValueError(f"{name} has {t.shape[0]} rows on dim 0, the config needs {T}")
+    tok, hd, el = t.stride()
+    if el != 1 or (heads > 1 and hd != width) or (T > 1 and tok % 8) or t.data_ptr() % 16:
+        raise ValueError(f"{name}: a token's heads must be contiguous, 16-byte aligned, at a "
+                         f"stride that is a multiple of 8 elements")
+    return tok if T > 1 else heads * width
+
+
+def _need_table(t, name):
+    _need(t, name, torch.float32, 2)
+    return t.shape[0], t.shape[1]
+
+
+def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, k_pages, v_pages,
+                     idx_k_pages, *, interleaved=False, idx_cos_sin=None, positions=None,
+                     out_cache_loc=None, idx_v=None, idx_v_pages=None, stream=None):
+    """Rotate the step's new queries and keys by their positions and store K / V
+    / index-K (and index-V) into the pools, after plan(), in place of
+    cache_write() (msa_rope_cache_write).  q [T, H_q, D], k, v [T, H_kv, D],
+    idx_q, idx_k, idx_v [T, H_kv, d] bf16 with any token stride (slices of a
+    fused projection), idx_* may be None.  cos_sin [positions, rotary_dim]
+    fp32: cosines, then sines; idx_cos_sin the index heads' own table, None =
+    cos_sin.  q_out, idx_q_out: the rotated queries, contiguous; each may be its
+    input.  positions: [T] int64, None = the plan's."""
+    _need_ws(cfg, ws)
+    T, hq, hkv, d = max_tokens(cfg), cfg.num_q_heads, cfg.num_kv_heads, cfg.index_dim
+    r = MsaRope()
+    r.q_stride = _need_rows(q, "q", T, hq, cfg.head_dim)
+    r.k_stride = _need_rows(k, "k", T, hkv, cfg.head_dim)
+    r.v_stride = _need_rows(v, "v", T, hkv, cfg.head_dim)
+    r.num_positions, r.rotary_dim = _need_table(cos_sin, "cos_sin")
+    r.cos_sin, r.interleaved = cos_sin.data_ptr(), bool(interleaved)
+    _need_tokens(cfg, T, q=q_out)
+    if idx_q is not None:
+        r.idx_q_stride = _need_rows(idx_q, "idx_q", T, hkv, d)
+        _need_tokens(cfg, T, idx_q=idx_q_out)
+    if idx_k is not None:
+        r.idx_k_stride = _need_rows(idx_k, "idx_k", T, hkv, d)
+        _need_pools(cfg, idx_k_pages=idx_k_pages)
+        _need(idx_k_pages, "idx_k_pages")
+    if idx_v is not None:
+        r.idx_v_stride = _need_rows(idx_v, "idx_v", T, hkv, d)
+        _need(idx_v_pages, "idx_v_pages", torch.bfloat16, 4, cfg.num_pages,
+              (hkv, cfg.block_size, d))
+    if idx_cos_sin is not None:
+        n, r.idx_rotary_dim = _need_table(idx_cos_sin, "idx_cos_sin")
+        r.num_positions = min(r.num_positions, n)
+        r.idx_cos_sin = idx_cos_sin.data_ptr()
+    else:
+        r.idx_rotary_dim = r.rotary_dim
+    _need_pools(cfg, k_pages, v_pages)
+    if positions is not None:
+        _need(positions, "positions", torch.int64, 1, T)
+    if out_cache_loc is not None:
+        _need(out_cache_loc, "out_cache_loc", torch.int64, 1, T)
+    _check("msa_rope_cache_write", lib().msa_rope_cache_write(
+        ctypes.byref(cfg), _ptr(ws), ctypes.byref(r), _ptr(q), _ptr(k), _ptr(v), _ptr(idx_q),
+        _ptr(idx_k), _ptr(idx_v), _ptr(positions), _ptr(out_cache_loc), _ptr(q_out),
+        _ptr(idx_q_out), _ptr(k_pages), _ptr(v_pages), _ptr(idx_k_pages), _ptr(idx_v_pages),
+        _stream(stream)))
+
+
 def index_attention_scratch_bytes(cfg) -> int:
     return lib().msa_index_attention_scratch_bytes(ctypes.byref(cfg))
 
@@ -474,6 +563,30 @@ def paged_decode(cfg, ws, q, k_pages, v_pages, page_table, dense_len, stream=Non
         _ptr(dense_len), _stream(stream)))
 
 
+def dense_decode_scratch_bytes(cfg) -> int:
+    n = lib().msa_dense_decode_scratch_bytes(ctypes.byref(cfg))
+    if n == 0:
+        _check("msa_dense_decode_scratch_bytes", validate_config(cfg) or 2)
+    return n
+
+
+def dense_decode(cfg, ws, q, k_pages, v_pages, scratch, out, lse, stream=None):
+    """Attention of every new token over its request's whole context, held in
+    NVFP4 pools (msa_dense_decode): the full-attention layers of a model, after
+    plan() and the cache write of the step; no combine() follows.  scratch of
+    dense_decode_scratch_bytes(cfg) bytes."""
+    _need_ws(cfg, ws)
+    _need_tokens(cfg, max_tokens(cfg), q=q, out=out, lse=lse)
+    _need_pools(cfg, k_pages, v_pages)
+    _need(scratch, "scratch", torch.uint8)
+    n = dense_decode_scratch_bytes(cfg)
+    if scratch.numel() < n:
+        raise ValueError(f"scratch has {scratch.numel()} bytes, the config needs {n}")
+    _check("msa_dense_decode", lib().msa_dense_decode(
+        ctypes.byref(cfg), _ptr(ws), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(scratch),
+        _ptr(out), _ptr(lse), _stream(stream)))
+
+
 def combine(cfg, ws, out, lse, stream=None):
     _need_ws(cfg, ws)
     _need_tokens(cfg, max_tokens(cfg), out=out, lse=lse)
@@ -528,16 +641,34 @@ def selftest_wait_timeout(cfg: MsaConfig, ws, stream=None):
 
 
 # ---------------------------------------------------------------- the step
+class Rope:
+    """A model's rotary embedding: cos_sin [positions, rotary_dim] fp32
+    (cosines, then sines), idx_cos_sin the index heads' own table or None."""
+
+    def __init__(self, cos_sin, interleaved: bool = False, idx_cos_sin=None):
+        self.cos_sin, self.interleaved, self.idx_cos_sin = cos_sin, interleaved, idx_cos_sin
+
+    def write(self, cfg, ws, q, k, v, idx_q, idx_k, q_out, idx_q_out, k_pages, v_pages,
+              idx_k_pages, out_cache_loc=None, stream=None):
+        rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, self.cos_sin, q_out, idx_q_out, k_pages,
+                         v_pages, idx_k_pages, interleaved=self.interleaved,
+                         idx_cos_sin=self.idx_cos_sin, out_cache_loc=out_cache_loc,
+                         stream=stream)
+
+
 class SparseAttention:
     """Owns the buffers of one configuration and runs the whole path:
     plan -> index score -> top-k select -> sparse decode -> combine."""
 
-    def __init__(self, cfg: MsaConfig, device="cuda", dense_sparse: bool = False):
+    def __init__(self, cfg: MsaConfig, device="cuda", dense_sparse: bool = False,
+                 rope: Optional[Rope] = None):
         """dense_sparse: decode through the compacted page table and the dense
         paged decode (msa_compact_selected + msa_paged_decode) instead of the
-        sparse decode over the selected lists."""
+        sparse decode over the selected lists.  rope: rotate the step's new
+        queries and keys with it as run() stores them (rope_cache_write)."""
         self.cfg = cfg
         self.dense_sparse = dense_sparse
+        self.rope = rope
         _check("msa_validate_config", validate_config(cfg))
         T = cfg.max_q_tokens or cfg.max_batch * cfg.q_len
         self.max_tokens = T
@@ -551,6 +682,10 @@ class SparseAttention:
                                device=device)
         self.lse = torch.empty((T, cfg.num_q_heads), dtype=torch.float32, device=device)
         self.prefill = cfg.mode == MSA_MODE_PREFILL
+        if rope is not None:
+            self.q_rot = torch.empty_like(self.out)
+            self.idx_q_rot = torch.empty((T, cfg.num_kv_heads, cfg.index_dim),
+                                         dtype=torch.bfloat16, device=device)
         if dense_sparse:
             if self.prefill:
                 raise ValueError("the dense-sparse form is a decode form")
@@ -567,14 +702,21 @@ class SparseAttention:
         split-K decode, combine).  Prefill (cu_seqlens_q required): plan, index
         score, top-k, CSR, sparse prefill tiles, combine.  new_kv = (k, v,
         idx_k) first stores the step's new rows into the pools (cache_write,
-        right after the plan; slots from out_cache_loc or from the plan)."""
+        right after the plan; slots from out_cache_loc or from the plan).  With
+        a rope, q, idx_q and the new keys come unrotated and new_kv is needed."""
         c = self.cfg
+        if self.rope is not None and new_kv is None:
+            raise ValueError("a rope rotates a step's new rows: new_kv is needed")
         if not self.prefill and cu_seqlens_q is None and new_kv is None and not self.dense_sparse:
             decode_step(c, self.ws, seq_lens, block_table, idx_q, idx_k_pages, q, k_pages,
                         v_pages, self.block_scores, self.selected, self.out, self.lse, stream)
             return self.out, self.lse
         plan(c, seq_lens, block_table, self.ws, cu_seqlens_q, stream)
-        if new_kv is not None:
+        if self.rope is not None:
+            self.rope.write(c, self.ws, q, new_kv[0], new_kv[1], idx_q, new_kv[2], self.q_rot,
+                            self.idx_q_rot, k_pages, v_pages, idx_k_pages, out_cache_loc, stream)
+            q, idx_q = self.q_rot, self.idx_q_rot
+        elif new_kv is not None:
             cache_write(c, self.ws, *new_kv[:3], k_pages, v_pages, idx_k_pages, out_cache_loc,
                         stream)
         index_score_topk(c, self.ws, idx_q, idx_k_pages, self.block_scores, self.selected, stream)
@@ -588,6 +730,48 @@ class SparseAttention:
         else:
             sparse_decode(c, self.ws, q, k_pages, v_pages, self.selected, stream)
         combine(c, self.ws, self.out, self.lse, stream)
+        return self.out, self.lse
+
+
+class DenseAttention:
+    """Owns the buffers of one full-attention layer shape (NVFP4 KV, decode /
+    verify) and runs it: plan -> cache write -> dense decode.  Layers of one
+    step may share a plan: pass ws, planned by SparseAttention.run or plan()
+    with the same config, and run(planned=True)."""
+
+    def __init__(self, cfg: MsaConfig, device="cuda", ws=None, rope: Optional[Rope] = None):
+        self.cfg = cfg
+        self.rope = rope
+        _check("msa_validate_config", validate_config(cfg))
+        T = max_tokens(cfg)
+        self.max_tokens = T
+        self.scratch = torch.empty(dense_decode_scratch_bytes(cfg), dtype=torch.uint8,
+                                   device=device)
+        self.ws = torch.empty(workspace_bytes(cfg), dtype=torch.uint8,
+                              device=device) if ws is None else ws
+        self.out = torch.empty((T, cfg.num_q_heads, cfg.head_dim), dtype=torch.bfloat16,
+                               device=device)
+        self.lse = torch.empty((T, cfg.num_q_heads), dtype=torch.float32, device=device)
+        if rope is not None:
+            self.q_rot = torch.empty_like(self.out)
+
+    def run(self, seq_lens, block_table, q, k_pages, v_pages, cu_seqlens_q=None, stream=None,
+            new_kv=None, out_cache_loc=None, planned=False):
+        """new_kv = (k, v) first stores the step's new rows into the pools; with
+        a rope, q and k are rotated by their positions on the way."""
+        c = self.cfg
+        if self.rope is not None and new_kv is None:
+            raise ValueError("a rope rotates a step's new rows: new_kv is needed")
+        if not planned:
+            plan(c, seq_lens, block_table, self.ws, cu_seqlens_q, stream)
+        if self.rope is not None:
+            self.rope.write(c, self.ws, q, *new_kv[:2], None, None, self.q_rot, None, k_pages,
+                            v_pages, None, out_cache_loc, stream)
+            q = self.q_rot
+        elif new_kv is not None:
+            cache_write(c, self.ws, *new_kv[:2], None, k_pages, v_pages, None, out_cache_loc,
+                        stream)
+        dense_decode(c, self.ws, q, k_pages, v_pages, self.scratch, self.out, self.lse, stream)
         return self.out, self.lse
 
 

@@ -99,12 +99,13 @@ enum {
                                   or the step's tokens exceed max_q_tokens        */
   MSA_DEVERR_SLOT_ALIGN = 4,   /* req_to_token slot of a block not page-aligned   */
   MSA_DEVERR_TIMEOUT = 8,      /* a pipeline wait gave up (results invalid)       */
-  MSA_DEVERR_FP16_RANGE = 16   /* a bf16 value beyond the fp16 range (|x| > 65504,
+  MSA_DEVERR_FP16_RANGE = 16,  /* a bf16 value beyond the fp16 range (|x| > 65504,
                                   or infinite) met an fp16 operand: the queries
-                                  of the fp8 / NVFP4 decode, the values of the
+                                  of the fp8 / NVFP4 decodes, the values of the
                                   prefill tiles (results involving it invalid).
                                   Magnitudes below 2^-14 are not flagged; they
                                   keep fp16's subnormal precision only.          */
+  MSA_DEVERR_POSITION = 32     /* a position outside the rotation table           */
 };
 
 /*
@@ -242,6 +243,57 @@ msa_status msa_cache_write(const msa_config* cfg, void* ws, const int64_t* out_c
                            msa_stream_t stream);
 
 /*
+ * Rotary position embedding of msa_rope_cache_write.  A table holds, for every
+ * position, the cosines of the rotary_dim / 2 angles, then their sines (fp32;
+ * angles of far positions are best computed in 64 bits).
+ */
+typedef struct msa_rope {
+  const float* cos_sin;       /* [num_positions, rotary_dim]                      */
+  const float* idx_cos_sin;   /* [num_positions, idx_rotary_dim] for the index
+                                 heads, or NULL: cos_sin (idx_rotary_dim is then
+                                 0 or rotary_dim)                                 */
+  int32_t rotary_dim;         /* of the 128 dims of q and k; a multiple of 32      */
+  int32_t idx_rotary_dim;     /* of the d dims of idx_q and idx_k; 0 = not rotated */
+  int32_t interleaved;        /* 0: dims i and i + rotary_dim / 2 form pair i;
+                                 1: dims 2i and 2i + 1                            */
+  int64_t num_positions;      /* rows of the tables                               */
+  int64_t q_stride, k_stride, v_stride;             /* elements from one token's row */
+  int64_t idx_q_stride, idx_k_stride, idx_v_stride; /* to the next (multiples of 8)  */
+} msa_rope;
+
+/*
+ * msa_rope_cache_write -- msa_cache_write of rows that are not rotated yet: the
+ * step's queries and keys (and index queries and keys) are rotated by their
+ * positions on the way, and the keys, values and index rows stored into the
+ * pools.  Run it after msa_plan, in place of msa_cache_write; the attention
+ * calls of the step then take q_out and idx_q_out.
+ *   q [T, H_q, D], k, v [T, H_kv, D], idx_q, idx_k, idx_v [T, H_kv, d]: bf16, a
+ *                  token's heads contiguous, tokens at rope->*_stride elements
+ *                  (slices of a fused projection row need no copy); idx_q,
+ *                  idx_k and idx_v may be NULL
+ *   positions      [T] int64, or NULL: the plan's
+ *   out_cache_loc  as msa_cache_write; the slots of a step must be distinct (of
+ *                  tokens that share one, the stored row is unspecified)
+ *   q_out [T, H_q, D], idx_q_out [T, H_kv, d]: bf16, contiguous; each may be its
+ *                  input if that is contiguous
+ * A pair (x, y) at angle (c, s) becomes (x c - y s, y c + x s), every product,
+ * difference and sum one IEEE fp32 operation; dims past rotary_dim are copied.
+ * Queries are rounded to bf16 once; keys go from fp32 to the pool's type in one
+ * rounding (the quantisers of msa_cache_write); values and idx_v are stored as
+ * by msa_cache_write.  Tokens of idle requests are skipped.  A token whose
+ * position lies outside the table is skipped and sets MSA_DEVERR_POSITION; a
+ * slot outside the pool leaves the pools as they are (q_out and idx_q_out are
+ * written) and sets MSA_DEVERR_PAGE_RANGE.  Pointers 16-byte aligned.  Either
+ * mode, every KV dtype.
+ */
+msa_status msa_rope_cache_write(const msa_config* cfg, void* ws, const msa_rope* rope,
+                                const void* q, const void* k, const void* v, const void* idx_q,
+                                const void* idx_k, const void* idx_v, const int64_t* positions,
+                                const int64_t* out_cache_loc, void* q_out, void* idx_q_out,
+                                void* k_pages, void* v_pages, void* idx_k_pages,
+                                void* idx_v_pages, msa_stream_t stream);
+
+/*
  * msa_index_attention -- the index-value branch's output (sglang
  * MiniMaxSparseAttnBackend: layers outside disable_value_layer_ids keep an
  * index-value cache, get_index_kv_buffer, and the sparse ops return (idx_o, o)
@@ -351,6 +403,29 @@ msa_status msa_compact_selected(const msa_config* cfg, const void* ws, const int
 msa_status msa_paged_decode(const msa_config* cfg, void* ws, const void* q, const void* k_pages,
                             const void* v_pages, const int32_t* page_table,
                             const int32_t* seq_lens, msa_stream_t stream);
+
+/*
+ * msa_dense_decode -- attention over the whole context (the full-attention
+ * layers beside the sparse ones; sglang MiniMaxHybridAttnBackend routes them to
+ * a dense backend), read from the NVFP4 pools, decode mode.  For each token t
+ * and query head, over the keys at positions <= position(t):
+ *     out = sum_u softmax_u(softmax_scale q . k_u) v_u,  lse = natural-log sum
+ * A request's cache is read once for all its new tokens.  Run it after msa_plan
+ * (and the cache write) of the step, once per full-attention layer; it needs no
+ * msa_combine.
+ *   scratch  msa_dense_decode_scratch_bytes(cfg) bytes, 256-byte aligned, no
+ *            initialisation needed; calls that overlap on the GPU need one each
+ *   out [T, H_q, D] bf16 (16-byte aligned), lse [T, H_q] float
+ * NVFP4 KV only, and H_q / H_kv * q_len <= 64, else MSA_ERR_UNSUPPORTED.  A
+ * request with more new tokens than cfg->q_len (possible through cu_seqlens_q)
+ * sets MSA_DEVERR_SEQ_LEN; it and idle requests get out = 0, lse = -inf.  Pages
+ * that the plan flagged are skipped.  Rows of out and lse from T on are left as
+ * they are.
+ */
+size_t msa_dense_decode_scratch_bytes(const msa_config* cfg);
+msa_status msa_dense_decode(const msa_config* cfg, void* ws, const void* q, const void* k_pages,
+                            const void* v_pages, void* scratch, void* out, float* lse,
+                            msa_stream_t stream);
 
 /*
  * msa_combine -- log-sum-exp merge of the split-K partials in ws

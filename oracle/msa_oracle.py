@@ -45,6 +45,7 @@ __all__ = [
     "attention", "combine", "sparse_attention", "build_k2q_csr", "e4m3_encode",
     "cache_slots", "cache_write", "e2m1_to_float", "nvfp4_dequant", "nvfp4_row_bytes",
     "NVFP4_BLOCK", "e2m1_encode", "nvfp4_quantize", "cache_write_nvfp4", "compact_selection", "paged_attention", "index_attention",
+    "rotate_rows", "bf16_round", "dense_attention",
 ]
 
 
@@ -500,6 +501,61 @@ def cache_write_nvfp4(pool: np.ndarray, slots: Sequence[int], rows: np.ndarray, 
         for h in range(H):
             out[page, 2 * h + kind, row, :] = nvfp4_quantize(rows[t, h], scale)
     return out
+
+
+# --------------------------------------------------------------------------
+# Rotary position embedding on the way into the cache, and the dense attention
+# of the full-attention layers (sglang MiniMaxHybridAttnBackend routes a layer
+# to the sparse or to a dense backend by its id).
+# --------------------------------------------------------------------------
+def rotate_rows(x: np.ndarray, cos: np.ndarray, sin: np.ndarray, interleaved: bool) -> np.ndarray:
+    """Rows x [T, H, W] rotated by the angles of each token, cos / sin [T, n],
+    as float32: pair i of a row is (x_i, x_{i + n}), or (x_2i, x_2i+1) when
+    interleaved, and becomes (a cos - b sin, b cos + a sin) with every product,
+    difference and sum one IEEE fp32 operation; dims past 2 n are copied."""
+    y = np.asarray(x, dtype=np.float32).copy()
+    n = cos.shape[1]
+    ia = np.arange(0, 2 * n, 2) if interleaved else np.arange(n)
+    ib = ia + (1 if interleaved else n)
+    c = np.asarray(cos, dtype=np.float32)[:, None, :]
+    s = np.asarray(sin, dtype=np.float32)[:, None, :]
+    a, b = y[..., ia], y[..., ib]
+    y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
+    return y
+
+
+def bf16_round(x: np.ndarray) -> np.ndarray:
+    """float32 values rounded to the nearest bf16, ties to even, as float64
+    (finite inputs within the bf16 range)."""
+    u = np.ascontiguousarray(x, dtype=np.float32).view(np.uint32).astype(np.uint64)
+    u = (u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000
+    return u.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def dense_attention(*, seq_lens, q_lens, block_table, q, k, v, num_kv_heads: int,
+                    block_size: int, softmax_scale: float):
+    """Every query token attends to all tokens of its request at positions <=
+    its own: q [T, H_q, D], k, v [pages, H_kv, P, D] dequantised pools, T =
+    sum(q_lens).  Returns out [T, H_q, D], lse [T, H_q] and the attention of
+    |v| (the scale of the output's rounding errors)."""
+    T, H_q, D = q.shape
+    G = H_q // num_kv_heads
+    out, mag = np.zeros((T, H_q, D)), np.zeros((T, H_q, D))
+    lse = np.full((T, H_q), -np.inf)
+    cache = (None, None, None)
+    for t, (r, p) in enumerate(query_positions(seq_lens, q_lens)):
+        if p < 0:
+            continue
+        if cache[0] != r:
+            L = int(seq_lens[r])
+            cache = (r, gather_sequence(k, block_table[r], L, block_size),
+                     gather_sequence(v, block_table[r], L, block_size))
+        for h in range(num_kv_heads):
+            rows = slice(h * G, (h + 1) * G)
+            kk, vv = cache[1][:p + 1, h], cache[2][:p + 1, h]
+            out[t, rows], lse[t, rows] = attention(q[t, rows], kk, vv, softmax_scale)
+            mag[t, rows], _ = attention(q[t, rows], kk, np.abs(vv), softmax_scale)
+    return out, lse, mag
 
 
 # --------------------------------------------------------------------------

@@ -1,0 +1,291 @@
+"""msa_rope_cache_write: the rotary embedding applied on the way into the pools.
+
+The rotation is byte work too: its products, differences and sums are single
+IEEE fp32 operations, so the rotated queries (rounded to bf16 once) and the
+pools after the write -- bf16 rows, e4m3 codes, NVFP4 rows -- must equal the
+oracle's byte for byte, for both pair layouts, partial rotations, an index
+table of its own, strided rows of a fused projection, explicit positions and
+slots.  Refused arguments are checked without a GPU."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_paged_msa_gb300 as msa
+import oracle
+from block_sparse_paged_msa_gb300 import ops
+from block_sparse_paged_msa_gb300 import workloads as wl
+from oracle_io import to_np
+
+INVALID, UNSUPPORTED = 1, 2
+
+
+# ------------------------------------------------------------ oracle pins (CPU)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_oracle_rotation_is_the_complex_product(interleaved):
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((5, 3, 128)).astype(np.float32)
+    ang = rng.uniform(0, 6, (5, 32))
+    y = oracle.rotate_rows(x, np.cos(ang), np.sin(ang), interleaved).astype(np.float64)
+    a, b = (x[..., 0:64:2], x[..., 1:64:2]) if interleaved else (x[..., :32], x[..., 32:64])
+    z = (a + 1j * b) * np.exp(1j * ang)[:, None, :]
+    ya, yb = (y[..., 0:64:2], y[..., 1:64:2]) if interleaved else (y[..., :32], y[..., 32:64])
+    # three roundings of a value of magnitude <= |z|, and the table's
+    assert np.all(np.abs(ya - z.real) <= 4 * 2.0 ** -24 * 2 * np.abs(z))
+    assert np.all(np.abs(yb - z.imag) <= 4 * 2.0 ** -24 * 2 * np.abs(z))
+    assert np.array_equal(y[..., 64:], x[..., 64:])
+
+
+def test_oracle_bf16_rounding():
+    x = np.concatenate([np.random.default_rng(4).standard_normal(4096) * 3,
+                        [0.0, 1.0, 1.0 + 2.0 ** -8, 1.0 + 3 * 2.0 ** -8, -1.0 - 2.0 ** -8]])
+    want = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).double().numpy()
+    assert np.array_equal(oracle.bf16_round(x.astype(np.float32)), want)
+
+
+# ------------------------------------------------------------ refusals (CPU)
+def _args(**kw):
+    """Arguments that pass every host check, as a dict of plain numbers."""
+    a = dict(q=16, k=16, v=16, iq=16, ik=16, iv=None, pos=None, loc=None, qo=16, iqo=16, kp=16,
+             vp=16, ikp=16, ivp=None, cs=16, ics=None, rot=64, irot=64, n=100, qs=1024, ks=128,
+             vs=128, iqs=64, iks=64, ivs=64, ws=256)
+    a.update(kw)
+    return a
+
+
+def _call(cfg, a):
+    P = ctypes.c_void_p
+    r = ops.MsaRope()
+    r.cos_sin, r.idx_cos_sin = a["cs"], a["ics"]
+    r.rotary_dim, r.idx_rotary_dim, r.num_positions = a["rot"], a["irot"], a["n"]
+    for f, n in (("q_stride", "qs"), ("k_stride", "ks"), ("v_stride", "vs"),
+                 ("idx_q_stride", "iqs"), ("idx_k_stride", "iks"), ("idx_v_stride", "ivs")):
+        setattr(r, f, a[n])
+    return ops.lib().msa_rope_cache_write(
+        ctypes.byref(cfg), P(a["ws"]), ctypes.byref(r),
+        *[P(a[n]) for n in ("q", "k", "v", "iq", "ik", "iv", "pos", "loc", "qo", "iqo", "kp",
+                            "vp", "ikp", "ivp")], None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(ws=None), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
+    (dict(v=None), INVALID), (dict(cs=None), INVALID), (dict(qo=None), INVALID),
+    (dict(kp=None), INVALID), (dict(vp=None), INVALID),
+    (dict(iqo=None), INVALID), (dict(ikp=None), INVALID), (dict(iv=16), INVALID),
+    (dict(rot=0), INVALID), (dict(rot=160), INVALID), (dict(irot=-32), INVALID),
+    (dict(irot=96), INVALID),                        # > index_dim
+    (dict(rot=48), UNSUPPORTED), (dict(irot=16, ics=16), UNSUPPORTED),
+    (dict(irot=32), INVALID),                        # not the heads' table's width
+    (dict(n=0), INVALID),
+    (dict(qs=1023), INVALID), (dict(qs=1016), INVALID), (dict(ks=120), INVALID),
+    (dict(vs=132), INVALID), (dict(iqs=60), INVALID), (dict(iks=68), INVALID),
+    (dict(q=24), INVALID), (dict(k=8), INVALID), (dict(v=8), INVALID), (dict(cs=8), INVALID),
+    (dict(ics=8), INVALID), (dict(qo=8), INVALID), (dict(iqo=8), INVALID), (dict(kp=8), INVALID),
+    (dict(vp=8), INVALID), (dict(ikp=8), INVALID), (dict(iq=8), INVALID), (dict(ik=8), INVALID),
+])
+def test_refused_on_the_host(bad, status):
+    cfg = msa.config_for(wl.WORKLOADS["tiny_decode"])        # 8 query heads, 1 KV head, d = 64
+    assert _call(cfg, _args(**bad)) == status
+    cfg.head_dim = 64
+    assert _call(cfg, _args(**bad)) == UNSUPPORTED           # the config is checked first
+
+
+def test_rows_layouts_refused_by_the_binding():
+    with pytest.raises(ValueError, match="CUDA"):
+        ops._need_rows(torch.zeros(2, 1, 128, dtype=torch.bfloat16), "q", 2, 1, 128)
+
+
+# ------------------------------------------------------------ parity (GPU)
+def _table(n, rot, device="cuda"):
+    inv = 1.0e4 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    ang = torch.arange(n, dtype=torch.float64)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], dim=1).float().to(device)
+
+
+def _fused(spec, T, seed, extra=8):
+    """q | k | v | idx_q | idx_k | idx_v as slices of one projection row."""
+    hq, hkv, d, D = spec.num_q_heads, spec.num_kv_heads, spec.index_dim, spec.head_dim
+    widths = [hq * D, hkv * D, hkv * D, hkv * d, hkv * d, hkv * d]
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    row = torch.randn((T, sum(widths) + extra), generator=gen, device="cuda").to(torch.bfloat16)
+    parts = torch.split(row[:, :sum(widths)], widths, dim=1)
+    return [p.reshape(T, -1, w) if T == 0 else p.view(T, p.shape[1] // w, w)
+            for p, w in zip(parts, (D, D, D, d, d, d))]
+
+
+def _expected(w, rows, pos, slots, cos_sin, idx_cos_sin, interleaved):
+    s = w.spec
+    q, k, v, iq, ik, iv = (to_np(x) for x in rows)
+    cs, ics = cos_sin.cpu().numpy(), idx_cos_sin.cpu().numpy()
+    n, m = cs.shape[1] // 2, ics.shape[1] // 2
+
+    def rot(x, tab, half):
+        return oracle.rotate_rows(x, tab[pos, :half], tab[pos, half:], interleaved)
+
+    qr, kr = rot(q, cs, n), rot(k, cs, n)
+    iqr, ikr = rot(iq, ics, m), rot(ik, ics, m)
+    if s.kv_dtype == "nvfp4":
+        kp = oracle.cache_write_nvfp4(to_np(w.k_pages), slots, kr, s.kv_scale, 0)
+        kp = vp = oracle.cache_write_nvfp4(kp, slots, v, s.kv_scale, 1)
+    elif s.kv_dtype == "fp8_e4m3":
+        kp = oracle.cache_write(to_np(w.k_pages), slots, kr, e4m3_scale=s.kv_scale)
+        vp = oracle.cache_write(to_np(w.v_pages), slots, v, e4m3_scale=s.kv_scale)
+    else:
+        kp = oracle.cache_write(to_np(w.k_pages), slots, oracle.bf16_round(kr))
+        vp = oracle.cache_write(to_np(w.v_pages), slots, v)
+    return (oracle.bf16_round(qr), oracle.bf16_round(iqr), kp, vp,
+            oracle.cache_write(to_np(w.idx_k_pages), slots, oracle.bf16_round(ikr)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["medium_decode", "fp8_decode", "nvfp4_decode", "tiny_decode",
+                                  "verify", "prefill", "nvfp4_prefill"])
+@pytest.mark.parametrize("rot,interleaved", [(32, False), (64, True), (96, False), (128, False)])
+def test_rotated_rows_and_pools_match_oracle(name, rot, interleaved):
+    spec = wl.small(name, batch=3) if name.endswith("_decode") and name != "tiny_decode" \
+        else wl.small(name)
+    w = wl.make_workload(spec, device="cuda")
+    cfg = msa.config_for(spec)
+    sa = msa.SparseAttention(cfg)
+    T = w.num_tokens
+    rows = _fused(spec, T, 11 + rot)
+    pos = np.array([p for _, p in oracle.query_positions(to_np(w.seq_lens), to_np(w.q_lens))])
+    slots = oracle.cache_slots(to_np(w.seq_lens), to_np(w.q_lens), to_np(w.block_table), 128)
+    tab = _table(int(w.seq_lens.max()), rot)
+    own = _table(int(w.seq_lens.max()), 32) if rot > spec.index_dim or rot == 96 else None
+    want = _expected(w, rows, pos, slots, tab, tab if own is None else own, interleaved)
+    q_out = torch.empty_like(sa.out)
+    iq_out = torch.empty((T, spec.num_kv_heads, spec.index_dim), dtype=torch.bfloat16,
+                         device="cuda")
+    iv_pages = torch.zeros_like(w.idx_k_pages)
+    msa.plan(cfg, w.seq_lens, w.block_table, sa.ws, w.cu_seqlens_q if sa.prefill else None)
+    msa.rope_cache_write(cfg, sa.ws, *rows[:5], tab, q_out, iq_out, w.k_pages, w.v_pages,
+                         w.idx_k_pages, interleaved=interleaved, idx_cos_sin=own, idx_v=rows[5],
+                         idx_v_pages=iv_pages)
+    torch.cuda.synchronize()
+    assert msa.check_device_error(sa.ws) == 0
+    for what, got, exp in zip(("q", "idx_q", "k_pages", "v_pages", "idx_k_pages"),
+                              (q_out, iq_out, w.k_pages, w.v_pages, w.idx_k_pages), want):
+        assert np.array_equal(to_np(got), exp), what
+    exp = oracle.cache_write(np.zeros(iv_pages.shape), slots, to_np(rows[5]))
+    assert np.array_equal(to_np(iv_pages), exp)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["tiny_decode", "nvfp4_decode"])
+def test_positions_slots_in_place_and_no_index_rows(name):
+    """Explicit positions and slots; queries rotated in place; no index rows;
+    rows past the step's tokens stay as they are."""
+    spec = wl.small(name) if name == "tiny_decode" else wl.small(name, batch=3)
+    w = wl.make_workload(spec, device="cuda")
+    B = spec.batch
+    cfg = msa.config_for(spec, max_batch=B + 2)
+    sa = msa.SparseAttention(cfg)
+    T = w.num_tokens
+    q, k, v, *_ = (x.contiguous() for x in _fused(spec, T + 2, 5))
+    pos = torch.tensor([7, 0, 4095][:T] + [0, 0], device="cuda")
+    slots = torch.randperm(spec.num_pages * 128, device="cuda")[:T + 2]
+    tab = _table(4096, 64)
+    rows = [x[:T] for x in (q, k, v)] + [x[:T] for x in _fused(spec, T, 6)[3:]]
+    want = _expected(w, rows, pos[:T].cpu().numpy(), slots[:T].tolist(), tab, tab, False)
+    tail, idx_before = q[T:].clone(), w.idx_k_pages.clone()
+    msa.plan(cfg, w.seq_lens, w.block_table, sa.ws)
+    msa.rope_cache_write(cfg, sa.ws, q, k, v, None, None, tab, q, None, w.k_pages, w.v_pages,
+                         None, positions=pos, out_cache_loc=slots)
+    assert msa.check_device_error(sa.ws) == 0
+    assert np.array_equal(to_np(q[:T]), want[0]) and torch.equal(q[T:], tail)
+    assert np.array_equal(to_np(w.k_pages), want[2])
+    assert np.array_equal(to_np(w.v_pages), want[3])
+    assert torch.equal(w.idx_k_pages, idx_before)
+
+
+@pytest.mark.gpu
+def test_bad_positions_and_slots_are_flagged_and_skipped():
+    spec = wl.small("fp8_decode", batch=3)
+    w = wl.make_workload(spec, device="cuda")
+    cfg = msa.config_for(spec)
+    sa = msa.SparseAttention(cfg)
+    rows = _fused(spec, 3, 8)
+    tab = _table(64, 64)
+    q_out = torch.zeros_like(sa.out)
+    iq_out = torch.zeros((3, spec.num_kv_heads, spec.index_dim), dtype=torch.bfloat16,
+                         device="cuda")
+    for pos, loc, bits, kept, rotated in (
+            ([5, 64, -1], [130, 400, 401], 32, [130, -1, -1], [0]),
+            ([5, 6, 7], [130, spec.num_pages * 128, -3], 1, [130, -1, -1], [0, 1, 2])):
+        q_out.zero_()
+        want = _expected(w, rows, np.clip(pos, 0, 63), kept, tab, tab, False)
+        msa.plan(cfg, w.seq_lens, w.block_table, sa.ws)
+        msa.rope_cache_write(cfg, sa.ws, *rows[:5], tab, q_out, iq_out, w.k_pages, w.v_pages,
+                             w.idx_k_pages, positions=torch.tensor(pos, device="cuda"),
+                             out_cache_loc=torch.tensor(loc, device="cuda"))
+        assert msa.check_device_error(sa.ws) == bits
+        got = to_np(q_out)
+        for t in range(3):
+            assert np.array_equal(got[t], want[0][t] if t in rotated else 0 * got[t])
+        for a, b in zip((w.k_pages, w.v_pages, w.idx_k_pages), want[2:]):
+            assert np.array_equal(to_np(a), b)
+
+
+@pytest.mark.gpu
+def test_idle_requests_are_skipped():
+    spec = wl.small("medium_decode", seq_lens=(900, 0, 300), seq_len_range=None, batch=3,
+                    num_pages=40)
+    w = wl.make_workload(spec, device="cuda")
+    cfg = msa.config_for(spec)
+    sa = msa.SparseAttention(cfg)
+    rows = _fused(spec, 3, 9)
+    tab = _table(900, 128)
+    slots = oracle.cache_slots(to_np(w.seq_lens), to_np(w.q_lens), to_np(w.block_table), 128)
+    want = _expected(w, rows, np.array([899, 0, 299]), slots, tab, tab, False)
+    q_out = torch.full_like(sa.out, 3.0)
+    iq_out = torch.full((3, spec.num_kv_heads, spec.index_dim), 3.0, dtype=torch.bfloat16,
+                        device="cuda")
+    msa.plan(cfg, w.seq_lens, w.block_table, sa.ws)
+    msa.rope_cache_write(cfg, sa.ws, *rows[:5], tab, q_out, iq_out, w.k_pages, w.v_pages,
+                         w.idx_k_pages)
+    assert msa.check_device_error(sa.ws) == 0
+    assert np.array_equal(to_np(q_out)[[0, 2]], want[0][[0, 2]])
+    assert bool((q_out[1] == 3.0).all()) and bool((iq_out[1] == 3.0).all())
+    for a, b in zip((w.k_pages, w.v_pages, w.idx_k_pages), want[2:]):
+        assert np.array_equal(to_np(a), b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["medium_decode", "nvfp4_decode", "verify", "prefill"])
+def test_sparse_step_with_a_rope_equals_rotation_then_write(name):
+    """SparseAttention(rope=...): the step equals, bit for bit, the one fed with
+    rows rotated beforehand (by the oracle) through cache_write."""
+    spec = wl.small(name, batch=3) if name.endswith("_decode") else wl.small(name)
+    w1, w2 = (wl.make_workload(spec, device="cuda") for _ in range(2))
+    cfg = msa.config_for(spec)
+    T = w1.num_tokens
+    q, k, v, iq, ik, _ = _fused(spec, T, 21)
+    tab = _table(int(w1.seq_lens.max()), 64)
+    pos = [p for _, p in oracle.query_positions(to_np(w1.seq_lens), to_np(w1.q_lens))]
+
+    def turned(x):
+        c = tab[pos].cpu().numpy()
+        y = oracle.bf16_round(oracle.rotate_rows(to_np(x), c[:, :32], c[:, 32:], False))
+        return torch.from_numpy(y).to(torch.bfloat16).cuda()
+
+    cu = w1.cu_seqlens_q if cfg.mode == ops.MSA_MODE_PREFILL else None
+    a = msa.SparseAttention(cfg, rope=msa.Rope(tab))
+    a.run(w1.seq_lens, w1.block_table, iq, w1.idx_k_pages, q, w1.k_pages, w1.v_pages,
+          cu_seqlens_q=cu, new_kv=(k, v, ik))
+    b = msa.SparseAttention(cfg)
+    if spec.kv_dtype == "nvfp4":
+        # its codes come from the unrounded rotated key: take the pools from the first run
+        kp, ikp, kv_new = w1.k_pages, w1.idx_k_pages, None
+    else:
+        kp, ikp, kv_new = w2.k_pages, w2.idx_k_pages, (turned(k), v.contiguous(), turned(ik))
+    b.run(w2.seq_lens, w2.block_table, turned(iq), ikp, turned(q), kp,
+          w1.v_pages if kv_new is None else w2.v_pages, cu_seqlens_q=cu, new_kv=kv_new)
+    torch.cuda.synchronize()
+    assert msa.check_device_error(a.ws) == 0
+    assert torch.equal(a.selected[:T], b.selected[:T])
+    assert torch.equal(a.out[:T], b.out[:T]) and torch.equal(a.lse[:T], b.lse[:T])
+    with pytest.raises(ValueError, match="new_kv"):
+        a.run(w1.seq_lens, w1.block_table, iq, w1.idx_k_pages, q, w1.k_pages, w1.v_pages)
