@@ -29,13 +29,11 @@
 // head share each read of a key.
 #include <atomic>
 
-#include "msa_device.cuh"
+#include "tcgen05.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kTileWarps = 4;                  // warps that share a page, 32 keys each
-constexpr int kTileTokens = kBlock / kTileWarps;
 constexpr int kMaxRows = 64;                   // query rows (tokens x group) of a KV head
 constexpr int kTeamsMax = 640;                  // partial slots: two per team
 constexpr int kPageBytes = kBlock * kFp4Row;   // one K or V slot, 9216 bytes
@@ -126,273 +124,248 @@ struct Walk {
   }
 };
 
-// Key n of k-step group nt (n-tile nt, column col) of a warp's 32 keys.  Keys
-// 4 apart sit 72 words = 8 banks apart, so the eight rows a warp reads together
-// (K: columns 0..7; V: columns of one parity) fall on distinct banks.
-__device__ __forceinline__ int key_of(int nt, int col) { return 4 * (col ^ (col >> 2)) + nt; }
+// ---------------------------------------------------------------- TMEM moves
+// 16 lanes x 256 bits a repetition: thread (g, c) = (lane / 4, lane % 4) holds,
+// per 8 columns, columns 2c, 2c + 1 of lane g (registers 0, 1) and of lane
+// g + 8 (registers 2, 3).
+template <int NG>
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[4 * NG]) {
+  static_assert(NG == 1 || NG == 2 || NG == 4 || NG == 8, "repetitions");
+  if constexpr (NG == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+  } else if constexpr (NG == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+    if constexpr (NG == 8)
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+          "%13,%14,%15}, [%16];"
+          : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+            "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+            "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          : "r"(taddr + 32)
+          : "memory");
+  }
+}
+__device__ __forceinline__ void tmem_st_16x256_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Lane i of the warp's quarter, 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values, transposed on the way: thread (g, c)
+// holds row g, columns 2c and 2c + 1 of each; lane 8 i + k gives the address
+// where column k of matrix i goes (8 values, 16 bytes).
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                          uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void named_bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+// Barrier over `count` threads that also tells whether any of them said so.
+__device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
+  int any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n"
+      " selp.b32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"((int)mine)
+      : "memory");
+  return any != 0;
+}
 
-// Two keys' code words (8 elements each) -> f16x2 pairs (key a, key b) of
-// elements 0..7, times the pair of block scales.
-__device__ __forceinline__ void pair_values(uint32_t wa, uint32_t wb, uint32_t sc,
-                                            uint32_t (&h)[8]) {
+// ---------------------------------------------------------------- dequantisation
+// K: this thread's key row (72 bytes) -> its TMEM lane, 64 columns of two dims.
+__device__ __forceinline__ void key_row(const uint8_t* row, uint32_t taddr) {
+  const uint2 sb = *reinterpret_cast<const uint2*>(row + kHeadDim / 2);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {       // 64 dims, 4 blocks
+    const uint32_t s4 = half ? sb.y : sb.x;
+    const uint32_t sp[2] = {e4m3x2_to_f16x2((uint16_t)(s4 & 0xffffu)),
+                            e4m3x2_to_f16x2((uint16_t)(s4 >> 16))};
+    uint32_t h[32];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * half + 8 * b);
+      const uint32_t sc = __byte_perm(sp[b >> 1], 0u, b & 1 ? 0x3232u : 0x1010u);
+      uint32_t lo[4], hi[4];
+      e2m1x8_to_f16x2(x.x, lo);
+      e2m1x8_to_f16x2(x.y, hi);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[8 * b + e] = hmul2_u32(lo[e], sc);
+        h[8 * b + 4 + e] = hmul2_u32(hi[e], sc);
+      }
+    }
+    tmem_st32(taddr + 32 * half, h);
+  }
+}
+
+// V, transposed: this warp's dims 32 w .. 32 w + 31 of the tile's 128 keys ->
+// TMEM lanes 32 w + 8 i + g = dim 32 w + 4 g + i, 64 columns of two keys.
+// EDGE: keys from ntok on do not exist (their rows may hold anything), and a
+// NaN scale of a key that not every row sees becomes 0 here (nan_keys).
+template <bool EDGE>
+__device__ __forceinline__ void value_dims(const uint8_t* vt, uint32_t taddr, int w, int lane,
+                                           int ntok, int all) {
   constexpr uint32_t m = 0x0f0f0f0fu;
-  const uint32_t even = (wa & m) | ((wb << 4) & ~m);
-  const uint32_t odd = ((wa >> 4) & m) | (wb & ~m);
-  uint32_t e[4], o[4];
-  e2m1x8_to_f16x2(even, e);
-  e2m1x8_to_f16x2(odd, o);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[2 * i] = hmul2_u32(e[i], sc);
-    h[2 * i + 1] = hmul2_u32(o[i], sc);
-  }
-}
-
-// Running state of MT 16-row tiles over this warp's keys.
-template <int MT>
-struct State {
-  float acc[MT][16][4];        // tile e: dims 32 c + e (0, 2) and 32 c + 16 + e (1, 3)
-  float m[MT][2];              // reference exponents of rows g and g + 8
-  uint64_t l[MT][2];           // this thread's part of the sums, as f32 pairs
-};
-
-// S = Q K^T of the warp's 32 keys (kt: their rows): lane (g, c) holds blocks c
-// and 4 + c of key column g, k-step 2 w + s takes elements 4 s .. 4 s + 3 of
-// its code word w.
-template <int MT>
-__device__ __forceinline__ void scores(float (&sc)[MT][4][4], const uint4* qf, const uint8_t* kt,
-                                       int lane) {
   const int g = lane >> 2, c = lane & 3;
-  const uint8_t* kr = kt + key_of(0, g) * kFp4Row;
-  uint32_t s2[4];
+  const uint8_t* codes = vt + 4 * c * kFp4Row + 16 * w + 2 * g;
+  const uint8_t* scales = vt + 4 * c * kFp4Row + kHeadDim / 2 + 2 * w + (g >> 2);
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    const uint2 sb = *reinterpret_cast<const uint2*>(kr + nt * kFp4Row + kHeadDim / 2);
-    s2[nt] = e4m3x2_to_f16x2((uint16_t)__byte_perm(sb.x, sb.y, (uint32_t)(c | (4 + c) << 4)));
+  for (int half = 0; half < 2; ++half) {       // 64 keys
+    uint32_t lo[16], hi[16];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
-  }
+    for (int qq = 0; qq < 4; ++qq) {
+      const int k0 = (64 * half + 16 * qq) * kFp4Row;   // keys 64 half + 16 qq + 4 c + 0..3
+      uint32_t u[4], s[4];
 #pragma unroll
-  for (int wb = 0; wb < 2; ++wb) {
-    uint2 x[4];
-    uint32_t sp[4];
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      x[nt] = *reinterpret_cast<const uint2*>(kr + nt * kFp4Row + 32 * wb + 8 * c);
-      sp[nt] = __byte_perm(s2[nt], 0u, wb ? 0x3232u : 0x1010u);
-    }
-#pragma unroll
-    for (int wi = 0; wi < 2; ++wi) {
-      uint32_t q[MT][2][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint4 v = qf[(i * 8 + 4 * wb + 2 * wi + s) * 32 + lane];
-          q[i][s][0] = v.x; q[i][s][1] = v.y; q[i][s][2] = v.z; q[i][s][3] = v.w;
-        }
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        uint32_t h[4];
-        e2m1x8_to_f16x2(wi ? x[nt].y : x[nt].x, h);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t b0 = hmul2_u32(h[2 * s], sp[nt]), b1 = hmul2_u32(h[2 * s + 1], sp[nt]);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) mma_f16(sc[i][nt], q[i][s], b0, b1);
+      for (int i = 0; i < 4; ++i) {
+        u[i] = *reinterpret_cast<const uint16_t*>(codes + k0 + i * kFp4Row);
+        s[i] = scales[k0 + i * kFp4Row];
+        if (EDGE) {
+          const int key = 64 * half + 16 * qq + 4 * c + i;
+          if (key >= ntok || (key >= all && (s[i] & 0x7f) == 0x7f)) s[i] = 0;
         }
       }
+      const uint32_t a = __byte_perm(u[0], u[2], 0x5410), b = __byte_perm(u[1], u[3], 0x5410);
+      const uint32_t even = (a & m) | ((b << 4) & ~m), odd = ((a >> 4) & m) | (b & ~m);
+      const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(s[0] | s[1] << 8));
+      const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(s[2] | s[3] << 8));
+      uint32_t e[4], o[4];                     // dims 0, 2 | 1, 3 of keys 0 1, then of 2 3
+      e2m1x8_to_f16x2(even, e);
+      e2m1x8_to_f16x2(odd, o);
+      lo[4 * qq] = hmul2_u32(e[0], s01);
+      lo[4 * qq + 1] = hmul2_u32(e[2], s23);
+      lo[4 * qq + 2] = hmul2_u32(o[0], s01);
+      lo[4 * qq + 3] = hmul2_u32(o[2], s23);
+      hi[4 * qq] = hmul2_u32(e[1], s01);
+      hi[4 * qq + 1] = hmul2_u32(e[3], s23);
+      hi[4 * qq + 2] = hmul2_u32(o[1], s01);
+      hi[4 * qq + 3] = hmul2_u32(o[3], s23);
     }
+    tmem_st_16x256_x4(taddr + 32 * half, lo);
+    tmem_st_16x256_x4(taddr + 32 * half + (16u << 16), hi);
   }
 }
 
-// Scores -> probabilities 2^(s' - m + kBias) as A fragments, with the sums.
-// The reference m of a row moves (and the row's output is rescaled) only when
-// it is still unset or a score passes it by more than kSlack: any m within
-// fp16's range of the maximum gives the same quotient.
-template <int MT, bool EDGE>
-__device__ __forceinline__ void softmax_step(State<MT>& st, float (&sc)[MT][4][4],
-                                             uint32_t (&pa)[MT][2][4], float scale_log2, int lane,
-                                             const int (&lim)[MT][2]) {
-  const int c = lane & 3;
-  bool move = false;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    float mx[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (EDGE && key_of(nt, 2 * c + e) >= lim[i][k]) sc[i][nt][2 * k + e] = -INFINITY;
-      mx[k] = fmax3(fmax3(sc[i][0][2 * k], sc[i][0][2 * k + 1], sc[i][1][2 * k]),
-                    fmax3(sc[i][1][2 * k + 1], sc[i][2][2 * k], sc[i][2][2 * k + 1]),
-                    fmaxf(sc[i][3][2 * k], sc[i][3][2 * k + 1]));
-      move |= mx[k] * scale_log2 > st.m[i][k] + kSlack;
-    }
-  }
-  if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x = sc[i][0][2 * k];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) x = fmax3(x, sc[i][nt][2 * k], sc[i][nt][2 * k + 1]);
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mn = fmaxf(st.m[i][k], x * scale_log2);
-        const float alpha = mn == -INFINITY ? 1.f : ex2_approx(st.m[i][k] - mn);
-        st.m[i][k] = mn;
-        st.l[i][k] = mul_f2(st.l[i][k], f2(alpha, alpha));
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          st.acc[i][e][2 * k] *= alpha;
-          st.acc[i][e][2 * k + 1] *= alpha;
-        }
-      }
-  }
-  const uint64_t sl = f2(scale_log2, scale_log2);
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float off = kBias - (st.m[i][k] == -INFINITY ? 0.f : st.m[i][k]);
-      const uint64_t o2 = f2(off, off);
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        float x0, x1;
-        f2_split(fma_f2(f2(sc[i][nt][2 * k], sc[i][nt][2 * k + 1]), sl, o2), x0, x1);
-        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        st.l[i][k] = add_f2(st.l[i][k], f2(p0, p1));
-        pa[i][nt >> 1][(nt & 1) * 2 + k] = pack_f16(p0, p1);
-      }
-    }
-}
-
-// O += P V of the warp's 32 keys (vt: their rows): lane (g, c) holds block g of
-// key columns 2c and 2c + 1.  EDGE: ntok keys exist, and every row sees `all`
-// of them.
-template <int MT, bool EDGE>
-__device__ __forceinline__ void values(State<MT>& st, const uint32_t (&pa)[MT][2][4],
-                                       const uint8_t* vt, int lane, const int (&lim)[MT][2],
-                                       int ntok, int all) {
-  const int g = lane >> 2, c = lane & 3;
-  const int ka = key_of(0, 2 * c), kb = key_of(0, 2 * c + 1);
-  const uint8_t *va = vt + ka * kFp4Row, *vb = vt + kb * kFp4Row;
-#pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
-    uint2 xa[2], xb[2];
-    uint32_t s2[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int nt = 2 * kk + j;
-      xa[j] = *reinterpret_cast<const uint2*>(va + nt * kFp4Row + 8 * g);
-      xb[j] = *reinterpret_cast<const uint2*>(vb + nt * kFp4Row + 8 * g);
-      uint32_t sa = va[nt * kFp4Row + kHeadDim / 2 + g], sb = vb[nt * kFp4Row + kHeadDim / 2 + g];
-      if (EDGE) {
-        // rows past the end may hold anything, and a row that some query may
-        // not see may hold a NaN scale: 0 * NaN is not 0 (added back below)
-        if (ka + nt >= ntok || (ka + nt >= all && (sa & 0x7f) == 0x7f)) sa = 0;
-        if (kb + nt >= ntok || (kb + nt >= all && (sb & 0x7f) == 0x7f)) sb = 0;
-      }
-      s2[j] = e4m3x2_to_f16x2((uint16_t)(sa | sb << 8));
-    }
-#pragma unroll
-    for (int wi = 0; wi < 2; ++wi) {
-      uint32_t b[2][8];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        pair_values(wi ? xa[j].y : xa[j].x, wi ? xb[j].y : xb[j].x, s2[j], b[j]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) mma_f16(st.acc[i][8 * wi + e], pa[i][kk], b[0][e], b[1][e]);
-    }
-  }
-  if (EDGE) {
-    // NaN scales among the keys that only later tokens see
-    for (int u = max(all, 0); u < min(ntok, kTileTokens); ++u) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if ((vt[u * kFp4Row + kHeadDim / 2 + 2 * c + half] & 0x7f) != 0x7f) continue;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (u < lim[i][k])
-#pragma unroll
-              for (int e = 0; e < 16; ++e) st.acc[i][e][2 * k + half] = NAN;
-      }
-    }
-  }
-}
-
-// A CTA is TEAMS independent teams, each with its own range of units, ring and
-// loader warp: RG groups of four consumer warps with MT row tiles of 16 each.
-// Registers move from the loaders' warpgroup to the consumers (setmaxnreg; the
-// shares add up to what the launch gets).
-template <int MT, int RG>
+// A CTA is kTeams independent teams of four warps, each with its own range of
+// units, ring, TMEM columns and loader warp.  NG: groups of 8 query rows.
+template <int NG>
 struct Shape {
-  static constexpr int kRows = 16 * MT * RG;
-  static constexpr int kTeams = kRows == 16 ? 3 : (kRows == 32 ? 2 : 1);
-  static constexpr int kTeamWarps = kTileWarps * RG;
-  static constexpr int kConsumerThreads = kTeamWarps * 32;        // of a team
-  static constexpr int kThreads = kTeams * kConsumerThreads + 128;
-  // 512 threads x 128 = 384 x 160 + 128 x 32; 384 x 168 = 256 x 224 + 128 x 56
-  static constexpr int kConsumerRegs = kRows == 16 ? 160 : 224;
-  static constexpr int kLoaderRegs = kRows == 16 ? 32 : 56;
-  static constexpr int kQBytes = MT * RG * 4096;
-  static constexpr int kOBytes = kTileWarps * kRows * 64 * 4;
-  static constexpr int kStages = kRows == 16 ? 5 : (kRows == 32 ? 6 : 12);
-  static constexpr int kTeamSmem = kStages * kPageBytes + kQBytes + kOBytes;
+  static constexpr int kN = NG < 2 ? 16 : 8 * NG;                 // MMA N
+  static constexpr int kTeams = NG <= 2 ? 3 : 2;
+  static constexpr int kThreads = kTeams * 128 + 128;
+  static constexpr int kCols = 128 + 2 * kN;                      // K | V | S | O
+  static constexpr int kStages = NG <= 2 ? 7 : (NG == 4 ? 9 : 8);
+  static constexpr int kOperand = kN * kHeadDim * 2;              // Q, and P
+  static constexpr int kTeamSmem = 2 * kOperand + kStages * kPageBytes;
   static constexpr int kSmem = kTeams * kTeamSmem;
 };
 
-template <int MT, int RG>
+template <int NG>
 struct TeamShared {
-  using S = Shape<MT, RG>;
-  float red_m[kTileWarps][S::kRows], red_l[kTileWarps][S::kRows];
-  uint64_t full_bar[S::kStages], empty_bar[S::kStages];
-  int usable[S::kStages];                      // K slots: 0 = the plan flagged the page
+  using S = Shape<NG>;
+  float red[4][S::kN];         // per warp: row maxima, row sums
+  float alpha[S::kN];
+  uint64_t full_bar[S::kStages], empty_bar[S::kStages], s_bar, o_bar;
+  int usable[S::kStages];      // K slots: 0 = the plan flagged the page
+  int tok[S::kN];              // token of each row within the request
+  unsigned nan[S::kN];         // value blocks that are NaN for the row (nan_keys)
 };
 
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(p));
+  return p != 0;
 }
 
-template <int MT, int RG>
-__global__ void __launch_bounds__(Shape<MT, RG>::kThreads, 1)
+template <int NG>
+__global__ void __launch_bounds__(Shape<NG>::kThreads, 1)
 dense_decode_kernel(WsView ws, DenseArgs a) {
-  using S = Shape<MT, RG>;
-  constexpr int kRows = S::kRows, kStages = S::kStages;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) TeamShared<MT, RG> shared[S::kTeams];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kConsumerWarps = S::kTeams * S::kTeamWarps;
-  const bool loader = warp >= kConsumerWarps;
-  const int team = loader ? warp - kConsumerWarps : warp / S::kTeamWarps;
+  using S = Shape<NG>;
+  constexpr int kN = S::kN, kStages = S::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(16) TeamShared<NG> shared[S::kTeams];
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const bool loader = warp >= 4 * S::kTeams;
+  const int team = loader ? min(warp - 4 * S::kTeams, S::kTeams - 1) : warp / 4;
+  const bool keeper = warp == 4 * S::kTeams + 3;                  // of the TMEM allocation
   if (tid < S::kTeams) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&shared[tid].full_bar[i], 1);
-      mbar_init(&shared[tid].empty_bar[i], S::kTeamWarps);
+      mbar_init(&shared[tid].empty_bar[i], 4);
     }
+    mbar_init(&shared[tid].s_bar, 1);
+    mbar_init(&shared[tid].o_bar, 1);
     fence_barrier_init();
   }
-  __syncthreads();
-  griddep_launch_dependents();
   griddep_wait();
+  if (keeper) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();                 // only now: a dependent may want TMEM too
+  constexpr int kDone = 15;                    // named barrier: every consumer, and the keeper
+  constexpr int kDoneCount = S::kTeams * 128 + 32;
+  if (keeper) {
+    named_bar_sync(kDone, kDoneCount);
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+    return;
+  }
+  TeamShared<NG>& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
   const int teams = S::kTeams * (int)gridDim.x;
-  uint8_t* ring = smem + (loader && team >= S::kTeams ? 0 : team) * S::kTeamSmem;
-  uint4* qfrag = reinterpret_cast<uint4*>(ring + kStages * kPageBytes);
-  float* obuf = reinterpret_cast<float*>(ring + kStages * kPageBytes + S::kQBytes);
+  uint8_t* qs_ = smem + team * S::kTeamSmem;   // Q and P: K-major, 128-byte swizzle
+  uint8_t* ps_ = qs_ + S::kOperand;
+  uint8_t* ring = ps_ + S::kOperand;
   Walk wk;
   int stage = 0;
   uint32_t phase = 0;
@@ -404,12 +377,11 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     // ---------------------------------------------------------------- loader
     // The pages of a segment 32 at a time (a lane each), one bulk copy per
     // K and V slot; of the last page only the rows that exist.
-    regs_down<S::kLoaderRegs>();
-    if (team >= S::kTeams || !wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane)) return;
-    TeamShared<MT, RG>& sh = shared[team];
+    if (warp - 4 * S::kTeams >= S::kTeams) return;
+    if (!wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane)) return;
     int arms = 0;
     while (wk.next(ws, a.Hkv)) {
-      if (wk.nq > a.q_len) continue;
+      if (wk.nq > a.q_len || wk.nq == 0) continue;
       const int32_t* bt = ws.block_table + (int64_t)wk.r * a.max_blocks;
       int ahead = wk.j0 + lane < wk.j1 ? bt[wk.j0 + lane] : -1;
       for (int jb = wk.j0; jb < wk.j1; jb += 32) {
@@ -421,22 +393,19 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
             const int rows = min(kBlock, wk.L - j * kBlock);
             const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;   // a multiple of 16
             const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2;
-            mbar_wait(&sh.empty_bar[stage], phase ^ 1u, ws.hdr);
-            sh.usable[stage] = page >= 0;
-            if (page < 0) {
-              mbar_arrive(&sh.full_bar[stage]);
-              ++arms;
-              advance();
-            } else {
-              mbar_arrive_expect_tx(&sh.full_bar[stage], bytes);
-              bulk_load(ring + stage * kPageBytes, a.k_pool + slot * kPageBytes, bytes,
-                        &sh.full_bar[stage]);
-              advance();
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {
               mbar_wait(&sh.empty_bar[stage], phase ^ 1u, ws.hdr);
-              mbar_arrive_expect_tx(&sh.full_bar[stage], bytes);
-              bulk_load(ring + stage * kPageBytes, a.v_pool + (slot + 1) * kPageBytes, bytes,
-                        &sh.full_bar[stage]);
-              arms += 2;
+              sh.usable[stage] = page >= 0;
+              if (page >= 0) {
+                mbar_arrive_expect_tx(&sh.full_bar[stage], bytes);
+                bulk_load(ring + stage * kPageBytes,
+                          (kind ? a.v_pool : a.k_pool) + (slot + kind) * kPageBytes, bytes,
+                          &sh.full_bar[stage]);
+              } else {
+                mbar_arrive(&sh.full_bar[stage]);
+              }
+              ++arms;
               advance();
             }
           }
@@ -452,185 +421,271 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   }
 
   // -------------------------------------------------------------- consumers
-  regs_up<S::kConsumerRegs>();
-  if (!wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane)) return;
-  TeamShared<MT, RG>& sh = shared[team];
-  const int tw = warp - team * S::kTeamWarps, ttid = tw * 32 + lane;   // within the team
-  const int rg = tw / kTileWarps, kw = tw % kTileWarps;
+  // Control flow depends on the plan's data alone (never on what a wait saw),
+  // so that the team's named barriers match even after a wait gave up.
+  const int w = warp & 3, ttid = tid & 127;    // within the team; ttid = key of a tile
   const int g = lane >> 2, c = lane & 3;
-  const uint4* qf = qfrag + rg * MT * 8 * 32;
-  auto sync = [&]() { named_bar_sync(1 + team, S::kConsumerThreads); };
+  const int bar_k = 1 + 4 * team, bar_o = 2 + 4 * team, bar_all = 3 + 4 * team;
+  const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols, lanes = (uint32_t)(32 * w) << 16;
+  const uint32_t tk = tm, tv = tm + 64, ts = tm + 128, to = tm + 128 + kN;
+  constexpr uint32_t idesc = idesc_f16(0, 128, kN);
+  // this lane's address for the transposed store of P: matrix i = keys 32 w + 8 i ..,
+  // column k = row 8 grp + k
+  const int pchunk = 4 * w + (lane >> 3);
+  const uint32_t paddr = smem_u32(ps_) + (pchunk >> 3) * kN * 128 + (lane & 7) * 128 +
+                         (((pchunk & 7) ^ (lane & 7)) << 4);
+  if (8 * NG < kN)                             // P rows that no group fills
+    for (int x = ttid; x < S::kOperand / 16; x += 128)
+      reinterpret_cast<uint4*>(ps_)[x] = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t s_phase = 0, o_phase = 0;
   auto release = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty_bar[stage]);
     advance();
   };
-  while (wk.next(ws, a.Hkv)) {
-    if (wk.nq > a.q_len) {                     // more tokens than the config's
-      if (ttid == 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
+  const bool any = wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane);
+  while (any && wk.next(ws, a.Hkv)) {
+    if (wk.nq > a.q_len || wk.nq == 0) {       // more tokens than the config's, or none
+      if (ttid == 0 && wk.nq > 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
       continue;
     }
     const int rows = wk.nq * a.G;
-    // ---- the rows' A fragments: k-step 2 w + s of lane (g, c) takes dims
-    // 16 c + 64 (w / 2) + 8 (w % 2) + 4 s + 0..3
+    // ---- Q: bf16 -> fp16 rows of the B operand, zero past the last row
     bool ovf = false;
-    for (int x = tw; x < MT * RG * 8; x += S::kTeamWarps) {
-      const int ks = x & 7, w = ks >> 1;
-      const int dim = 16 * c + 64 * (w >> 1) + 8 * (w & 1) + 4 * (ks & 1);
-      uint32_t f[4];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int row = (x >> 3) * 16 + g + 8 * k;
-        uint2 v = make_uint2(0u, 0u);
-        if (row < rows)
-          v = *reinterpret_cast<const uint2*>(
-              a.q +
-              ((int64_t)(wk.qs + row / a.G) * a.Hq + wk.h * a.G + row % a.G) * kHeadDim + dim);
-        f[k] = bf16x2_to_f16x2(v.x);
-        f[k + 2] = bf16x2_to_f16x2(v.y);
-        ovf |= f16x2_has_inf(f[k]) | f16x2_has_inf(f[k + 2]);
-      }
-      qfrag[x * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+    for (int x = ttid; x < kN * 16; x += 128) {
+      const int n = x >> 4, ch = x & 15;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (n < rows)
+        v = *reinterpret_cast<const uint4*>(
+            a.q + ((int64_t)(wk.qs + n / a.G) * a.Hq + wk.h * a.G + n % a.G) * kHeadDim + 8 * ch);
+      v.x = bf16x2_to_f16x2(v.x);
+      v.y = bf16x2_to_f16x2(v.y);
+      v.z = bf16x2_to_f16x2(v.z);
+      v.w = bf16x2_to_f16x2(v.w);
+      ovf |= f16x2_has_inf(v.x) | f16x2_has_inf(v.y) | f16x2_has_inf(v.z) | f16x2_has_inf(v.w);
+      *reinterpret_cast<uint4*>(qs_ + kmaj_off(n, ch, kN)) = v;
     }
     if (__any_sync(0xffffffffu, ovf) && lane == 0) set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
-    sync();
+    if (ttid < kN) {
+      sh.tok[ttid] = min(ttid / a.G, wk.nq - 1);
+      sh.nan[ttid] = 0u;
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(bar_all, 128);
 
-    State<MT> st;
-    int seen[MT][2];                           // keys of the request each row sees
+    float m[NG][2], l[NG][2];                  // rows 8 i + 2 c + {0, 1}
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        st.acc[i][e][0] = st.acc[i][e][1] = st.acc[i][e][2] = st.acc[i][e][3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        st.m[i][k] = -INFINITY;
-        st.l[i][k] = 0ull;
-        const int row = (rg * MT + i) * 16 + g + 8 * k;
-        seen[i][k] = wk.L - wk.nq + min(row / a.G, max(wk.nq - 1, 0)) + 1;
-      }
+    for (int i = 0; i < NG; ++i) {
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
     }
     for (int j = wk.j0; j < wk.j1; ++j) {
+      // ---- K -> TMEM, S^T = K Q^T (128 keys x rows)
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
-      if (!sh.usable[stage]) {
-        release();
-        continue;
+      const int ntok = sh.usable[stage] ? wk.L - j * kBlock : 0;   // keys that exist
+      const int all = ntok - wk.nq + 1;                            // and that every row sees
+      key_row(ring + stage * kPageBytes + ttid * kFp4Row, tk + lanes);
+      release();
+      tmem_st_wait();
+      tc_fence_before();
+      if (w == 0) {
+        named_bar_sync(bar_k, 128);
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t dq = kstep_desc(smem_u32(qs_), 0, kN);
+          const uint32_t qlo = (uint32_t)dq, qhi = (uint32_t)(dq >> 32);
+          umma_ts<false>(ts, tk, qlo, qhi, idesc);
+#pragma unroll
+          for (int ks = 1; ks < 8; ++ks)
+            umma_ts<true>(ts, tk + 8 * ks, qlo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, qhi, idesc);
+          umma_commit(&sh.s_bar);
+        }
+        __syncwarp();
+      } else {
+        named_bar_arrive(bar_k, 128);
       }
-      const int base = j * kBlock + kw * kTileTokens;   // this warp's first key
-      const int ntok = wk.L - base;                     // its keys that exist
-      const int all = ntok - wk.nq + 1;                 // and that every row sees
-      int lim[MT][2];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) lim[i][k] = seen[i][k] - base;
-      float sc[MT][4][4];
-      uint32_t pa[MT][2][4];
-      const uint8_t* tile = ring + kw * kTileTokens * kFp4Row;
-      if (ntok > 0) scores<MT>(sc, qf, tile + stage * kPageBytes, lane);
-      release();
-      if (all >= kTileTokens)
-        softmax_step<MT, false>(st, sc, pa, a.scale_log2, lane, lim);
-      else if (ntok > 0)
-        softmax_step<MT, true>(st, sc, pa, a.scale_log2, lane, lim);
+      // ---- V -> TMEM, once the last P V has read its predecessor
+      if (j > wk.j0) {
+        mbar_wait(&sh.o_bar, o_phase, ws.hdr);
+        o_phase ^= 1u;
+        tc_fence_after();
+      }
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
-      if (all >= kTileTokens)
-        values<MT, false>(st, pa, tile + stage * kPageBytes, lane, lim, ntok, all);
-      else if (ntok > 0)
-        values<MT, true>(st, pa, tile + stage * kPageBytes, lane, lim, ntok, all);
+      const uint8_t* vt = ring + stage * kPageBytes;
+      if (all >= kBlock) {
+        value_dims<false>(vt, tv + lanes, w, lane, ntok, all);
+      } else {
+        value_dims<true>(vt, tv + lanes, w, lane, ntok, all);
+        if (ttid >= all && ttid < ntok) {      // NaN scales that only later tokens see
+          unsigned bad = 0;
+          for (int b = 0; b < 8; ++b)
+            bad |= (vt[ttid * kFp4Row + kHeadDim / 2 + b] & 0x7f) == 0x7f ? 1u << b : 0u;
+          if (bad)
+            for (int n = 0; n < rows; ++n)
+              if (ttid < all + sh.tok[n]) atomicOr(&sh.nan[n], bad);
+        }
+      }
       release();
+      // ---- softmax of S^T: 8 keys (16 hf + g, + 8) of rows 8 i + 2 c + {0, 1}
+      mbar_wait(&sh.s_bar, s_phase, ws.hdr);
+      s_phase ^= 1u;
+      tc_fence_after();
+      uint32_t x[2][4 * NG];
+      tmem_ld_16x256<NG>(ts + lanes, x[0]);
+      tmem_ld_16x256<NG>(ts + lanes + (16u << 16), x[1]);
+      tmem_ld_wait();
+      if (all < kBlock) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int e = 0; e < 4 * NG; ++e) {
+            const int key = 32 * w + 16 * hf + g + 8 * ((e >> 1) & 1);
+            const int lim = min(ntok, all + sh.tok[8 * (e >> 2) + 2 * c + (e & 1)]);
+            if (key >= lim) x[hf][e] = 0xff800000u;
+          }
+      }
+      auto xf = [&](int hf, int i, int e) { return __uint_as_float(x[hf][4 * i + e]); };
+      bool move = false;
+      float mx[NG][2];
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          mx[i][k] = fmaxf(fmax3(xf(0, i, k), xf(0, i, k + 2), xf(1, i, k)), xf(1, i, k + 2)) *
+                     a.scale_log2;
+          move |= mx[i][k] > m[i][k] + kSlack;
+        }
+      if (named_bar_any(bar_all, 128, move)) {
+        // new references: the row maxima over the team's keys
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1)
+              mx[i][k] = fmaxf(mx[i][k], __shfl_xor_sync(0xffffffffu, mx[i][k], o));
+            if (g == 0) sh.red[w][8 * i + 2 * c + k] = mx[i][k];
+          }
+        named_bar_sync(bar_all, 128);
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int n = 8 * i + 2 * c + k;
+            const float mn = fmaxf(fmax3(m[i][k], sh.red[0][n], sh.red[1][n]),
+                                   fmaxf(sh.red[2][n], sh.red[3][n]));
+            const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m[i][k] - mn);
+            m[i][k] = mn;
+            l[i][k] *= alpha;
+            if (w == 0 && g == 0) sh.alpha[n] = alpha;
+          }
+        named_bar_sync(bar_all, 128);
+        if (j > wk.j0) {
+#pragma unroll
+          for (int n0 = 0; n0 < 8 * NG; n0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + lanes + n0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (n0 + e < 8 * NG)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * sh.alpha[n0 + e]);
+            tmem_st16(to + lanes + n0, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      // ---- P = 2^(s' - m + bias) as the B operand [row][key]
+      const uint64_t sl = f2(a.scale_log2, a.scale_log2);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const uint64_t off = f2(kBias - (m[i][0] == -INFINITY ? 0.f : m[i][0]),
+                                kBias - (m[i][1] == -INFINITY ? 0.f : m[i][1]));
+        uint64_t sum = f2(l[i][0], l[i][1]);
+        uint32_t p[4];
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {          // keys 8 o + g
+          float p0, p1;
+          f2_split(fma_f2(f2u(x[o >> 1][4 * i + 2 * (o & 1)], x[o >> 1][4 * i + 2 * (o & 1) + 1]),
+                          sl, off),
+                   p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          sum = add_f2(sum, f2(p0, p1));
+          p[o] = pack_f16(p0, p1);
+        }
+        f2_split(sum, l[i][0], l[i][1]);
+        stsm_x4_t(paddr + i * 1024, p[0], p[1], p[2], p[3]);
+      }
+      fence_proxy_async_smem();
+      tmem_st_wait();
+      tc_fence_before();
+      // ---- O^T += V^T P (128 dims x rows)
+      if (w == 0) {
+        named_bar_sync(bar_o, 128);
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t dp = kstep_desc(smem_u32(ps_), 0, kN);
+          const uint32_t plo = (uint32_t)dp, phi = (uint32_t)(dp >> 32);
+          if (j == wk.j0) umma_ts<false>(to, tv, plo, phi, idesc);
+          else umma_ts<true>(to, tv, plo, phi, idesc);
+#pragma unroll
+          for (int ks = 1; ks < 8; ++ks)
+            umma_ts<true>(to, tv + 8 * ks, plo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, phi, idesc);
+          umma_commit(&sh.o_bar);
+        }
+        __syncwarp();
+      } else {
+        named_bar_arrive(bar_o, 128);
+      }
     }
 
-    // ---- merge the four warps of each row group
+    // ---- the segment's result: whole rows, or a partial
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x, y;
-        f2_split(st.l[i][k], x, y);
-        x += y;
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (c == 0) {
-          const int row = (rg * MT + i) * 16 + g + 8 * k;
-          sh.red_m[kw][row] = st.m[i][k];
-          sh.red_l[kw][row] = x;
-        }
-      }
-    sync();
-    float f[MT][2];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int row = (rg * MT + i) * 16 + g + 8 * k;
-        float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kTileWarps; ++w) M = fmaxf(M, sh.red_m[w][row]);
-        f[i][k] = M == -INFINITY ? 1.f : ex2_approx(st.m[i][k] - M);
+        for (int o = 4; o <= 16; o <<= 1)
+          l[i][k] += __shfl_xor_sync(0xffffffffu, l[i][k], o);
+        const int n = 8 * i + 2 * c + k;
+        if (g == 0) sh.red[w][n] = l[i][k];
+        if (w == 0 && g == 0) sh.alpha[n] = m[i][k];
       }
+    mbar_wait(&sh.o_bar, o_phase, ws.hdr);
+    o_phase ^= 1u;
+    tc_fence_after();
+    named_bar_sync(bar_all, 128);
+    const int dim = 32 * w + 4 * (lane & 7) + (lane >> 3);        // of this thread's TMEM lane
     const int slot = 2 * vid + (wk.starts ? 1 : 0);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {              // dims 32 c + 16 half + 8 p + 0..7
-      if (p) sync();
+    for (int n0 = 0; n0 < 8 * NG; n0 += 16) {
+      uint32_t o[16];
+      tmem_ld16(to + lanes + n0, o);
+      tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = (rg * MT + i) * 16 + g + 8 * k;
-            float4* dst = reinterpret_cast<float4*>(obuf + (kw * kRows + row) * 64 + 16 * c +
-                                                    8 * half);
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = st.acc[i][8 * p + e][2 * k + half] * f[i][k];
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-          }
-      sync();
-      for (int x = ttid; x < kRows * 8; x += S::kConsumerThreads) {
-        const int row = x >> 3, part = x & 7;
-        if (row >= rows) continue;
-        float M = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kTileWarps; ++w) M = fmaxf(M, sh.red_m[w][row]);
-#pragma unroll
-        for (int w = 0; w < kTileWarps; ++w)
-          sum += sh.red_l[w][row] * (M == -INFINITY ? 1.f : ex2_approx(sh.red_m[w][row] - M));
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kTileWarps; ++w) {
-          const float4* s4 =
-              reinterpret_cast<const float4*>(obuf + (w * kRows + row) * 64 + 8 * part);
-          const float4 x0 = s4[0], x1 = s4[1];
-          v[0] += x0.x; v[1] += x0.y; v[2] += x0.z; v[3] += x0.w;
-          v[4] += x1.x; v[5] += x1.y; v[6] += x1.z; v[7] += x1.w;
-        }
-        const int dim = 16 * part + 8 * p;
+      for (int e = 0; e < 16; ++e) {
+        const int n = n0 + e;
+        if (n >= 8 * NG || n >= rows) continue;
+        const float sum = sh.red[0][n] + sh.red[1][n] + sh.red[2][n] + sh.red[3][n];
+        const float M = sh.alpha[n];
+        float v = __uint_as_float(o[e]);
+        if ((sh.nan[n] >> (dim >> 4)) & 1u) v = NAN;
         if (wk.whole) {
-          const int64_t hq =
-              (int64_t)(wk.qs + row / a.G) * a.Hq + wk.h * a.G + row % a.G;
-          const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
-          uint32_t pk[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pk[e] = pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
-          *reinterpret_cast<uint4*>(a.out + hq * kHeadDim + dim) =
-              make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          if (p == 0 && part == 0)
-            a.lse[hq] = sum == 0.f ? -INFINITY : (M + log2f(sum) - kBias) * kLn2;
+          const int64_t hq = (int64_t)(wk.qs + n / a.G) * a.Hq + wk.h * a.G + n % a.G;
+          a.out[hq * kHeadDim + dim] = __float2bfloat16_rn(sum == 0.f ? 0.f : v * (a.v_scale / sum));
+          if (ttid == 0) a.lse[hq] = sum == 0.f ? -INFINITY : (M + log2f(sum) - kBias) * kLn2;
         } else {
-          float4* dst = reinterpret_cast<float4*>(
-              a.o_part + ((int64_t)slot * a.rows + row) * kHeadDim + dim);
-          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-          if (p == 0 && part == 0)
-            a.ml_part[(int64_t)slot * a.rows + row] = make_float2(M, sum);
+          a.o_part[((int64_t)slot * a.rows + n) * kHeadDim + dim] = v;
+          if (ttid == 0) a.ml_part[(int64_t)slot * a.rows + n] = make_float2(M, sum);
         }
       }
     }
-    sync();
+    tc_fence_before();
+    named_bar_sync(bar_all, 128);              // red, alpha, tok, nan are free again
   }
+  tc_fence_before();
+  named_bar_arrive(kDone, kDoneCount);
 }
 
 // Merges the partials of the (request, head) groups that lie in several teams'
@@ -710,14 +765,14 @@ dense_merge_kernel(WsView ws, DenseArgs a, int teams) {
   if (lane == 0) a.lse[hq] = l == 0.f ? -INFINITY : (M + log2f(l) - kBias) * kLn2;
 }
 
-template <int MT, int RG>
+template <int NG>
 msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cudaStream_t s) {
-  using S = Shape<MT, RG>;
+  using S = Shape<NG>;
   static std::atomic<bool> ready[64];          // shared-memory limit raised, per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MSA_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(dense_decode_kernel<MT, RG>,
+    if (cudaFuncSetAttribute(dense_decode_kernel<NG>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::kSmem) != cudaSuccess)
       return MSA_ERR_CUDA;
@@ -728,7 +783,7 @@ msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cuda
   if (grid > units) grid = units;
   if (grid <= 0) return MSA_ERR_CUDA;
   const int teams = (int)grid * S::kTeams;
-  msa_status st = launch_pdl(dense_decode_kernel<MT, RG>, dim3((unsigned)grid),
+  msa_status st = launch_pdl(dense_decode_kernel<NG>, dim3((unsigned)grid),
                              dim3(S::kThreads), S::kSmem, s, v, a);
   if (st != MSA_OK) return st;
   return launch_pdl(dense_merge_kernel,
@@ -786,7 +841,8 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   const WsView v = view_of(*cfg, ws);
   const int64_t units = (int64_t)cfg->max_batch * cfg->max_blocks_per_req * a.Hkv;
   cudaStream_t s = (cudaStream_t)stream;
-  if (a.rows <= 16) return launch_dense<1, 1>(v, a, units, s);
-  if (a.rows <= 32) return launch_dense<2, 1>(v, a, units, s);
-  return launch_dense<2, 2>(v, a, units, s);
+  if (a.rows <= 8) return launch_dense<1>(v, a, units, s);
+  if (a.rows <= 16) return launch_dense<2>(v, a, units, s);
+  if (a.rows <= 32) return launch_dense<4>(v, a, units, s);
+  return launch_dense<8>(v, a, units, s);
 }
