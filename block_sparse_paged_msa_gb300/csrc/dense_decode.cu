@@ -288,13 +288,48 @@ __device__ __forceinline__ void value_dims(const uint8_t* vt, uint32_t taddr, in
   }
 }
 
-// A CTA is kTeams independent teams of four warps, each with its own range of
-// units, ring, TMEM columns and loader warp.  NG: groups of 8 query rows.
+// The tiles (pages) of a range, one after the other, for a role that walks
+// them by itself.
+struct Tiles {
+  Walk wk;
+  int j, seg;                  // block of the current tile, its segment's number
+  bool first, last;            // of the segment
+
+  __device__ __forceinline__ bool open(const WsView& ws, const DenseArgs& a, int vid, int teams,
+                                       int lane) {
+    j = 0;
+    seg = -1;
+    last = true;
+    return wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane);
+  }
+  // Skips the segments of requests without new tokens, or with more than the
+  // config's (the consumers flag those).
+  __device__ __forceinline__ bool next(const WsView& ws, const DenseArgs& a) {
+    first = last;
+    if (last) {
+      do {
+        if (!wk.next(ws, a.Hkv)) return false;
+      } while (wk.nq > a.q_len || wk.nq == 0);
+      ++seg;
+      j = wk.j0;
+    } else {
+      ++j;
+    }
+    last = j + 1 == wk.j1;
+    return true;
+  }
+};
+
+// A CTA is kTeams independent teams of four consumer warps, each with its own
+// range of units, ring, TMEM columns, loader warp and MMA warp; one more warp
+// keeps the TMEM allocation.  NG: groups of 8 query rows.
 template <int NG>
 struct Shape {
   static constexpr int kN = NG < 2 ? 16 : 8 * NG;                 // MMA N
   static constexpr int kTeams = NG <= 2 ? 3 : 2;
-  static constexpr int kThreads = kTeams * 128 + 128;
+  static constexpr int kThreads = kTeams * 128 + 256;
+  // 640 x 96 = 384 x 128 + 256 x 48; 512 x 128 = 256 x 200 + 256 x 56
+  static constexpr int kConsumerRegs = NG <= 2 ? 128 : 200, kMiscRegs = NG <= 2 ? 48 : 56;
   static constexpr int kCols = 128 + 2 * kN;                      // K | V | S | O
   static constexpr int kStages = NG <= 2 ? 7 : (NG == 4 ? 9 : 8);
   static constexpr int kOperand = kN * kHeadDim * 2;              // Q, and P
@@ -306,12 +341,23 @@ template <int NG>
 struct TeamShared {
   using S = Shape<NG>;
   float red[4][S::kN];         // per warp: row maxima, row sums
-  float alpha[S::kN];
-  uint64_t full_bar[S::kStages], empty_bar[S::kStages], s_bar, o_bar;
+  float alpha[S::kN], ref[S::kN];              // rescaling, final references
+  uint64_t full_bar[S::kStages], empty_bar[S::kStages];
+  uint64_t k_ready, s_ready;   // K (and Q) written; S written and K read
+  uint64_t p_ready, o_ready;   // P and V written; O updated and P and V read
   int usable[S::kStages];      // K slots: 0 = the plan flagged the page
   int tok[S::kN];              // token of each row within the request
-  unsigned nan[S::kN];         // value blocks that are NaN for the row (nan_keys)
+  unsigned nan[S::kN];         // value blocks that are NaN for the row
 };
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
@@ -330,17 +376,19 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   __shared__ __align__(16) TeamShared<NG> shared[S::kTeams];
   __shared__ uint32_t tmem_base;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const bool loader = warp >= 4 * S::kTeams;
-  const int team = loader ? min(warp - 4 * S::kTeams, S::kTeams - 1) : warp / 4;
-  const bool keeper = warp == 4 * S::kTeams + 3;                  // of the TMEM allocation
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
+  const int extra = warp - 4 * S::kTeams;      // loaders, MMA warps, keeper
+  const int team = extra < 0 ? warp / 4 : (extra < S::kTeams ? extra : extra - S::kTeams);
+  const bool keeper = extra == 2 * S::kTeams;  // of the TMEM allocation
   if (tid < S::kTeams) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&shared[tid].full_bar[i], 1);
       mbar_init(&shared[tid].empty_bar[i], 4);
     }
-    mbar_init(&shared[tid].s_bar, 1);
-    mbar_init(&shared[tid].o_bar, 1);
+    mbar_init(&shared[tid].k_ready, 128);
+    mbar_init(&shared[tid].s_ready, 1);
+    mbar_init(&shared[tid].p_ready, 128);
+    mbar_init(&shared[tid].o_ready, 1);
     fence_barrier_init();
   }
   griddep_wait();
@@ -354,10 +402,13 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   griddep_launch_dependents();                 // only now: a dependent may want TMEM too
   constexpr int kDone = 15;                    // named barrier: every consumer, and the keeper
   constexpr int kDoneCount = S::kTeams * 128 + 32;
-  if (keeper) {
-    named_bar_sync(kDone, kDoneCount);
-    tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+  if (extra >= 0) regs_down<S::kMiscRegs>();
+  if (extra >= 2 * S::kTeams) {
+    if (keeper) {
+      named_bar_sync(kDone, kDoneCount);
+      tc_fence_after();
+      tmem_dealloc(tmem_base, 512);
+    }
     return;
   }
   TeamShared<NG>& sh = shared[team];
@@ -366,50 +417,82 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   uint8_t* qs_ = smem + team * S::kTeamSmem;   // Q and P: K-major, 128-byte swizzle
   uint8_t* ps_ = qs_ + S::kOperand;
   uint8_t* ring = ps_ + S::kOperand;
-  Walk wk;
-  int stage = 0;
-  uint32_t phase = 0;
-  auto advance = [&]() {
-    if (++stage == kStages) { stage = 0; phase ^= 1u; }
-  };
+  const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols;
+  const uint32_t tk = tm, tv = tm + 64, ts = tm + 128, to = tm + 128 + kN;
 
-  if (loader) {
+  if (extra >= S::kTeams) {
+    // ------------------------------------------------------------------ MMAs
+    // The whole warp runs, an elected lane issues: under elect.sync an MMA of
+    // 16 columns issues every 9 cycles, under `lane == 0` (its operands then
+    // move to uniform registers one by one) every 46.
+    constexpr uint32_t idesc = idesc_f16(0, 128, kN);
+    const uint64_t dq = kstep_desc(smem_u32(qs_), 0, kN), dp = kstep_desc(smem_u32(ps_), 0, kN);
+    const uint32_t qlo = (uint32_t)dq, plo = (uint32_t)dp, hi = (uint32_t)(dq >> 32);
+    Tiles tl;
+    if (!tl.open(ws, a, vid, teams, lane)) return;
+    for (uint32_t ph = 0; tl.next(ws, a); ph ^= 1u) {
+      mbar_wait(&sh.k_ready, ph, ws.hdr);
+      __syncwarp();
+      tc_fence_after();
+      if (elect_one()) {                       // S^T = K Q^T (128 keys x rows)
+        umma_ts<false>(ts, tk, qlo, hi, idesc);
+#pragma unroll
+        for (int ks = 1; ks < 8; ++ks)
+          umma_ts<true>(ts, tk + 8 * ks, qlo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, hi, idesc);
+        umma_commit(&sh.s_ready);
+      }
+      __syncwarp();
+      mbar_wait(&sh.p_ready, ph, ws.hdr);
+      __syncwarp();
+      tc_fence_after();
+      if (elect_one()) {                       // O^T += V^T P (128 dims x rows)
+        if (tl.first) umma_ts<false>(to, tv, plo, hi, idesc);
+        else umma_ts<true>(to, tv, plo, hi, idesc);
+#pragma unroll
+        for (int ks = 1; ks < 8; ++ks)
+          umma_ts<true>(to, tv + 8 * ks, plo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, hi, idesc);
+        umma_commit(&sh.o_ready);
+      }
+      __syncwarp();
+    }
+    return;
+  }
+
+  if (extra >= 0) {
     // ---------------------------------------------------------------- loader
     // The pages of a segment 32 at a time (a lane each), one bulk copy per
     // K and V slot; of the last page only the rows that exist.
-    if (warp - 4 * S::kTeams >= S::kTeams) return;
-    if (!wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane)) return;
-    int arms = 0;
-    while (wk.next(ws, a.Hkv)) {
-      if (wk.nq > a.q_len || wk.nq == 0) continue;
-      const int32_t* bt = ws.block_table + (int64_t)wk.r * a.max_blocks;
-      int ahead = wk.j0 + lane < wk.j1 ? bt[wk.j0 + lane] : -1;
-      for (int jb = wk.j0; jb < wk.j1; jb += 32) {
-        const int mine = ahead;
-        ahead = jb + 32 + lane < wk.j1 ? bt[jb + 32 + lane] : -1;
-        for (int j = jb; j < min(jb + 32, wk.j1); ++j) {
-          const int page = __shfl_sync(0xffffffffu, mine, j - jb);
-          if (lane == 0) {
-            const int rows = min(kBlock, wk.L - j * kBlock);
-            const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;   // a multiple of 16
-            const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2;
-#pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {
-              mbar_wait(&sh.empty_bar[stage], phase ^ 1u, ws.hdr);
-              sh.usable[stage] = page >= 0;
-              if (page >= 0) {
-                mbar_arrive_expect_tx(&sh.full_bar[stage], bytes);
-                bulk_load(ring + stage * kPageBytes,
-                          (kind ? a.v_pool : a.k_pool) + (slot + kind) * kPageBytes, bytes,
-                          &sh.full_bar[stage]);
-              } else {
-                mbar_arrive(&sh.full_bar[stage]);
-              }
-              ++arms;
-              advance();
-            }
+    Tiles tl;
+    if (!tl.open(ws, a, vid, teams, lane)) return;
+    int arms = 0, stage = 0, mine = 0;
+    uint32_t phase = 0;
+    while (tl.next(ws, a)) {
+      const Walk& wk = tl.wk;
+      const int at = (tl.j - wk.j0) & 31;
+      if (at == 0)
+        mine = tl.j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + tl.j + lane]
+                                   : -1;
+      const int page = __shfl_sync(0xffffffffu, mine, at);
+      const int rows = min(kBlock, wk.L - tl.j * kBlock);
+      const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;       // a multiple of 16
+      const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2;
+      for (int kind = 0; kind < 2; ++kind) {
+        mbar_wait(&sh.empty_bar[stage], phase ^ 1u, ws.hdr);
+        __syncwarp();
+        if (elect_one()) {
+          sh.usable[stage] = page >= 0;
+          if (page >= 0) {
+            mbar_arrive_expect_tx(&sh.full_bar[stage], bytes);
+            bulk_load(ring + stage * kPageBytes,
+                      (kind ? a.v_pool : a.k_pool) + (slot + kind) * kPageBytes, bytes,
+                      &sh.full_bar[stage]);
+          } else {
+            mbar_arrive(&sh.full_bar[stage]);
           }
         }
+        __syncwarp();
+        ++arms;
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
     // Normally the consumers wait for every copy issued here.  After a wait
@@ -421,14 +504,16 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   }
 
   // -------------------------------------------------------------- consumers
+  regs_up<S::kConsumerRegs>();
   // Control flow depends on the plan's data alone (never on what a wait saw),
   // so that the team's named barriers match even after a wait gave up.
   const int w = warp & 3, ttid = tid & 127;    // within the team; ttid = key of a tile
   const int g = lane >> 2, c = lane & 3;
-  const int bar_k = 1 + 4 * team, bar_o = 2 + 4 * team, bar_all = 3 + 4 * team;
-  const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols, lanes = (uint32_t)(32 * w) << 16;
-  const uint32_t tk = tm, tv = tm + 64, ts = tm + 128, to = tm + 128 + kN;
-  constexpr uint32_t idesc = idesc_f16(0, 128, kN);
+  const int bar = 1 + team;                    // the team's named barrier
+  const uint32_t lanes = (uint32_t)(32 * w) << 16;
+  int stage = 0;
+  uint32_t phase = 0, ph = 0, o_phase = 0;     // ph: of the tile's S
+  Walk wk;
   // this lane's address for the transposed store of P: matrix i = keys 32 w + 8 i ..,
   // column k = row 8 grp + k
   const int pchunk = 4 * w + (lane >> 3);
@@ -437,11 +522,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   if (8 * NG < kN)                             // P rows that no group fills
     for (int x = ttid; x < S::kOperand / 16; x += 128)
       reinterpret_cast<uint4*>(ps_)[x] = make_uint4(0u, 0u, 0u, 0u);
-  uint32_t s_phase = 0, o_phase = 0;
   auto release = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty_bar[stage]);
-    advance();
+    if (++stage == kStages) { stage = 0; phase ^= 1u; }
   };
   const bool any = wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane);
   while (any && wk.next(ws, a.Hkv)) {
@@ -471,7 +555,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       sh.nan[ttid] = 0u;
     }
     fence_proxy_async_smem();
-    named_bar_sync(bar_all, 128);
+    named_bar_sync(bar, 128);
 
     float m[NG][2], l[NG][2];                  // rows 8 i + 2 c + {0, 1}
 #pragma unroll
@@ -488,25 +572,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       release();
       tmem_st_wait();
       tc_fence_before();
-      if (w == 0) {
-        named_bar_sync(bar_k, 128);
-        if (elect_one()) {
-          tc_fence_after();
-          const uint64_t dq = kstep_desc(smem_u32(qs_), 0, kN);
-          const uint32_t qlo = (uint32_t)dq, qhi = (uint32_t)(dq >> 32);
-          umma_ts<false>(ts, tk, qlo, qhi, idesc);
-#pragma unroll
-          for (int ks = 1; ks < 8; ++ks)
-            umma_ts<true>(ts, tk + 8 * ks, qlo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, qhi, idesc);
-          umma_commit(&sh.s_bar);
-        }
-        __syncwarp();
-      } else {
-        named_bar_arrive(bar_k, 128);
-      }
+      mbar_arrive(&sh.k_ready);
       // ---- V -> TMEM, once the last P V has read its predecessor
       if (j > wk.j0) {
-        mbar_wait(&sh.o_bar, o_phase, ws.hdr);
+        mbar_wait(&sh.o_ready, o_phase, ws.hdr);
         o_phase ^= 1u;
         tc_fence_after();
       }
@@ -527,8 +596,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       }
       release();
       // ---- softmax of S^T: 8 keys (16 hf + g, + 8) of rows 8 i + 2 c + {0, 1}
-      mbar_wait(&sh.s_bar, s_phase, ws.hdr);
-      s_phase ^= 1u;
+      mbar_wait(&sh.s_ready, ph, ws.hdr);
+      ph ^= 1u;
       tc_fence_after();
       uint32_t x[2][4 * NG];
       tmem_ld_16x256<NG>(ts + lanes, x[0]);
@@ -555,7 +624,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
                      a.scale_log2;
           move |= mx[i][k] > m[i][k] + kSlack;
         }
-      if (named_bar_any(bar_all, 128, move)) {
+      if (named_bar_any(bar, 128, move)) {
         // new references: the row maxima over the team's keys
 #pragma unroll
         for (int i = 0; i < NG; ++i)
@@ -566,7 +635,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
               mx[i][k] = fmaxf(mx[i][k], __shfl_xor_sync(0xffffffffu, mx[i][k], o));
             if (g == 0) sh.red[w][8 * i + 2 * c + k] = mx[i][k];
           }
-        named_bar_sync(bar_all, 128);
+        named_bar_sync(bar, 128);
 #pragma unroll
         for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -579,7 +648,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
             l[i][k] *= alpha;
             if (w == 0 && g == 0) sh.alpha[n] = alpha;
           }
-        named_bar_sync(bar_all, 128);
+        named_bar_sync(bar, 128);
         if (j > wk.j0) {
 #pragma unroll
           for (int n0 = 0; n0 < 8 * NG; n0 += 16) {
@@ -620,24 +689,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
-      // ---- O^T += V^T P (128 dims x rows)
-      if (w == 0) {
-        named_bar_sync(bar_o, 128);
-        if (elect_one()) {
-          tc_fence_after();
-          const uint64_t dp = kstep_desc(smem_u32(ps_), 0, kN);
-          const uint32_t plo = (uint32_t)dp, phi = (uint32_t)(dp >> 32);
-          if (j == wk.j0) umma_ts<false>(to, tv, plo, phi, idesc);
-          else umma_ts<true>(to, tv, plo, phi, idesc);
-#pragma unroll
-          for (int ks = 1; ks < 8; ++ks)
-            umma_ts<true>(to, tv + 8 * ks, plo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, phi, idesc);
-          umma_commit(&sh.o_bar);
-        }
-        __syncwarp();
-      } else {
-        named_bar_arrive(bar_o, 128);
-      }
+      mbar_arrive(&sh.p_ready);
     }
 
     // ---- the segment's result: whole rows, or a partial
@@ -650,12 +702,12 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
           l[i][k] += __shfl_xor_sync(0xffffffffu, l[i][k], o);
         const int n = 8 * i + 2 * c + k;
         if (g == 0) sh.red[w][n] = l[i][k];
-        if (w == 0 && g == 0) sh.alpha[n] = m[i][k];
+        if (w == 0 && g == 0) sh.ref[n] = m[i][k];
       }
-    mbar_wait(&sh.o_bar, o_phase, ws.hdr);
+    mbar_wait(&sh.o_ready, o_phase, ws.hdr);
     o_phase ^= 1u;
     tc_fence_after();
-    named_bar_sync(bar_all, 128);
+    named_bar_sync(bar, 128);
     const int dim = 32 * w + 4 * (lane & 7) + (lane >> 3);        // of this thread's TMEM lane
     const int slot = 2 * vid + (wk.starts ? 1 : 0);
 #pragma unroll
@@ -668,7 +720,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         const int n = n0 + e;
         if (n >= 8 * NG || n >= rows) continue;
         const float sum = sh.red[0][n] + sh.red[1][n] + sh.red[2][n] + sh.red[3][n];
-        const float M = sh.alpha[n];
+        const float M = sh.ref[n];
         float v = __uint_as_float(o[e]);
         if ((sh.nan[n] >> (dim >> 4)) & 1u) v = NAN;
         if (wk.whole) {
@@ -682,7 +734,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       }
     }
     tc_fence_before();
-    named_bar_sync(bar_all, 128);              // red, alpha, tok, nan are free again
+    named_bar_sync(bar, 128);              // red, ref, tok, nan are free again
   }
   tc_fence_before();
   named_bar_arrive(kDone, kDoneCount);
