@@ -35,13 +35,14 @@ namespace msa {
 namespace {
 
 constexpr int kMaxRows = 64;                   // query rows (tokens x group) of a KV head
-constexpr int kTeamsMax = 640;                  // partial slots: two per team
+constexpr int kTeamsMax = 512;                 // partial slots: two per team
 constexpr int kPageBytes = kBlock * kFp4Row;   // one K or V slot, 9216 bytes
 constexpr float kBias = 7.f;                   // exponent offset of the probabilities
 constexpr float kSlack = 8.f;                  // 2^(kBias + kSlack) is below fp16's largest
 
 struct DenseArgs {
   int Hkv, Hq, G, q_len, max_blocks, max_batch, rows;   // rows = G * q_len
+  uint32_t g_magic;                            // row / G = row * g_magic >> 16
   float scale_log2, v_scale;
   const __nv_bfloat16* q;
   const uint8_t *k_pool, *v_pool;
@@ -49,27 +50,41 @@ struct DenseArgs {
   float* lse;
   float* o_part;                               // [2 * teams][rows][128]
   float2* ml_part;                             // [2 * teams][rows] (m, sum)
+  int4* split;                                 // [teams] the split group that starts in the
+                                               // team's range: (partials, first token, head,
+                                               // tokens); 0 partials = none
+
+  __device__ __forceinline__ int token_of(int row) const { return (int)(row * g_magic >> 16); }
+  // row n of head h of a request whose tokens start at qs, as a row of q and out
+  __device__ __forceinline__ int64_t q_row(int qs, int h, int n) const {
+    const int t = token_of(n);
+    return (int64_t)(qs + t) * Hq + h * G + n - t * G;
+  }
 };
 
-// The range of units of team c of n: [U c / n, U (c + 1) / n).
-__device__ __forceinline__ int64_t range_of(int64_t U, int c, int n) { return U * c / n; }
-// The team whose range holds unit u.
-__device__ __forceinline__ int team_of(int64_t U, int64_t u, int n) {
-  return (int)(((u + 1) * n - 1) / U);
-}
+// U units in n contiguous ranges, the first U % n of them one unit longer.
+struct Partition {
+  uint32_t q, rem;
+  __device__ __forceinline__ Partition(uint32_t U, uint32_t n) : q(U / n), rem(U - U / n * n) {}
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + min(c, rem); }
+  __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+    const uint32_t longer = rem * (q + 1);
+    return u < longer ? u / (q + 1) : rem + (u - longer) / q;
+  }
+};
 
 // The request that holds unit u: the last r with cu[r] * Hkv <= u (requests
 // without blocks hold none).  One warp, 32 probes at a time; `first` is this
 // lane's cu[min(lane, max_batch)], so that a batch of up to 32 needs no load.
-__device__ __forceinline__ int request_of(const int32_t* cu, int first, int batch, int Hkv,
-                                          int64_t u, int lane) {
+__device__ __forceinline__ int request_of(const int32_t* cu, int first, int batch, uint32_t Hkv,
+                                          uint32_t u, int lane) {
   int lo = 0, n = batch;                       // the answer lies in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lo + lane * step;
     const bool in = i < lo + n;
     const int at = batch <= 32 ? first : (in ? cu[i] : 0);
-    const bool below = in && (int64_t)at * Hkv <= u;
+    const bool below = in && (uint32_t)at * Hkv <= u;
     const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));   // lane 0 is always below
     const int end = lo + n;
     lo += k * step;
@@ -80,30 +95,32 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int first, int batc
 
 // A team's walk over its range: one segment per (request, KV head) it meets.
 struct Walk {
-  int64_t u, end;              // next unit, end of the range
+  uint32_t u, end;             // next unit, end of the range
   int r;                       // request of unit u
   // the current segment
-  int h, j0, j1, nq, qs, L, nb;
+  int h, j0, j1, nq, qs, L;
+  uint32_t last;               // its group's last unit
   bool starts, whole;          // it starts its group; it is all of its group
 
   // The range of team vid; false if it has none.  One warp, all lanes alike.
-  __device__ __forceinline__ bool open(const WsView& ws, int max_batch, int Hkv, int vid,
-                                       int teams, int lane) {
-    const int first = ws.req_cu_nb[min(lane, max_batch)];
+  __device__ __forceinline__ bool open(const WsView& ws, const DenseArgs& a, int vid, int teams,
+                                       int lane) {
+    const int first = ws.req_cu_nb[min(lane, a.max_batch)];
     const int batch = ws.hdr->batch;
-    const int64_t U = (int64_t)ws.hdr->total_blocks * Hkv;
-    const int n = (int)min((int64_t)teams, U);
-    if (vid >= n) return false;
-    u = range_of(U, vid, n);
-    end = range_of(U, vid + 1, n);
-    r = request_of(ws.req_cu_nb, first, batch, Hkv, u, lane);
+    const uint32_t U = (uint32_t)ws.hdr->total_blocks * a.Hkv;
+    const uint32_t n = min((uint32_t)teams, U);
+    if ((uint32_t)vid >= n) return false;
+    const Partition p(U, n);
+    u = p.start(vid);
+    end = p.start(vid + 1);
+    r = request_of(ws.req_cu_nb, first, batch, a.Hkv, u, lane);
     return true;
   }
   // The next segment; false at the end of the range.
-  __device__ __forceinline__ bool next(const WsView& ws, int Hkv) {
+  __device__ __forceinline__ bool next(const WsView& ws, uint32_t Hkv) {
     if (u >= end) return false;
-    int cu0 = ws.req_cu_nb[r], cu1 = ws.req_cu_nb[r + 1];   // u is below the last request's end
-    while ((int64_t)cu1 * Hkv <= u) {
+    uint32_t cu0 = ws.req_cu_nb[r], cu1 = ws.req_cu_nb[r + 1];   // u is below the last request's end
+    while (cu1 * Hkv <= u) {
       ++r;
       cu0 = cu1;
       cu1 = ws.req_cu_nb[r + 1];
@@ -111,14 +128,14 @@ struct Walk {
     qs = ws.req_qstart[r];
     nq = ws.req_qstart[r + 1] - qs;
     L = ws.req_seq_len[r];
-    nb = cu1 - cu0;
-    const int64_t first = (int64_t)cu0 * Hkv;
-    h = (int)((u - first) / nb);
-    const int64_t ga = first + (int64_t)h * nb;             // the group's units: [ga, ga + nb)
+    const uint32_t nb = cu1 - cu0;
+    h = (int)((u - cu0 * Hkv) / nb);
+    const uint32_t ga = cu0 * Hkv + h * nb;                 // the group's units: [ga, ga + nb)
+    last = ga + nb - 1;
     j0 = (int)(u - ga);
     j1 = (int)(min(ga + nb, end) - ga);
     starts = j0 == 0;
-    whole = starts && j1 == nb;
+    whole = starts && j1 == (int)nb;
     u = ga + j1;
     return true;
   }
@@ -217,7 +234,7 @@ __device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
 // K: this thread's key row (72 bytes) -> its TMEM lane, 64 columns of two dims.
 __device__ __forceinline__ void key_row(const uint8_t* row, uint32_t taddr) {
   const uint2 sb = *reinterpret_cast<const uint2*>(row + kHeadDim / 2);
-#pragma unroll
+#pragma unroll 1
   for (int half = 0; half < 2; ++half) {       // 64 dims, 4 blocks
     const uint32_t s4 = half ? sb.y : sb.x;
     const uint32_t sp[2] = {e4m3x2_to_f16x2((uint16_t)(s4 & 0xffffu)),
@@ -242,16 +259,17 @@ __device__ __forceinline__ void key_row(const uint8_t* row, uint32_t taddr) {
 
 // V, transposed: this warp's dims 32 w .. 32 w + 31 of the tile's 128 keys ->
 // TMEM lanes 32 w + 8 i + g = dim 32 w + 4 g + i, 64 columns of two keys.
-// EDGE: keys from ntok on do not exist (their rows may hold anything), and a
-// NaN scale of a key that not every row sees becomes 0 here (nan_keys).
-template <bool EDGE>
+// Keys from ntok on do not exist (their rows may hold anything), and a NaN
+// scale of a key that not every row sees becomes 0 here: 0 * NaN is not 0 (the
+// rows that see it get it back at the end).
 __device__ __forceinline__ void value_dims(const uint8_t* vt, uint32_t taddr, int w, int lane,
                                            int ntok, int all) {
   constexpr uint32_t m = 0x0f0f0f0fu;
   const int g = lane >> 2, c = lane & 3;
   const uint8_t* codes = vt + 4 * c * kFp4Row + 16 * w + 2 * g;
   const uint8_t* scales = vt + 4 * c * kFp4Row + kHeadDim / 2 + 2 * w + (g >> 2);
-#pragma unroll
+  const bool edge = all < kBlock;
+#pragma unroll 1
   for (int half = 0; half < 2; ++half) {       // 64 keys
     uint32_t lo[16], hi[16];
 #pragma unroll
@@ -262,7 +280,10 @@ __device__ __forceinline__ void value_dims(const uint8_t* vt, uint32_t taddr, in
       for (int i = 0; i < 4; ++i) {
         u[i] = *reinterpret_cast<const uint16_t*>(codes + k0 + i * kFp4Row);
         s[i] = scales[k0 + i * kFp4Row];
-        if (EDGE) {
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const int key = 64 * half + 16 * qq + 4 * c + i;
           if (key >= ntok || (key >= all && (s[i] & 0x7f) == 0x7f)) s[i] = 0;
         }
@@ -300,7 +321,7 @@ struct Tiles {
     j = 0;
     seg = -1;
     last = true;
-    return wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane);
+    return wk.open(ws, a, vid, teams, lane);
   }
   // Skips the segments of requests without new tokens, or with more than the
   // config's (the consumers flag those).
@@ -331,11 +352,14 @@ struct Shape {
   // 640 x 96 = 384 x 128 + 256 x 48; 512 x 128 = 256 x 200 + 256 x 56
   static constexpr int kConsumerRegs = NG <= 2 ? 128 : 200, kMiscRegs = NG <= 2 ? 48 : 56;
   static constexpr int kCols = 128 + 2 * kN;                      // K | V | S | O
-  static constexpr int kStages = NG <= 2 ? 7 : (NG == 4 ? 9 : 8);
-  static constexpr int kOperand = kN * kHeadDim * 2;              // Q, and P
-  static constexpr int kTeamSmem = 2 * kOperand + kStages * kPageBytes;
+  static constexpr int kStages = NG <= 2 ? 6 : (NG == 4 ? 8 : 6);
+  static constexpr int kOperand = kN * kHeadDim * 2;              // a Q buffer, and P
+  static constexpr int kTeamSmem = 3 * kOperand + kStages * kPageBytes;
   static constexpr int kSmem = kTeams * kTeamSmem;
 };
+
+// Phase parity of the use number t of buffer t & 1.
+__device__ __forceinline__ uint32_t par(int t) { return (uint32_t)(t >> 1) & 1u; }
 
 template <int NG>
 struct TeamShared {
@@ -343,7 +367,8 @@ struct TeamShared {
   float red[4][S::kN];         // per warp: row maxima, row sums
   float alpha[S::kN], ref[S::kN];              // rescaling, final references
   uint64_t full_bar[S::kStages], empty_bar[S::kStages];
-  uint64_t k_ready, s_ready;   // K (and Q) written; S written and K read
+  uint64_t q_ready[2], q_free[2];              // Q written by the loader; buffer free again
+  uint64_t k_ready, s_ready;   // K written; S written and K read
   uint64_t p_ready, o_ready;   // P and V written; O updated and P and V read
   int usable[S::kStages];      // K slots: 0 = the plan flagged the page
   int tok[S::kN];              // token of each row within the request
@@ -381,44 +406,56 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   const int team = extra < 0 ? warp / 4 : (extra < S::kTeams ? extra : extra - S::kTeams);
   const bool keeper = extra == 2 * S::kTeams;  // of the TMEM allocation
   if (tid < S::kTeams) {
+    TeamShared<NG>& st = shared[tid];
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&shared[tid].full_bar[i], 1);
-      mbar_init(&shared[tid].empty_bar[i], 4);
+      mbar_init(&st.full_bar[i], 1);
+      mbar_init(&st.empty_bar[i], 4);
     }
-    mbar_init(&shared[tid].k_ready, 128);
-    mbar_init(&shared[tid].s_ready, 1);
-    mbar_init(&shared[tid].p_ready, 128);
-    mbar_init(&shared[tid].o_ready, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&st.q_ready[i], 32);
+      mbar_init(&st.q_free[i], 128);
+    }
+    mbar_init(&st.k_ready, 128);
+    mbar_init(&st.s_ready, 1);
+    mbar_init(&st.p_ready, 128);
+    mbar_init(&st.o_ready, 1);
     fence_barrier_init();
   }
-  griddep_wait();
-  if (keeper) {
-    tmem_alloc(&tmem_base, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  griddep_launch_dependents();                 // only now: a dependent may want TMEM too
+  griddep_wait();
   constexpr int kDone = 15;                    // named barrier: every consumer, and the keeper
   constexpr int kDoneCount = S::kTeams * 128 + 32;
+  constexpr int kAlloc = 14;                   // the same and the MMA warps
+  constexpr int kAllocCount = S::kTeams * 160 + 32;
   if (extra >= 0) regs_down<S::kMiscRegs>();
   if (extra >= 2 * S::kTeams) {
-    if (keeper) {
-      named_bar_sync(kDone, kDoneCount);
-      tc_fence_after();
-      tmem_dealloc(tmem_base, 512);
+    if (!keeper) return;
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+    tc_fence_before();
+    named_bar_sync(kAlloc, kAllocCount);
+    tc_fence_after();
+    griddep_launch_dependents();               // only now: a dependent may want TMEM too
+    // tokens of no request, and of requests with more tokens than the config's
+    const int T = ws.hdr->num_tokens;
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+      const int r = ws.tok_req[t];
+      if (r >= 0 && ws.req_qstart[r + 1] - ws.req_qstart[r] <= a.q_len) continue;
+      for (int x = lane; x < a.Hq * (kHeadDim / 8); x += 32)
+        reinterpret_cast<uint4*>(a.out + (int64_t)t * a.Hq * kHeadDim)[x] = make_uint4(0, 0, 0, 0);
+      for (int x = lane; x < a.Hq; x += 32) a.lse[(int64_t)t * a.Hq + x] = -INFINITY;
     }
+    named_bar_sync(kDone, kDoneCount);
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
     return;
   }
   TeamShared<NG>& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
   const int teams = S::kTeams * (int)gridDim.x;
-  uint8_t* qs_ = smem + team * S::kTeamSmem;   // Q and P: K-major, 128-byte swizzle
-  uint8_t* ps_ = qs_ + S::kOperand;
-  uint8_t* ring = ps_ + S::kOperand;
-  const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols;
-  const uint32_t tk = tm, tv = tm + 64, ts = tm + 128, to = tm + 128 + kN;
+  uint8_t* qbuf = smem + team * S::kTeamSmem;  // Q x 2 and P: K-major, 128-byte swizzle
+  uint8_t* pbuf = qbuf + 2 * S::kOperand;
+  uint8_t* ring = pbuf + S::kOperand;
 
   if (extra >= S::kTeams) {
     // ------------------------------------------------------------------ MMAs
@@ -426,11 +463,18 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     // 16 columns issues every 9 cycles, under `lane == 0` (its operands then
     // move to uniform registers one by one) every 46.
     constexpr uint32_t idesc = idesc_f16(0, 128, kN);
-    const uint64_t dq = kstep_desc(smem_u32(qs_), 0, kN), dp = kstep_desc(smem_u32(ps_), 0, kN);
-    const uint32_t qlo = (uint32_t)dq, plo = (uint32_t)dp, hi = (uint32_t)(dq >> 32);
+    const uint64_t dq = kstep_desc(smem_u32(qbuf), 0, kN), dp = kstep_desc(smem_u32(pbuf), 0, kN);
+    const uint32_t plo = (uint32_t)dp, hi = (uint32_t)(dq >> 32);
     Tiles tl;
-    if (!tl.open(ws, a, vid, teams, lane)) return;
+    const bool any = tl.open(ws, a, vid, teams, lane);
+    named_bar_sync(kAlloc, kAllocCount);
+    tc_fence_after();
+    const uint32_t tk = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols, tv = tk + 64,
+                   ts = tk + 128, to = tk + 128 + kN;
+    if (!any) return;
     for (uint32_t ph = 0; tl.next(ws, a); ph ^= 1u) {
+      const uint32_t qlo = (uint32_t)dq + (tl.seg & 1) * (S::kOperand >> 4);
+      if (tl.first) mbar_wait(&sh.q_ready[tl.seg & 1], par(tl.seg), ws.hdr);
       mbar_wait(&sh.k_ready, ph, ws.hdr);
       __syncwarp();
       tc_fence_after();
@@ -461,7 +505,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   if (extra >= 0) {
     // ---------------------------------------------------------------- loader
     // The pages of a segment 32 at a time (a lane each), one bulk copy per
-    // K and V slot; of the last page only the rows that exist.
+    // K and V slot; of the last page only the rows that exist.  Each segment's
+    // Q rows, bf16 -> fp16, go to the B operand after its first page.
     Tiles tl;
     if (!tl.open(ws, a, vid, teams, lane)) return;
     int arms = 0, stage = 0, mine = 0;
@@ -494,6 +539,29 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         ++arms;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
+      if (tl.first) {
+        const int nrows = wk.nq * a.G, b = tl.seg & 1;
+        if (tl.seg >= 2) mbar_wait(&sh.q_free[b], par(tl.seg - 2), ws.hdr);
+        bool ovf = false;
+#pragma unroll 4
+        for (int x = lane; x < kN * 16; x += 32) {
+          const int n = x >> 4, ch = x & 15;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);                   // rows past the last: zero
+          if (n < nrows)
+            v = *reinterpret_cast<const uint4*>(a.q + a.q_row(wk.qs, wk.h, n) * kHeadDim + 8 * ch);
+          v.x = bf16x2_to_f16x2(v.x);
+          v.y = bf16x2_to_f16x2(v.y);
+          v.z = bf16x2_to_f16x2(v.z);
+          v.w = bf16x2_to_f16x2(v.w);
+          ovf |= f16x2_has_inf(v.x) | f16x2_has_inf(v.y) | f16x2_has_inf(v.z) |
+                 f16x2_has_inf(v.w);
+          *reinterpret_cast<uint4*>(qbuf + b * S::kOperand + kmaj_off(n, ch, kN)) = v;
+        }
+        if (__any_sync(0xffffffffu, ovf) && lane == 0)
+          set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.q_ready[b]);
+      }
     }
     // Normally the consumers wait for every copy issued here.  After a wait
     // gave up they may not have: let the copies in flight land.
@@ -513,48 +581,37 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   const uint32_t lanes = (uint32_t)(32 * w) << 16;
   int stage = 0;
   uint32_t phase = 0, ph = 0, o_phase = 0;     // ph: of the tile's S
-  Walk wk;
   // this lane's address for the transposed store of P: matrix i = keys 32 w + 8 i ..,
   // column k = row 8 grp + k
   const int pchunk = 4 * w + (lane >> 3);
-  const uint32_t paddr = smem_u32(ps_) + (pchunk >> 3) * kN * 128 + (lane & 7) * 128 +
+  const uint32_t paddr = smem_u32(pbuf) + (pchunk >> 3) * kN * 128 + (lane & 7) * 128 +
                          (((pchunk & 7) ^ (lane & 7)) << 4);
   if (8 * NG < kN)                             // P rows that no group fills
     for (int x = ttid; x < S::kOperand / 16; x += 128)
-      reinterpret_cast<uint4*>(ps_)[x] = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint4*>(pbuf)[x] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   auto release = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty_bar[stage]);
     if (++stage == kStages) { stage = 0; phase ^= 1u; }
   };
-  const bool any = wk.open(ws, a.max_batch, a.Hkv, vid, teams, lane);
-  while (any && wk.next(ws, a.Hkv)) {
+  Walk wk;
+  const bool any = wk.open(ws, a, vid, teams, lane);
+  named_bar_sync(kAlloc, kAllocCount);
+  tc_fence_after();
+  const uint32_t tm = tmem_base + team * S::kCols + lanes;
+  const uint32_t tk = tm, tv = tm + 64, ts = tm + 128, to = tm + 128 + kN;
+  int4 split = make_int4(0, 0, 0, 0);
+  for (int seg = 0; any && wk.next(ws, a.Hkv);) {
     if (wk.nq > a.q_len || wk.nq == 0) {       // more tokens than the config's, or none
       if (ttid == 0 && wk.nq > 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
       continue;
     }
     const int rows = wk.nq * a.G;
-    // ---- Q: bf16 -> fp16 rows of the B operand, zero past the last row
-    bool ovf = false;
-    for (int x = ttid; x < kN * 16; x += 128) {
-      const int n = x >> 4, ch = x & 15;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (n < rows)
-        v = *reinterpret_cast<const uint4*>(
-            a.q + ((int64_t)(wk.qs + n / a.G) * a.Hq + wk.h * a.G + n % a.G) * kHeadDim + 8 * ch);
-      v.x = bf16x2_to_f16x2(v.x);
-      v.y = bf16x2_to_f16x2(v.y);
-      v.z = bf16x2_to_f16x2(v.z);
-      v.w = bf16x2_to_f16x2(v.w);
-      ovf |= f16x2_has_inf(v.x) | f16x2_has_inf(v.y) | f16x2_has_inf(v.z) | f16x2_has_inf(v.w);
-      *reinterpret_cast<uint4*>(qs_ + kmaj_off(n, ch, kN)) = v;
-    }
-    if (__any_sync(0xffffffffu, ovf) && lane == 0) set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
     if (ttid < kN) {
-      sh.tok[ttid] = min(ttid / a.G, wk.nq - 1);
+      sh.tok[ttid] = min(a.token_of(ttid), wk.nq - 1);
       sh.nan[ttid] = 0u;
     }
-    fence_proxy_async_smem();
     named_bar_sync(bar, 128);
 
     float m[NG][2], l[NG][2];                  // rows 8 i + 2 c + {0, 1}
@@ -568,7 +625,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const int ntok = sh.usable[stage] ? wk.L - j * kBlock : 0;   // keys that exist
       const int all = ntok - wk.nq + 1;                            // and that every row sees
-      key_row(ring + stage * kPageBytes + ttid * kFp4Row, tk + lanes);
+      key_row(ring + stage * kPageBytes + ttid * kFp4Row, tk);
       release();
       tmem_st_wait();
       tc_fence_before();
@@ -581,10 +638,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       }
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const uint8_t* vt = ring + stage * kPageBytes;
-      if (all >= kBlock) {
-        value_dims<false>(vt, tv + lanes, w, lane, ntok, all);
-      } else {
-        value_dims<true>(vt, tv + lanes, w, lane, ntok, all);
+      value_dims(vt, tv, w, lane, ntok, all);
+      if (all < kBlock) {
         if (ttid >= all && ttid < ntok) {      // NaN scales that only later tokens see
           unsigned bad = 0;
           for (int b = 0; b < 8; ++b)
@@ -600,8 +655,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       ph ^= 1u;
       tc_fence_after();
       uint32_t x[2][4 * NG];
-      tmem_ld_16x256<NG>(ts + lanes, x[0]);
-      tmem_ld_16x256<NG>(ts + lanes + (16u << 16), x[1]);
+      tmem_ld_16x256<NG>(ts, x[0]);
+      tmem_ld_16x256<NG>(ts + (16u << 16), x[1]);
       tmem_ld_wait();
       if (all < kBlock) {
 #pragma unroll
@@ -653,13 +708,13 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 #pragma unroll
           for (int n0 = 0; n0 < 8 * NG; n0 += 16) {
             uint32_t o[16];
-            tmem_ld16(to + lanes + n0, o);
+            tmem_ld16(to + n0, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               if (n0 + e < 8 * NG)
                 o[e] = __float_as_uint(__uint_as_float(o[e]) * sh.alpha[n0 + e]);
-            tmem_st16(to + lanes + n0, o);
+            tmem_st16(to + n0, o);
           }
           tmem_st_wait();
         }
@@ -708,113 +763,142 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     o_phase ^= 1u;
     tc_fence_after();
     named_bar_sync(bar, 128);
+    // O^T -> [row][dim] in the segment's Q buffer and in P (S and P V are done)
     const int dim = 32 * w + 4 * (lane & 7) + (lane >> 3);        // of this thread's TMEM lane
-    const int slot = 2 * vid + (wk.starts ? 1 : 0);
+    uint8_t* qcur = qbuf + (seg & 1) * S::kOperand;
+    auto o_row = [&](int n) {
+      return reinterpret_cast<float*>((n < kN / 2 ? qcur : pbuf) + (n & (kN / 2 - 1)) * 512);
+    };
 #pragma unroll
     for (int n0 = 0; n0 < 8 * NG; n0 += 16) {
       uint32_t o[16];
-      tmem_ld16(to + lanes + n0, o);
+      tmem_ld16(to + n0, o);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int n = n0 + e;
-        if (n >= 8 * NG || n >= rows) continue;
-        const float sum = sh.red[0][n] + sh.red[1][n] + sh.red[2][n] + sh.red[3][n];
-        const float M = sh.ref[n];
-        float v = __uint_as_float(o[e]);
-        if ((sh.nan[n] >> (dim >> 4)) & 1u) v = NAN;
-        if (wk.whole) {
-          const int64_t hq = (int64_t)(wk.qs + n / a.G) * a.Hq + wk.h * a.G + n % a.G;
-          a.out[hq * kHeadDim + dim] = __float2bfloat16_rn(sum == 0.f ? 0.f : v * (a.v_scale / sum));
-          if (ttid == 0) a.lse[hq] = sum == 0.f ? -INFINITY : (M + log2f(sum) - kBias) * kLn2;
-        } else {
-          a.o_part[((int64_t)slot * a.rows + n) * kHeadDim + dim] = v;
-          if (ttid == 0) a.ml_part[(int64_t)slot * a.rows + n] = make_float2(M, sum);
-        }
-      }
+      for (int e = 0; e < 16; ++e)
+        if (n0 + e < 8 * NG) o_row(n0 + e)[dim] = __uint_as_float(o[e]);
     }
     tc_fence_before();
-    named_bar_sync(bar, 128);              // red, ref, tok, nan are free again
+    named_bar_sync(bar, 128);
+    const int64_t slot = 2 * vid + (wk.starts ? 1 : 0);
+#pragma unroll 1
+    for (int x = ttid; x < rows * 16; x += 128) {
+      const int n = x >> 4, part = x & 15;     // 8 dims, half a value block
+      const float sum = sh.red[0][n] + sh.red[1][n] + sh.red[2][n] + sh.red[3][n];
+      const float4* src = reinterpret_cast<const float4*>(o_row(n) + 8 * part);
+      float4 y0 = src[0], y1 = src[1];
+      if ((sh.nan[n] >> (part >> 1)) & 1u) y0 = y1 = make_float4(NAN, NAN, NAN, NAN);
+      if (wk.whole) {
+        const int64_t row = a.q_row(wk.qs, wk.h, n);
+        const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+        *reinterpret_cast<uint4*>(a.out + row * kHeadDim + 8 * part) =
+            make_uint4(pack_bf16(y0.x * inv, y0.y * inv), pack_bf16(y0.z * inv, y0.w * inv),
+                       pack_bf16(y1.x * inv, y1.y * inv), pack_bf16(y1.z * inv, y1.w * inv));
+        if (part == 0)
+          a.lse[row] = sum == 0.f ? -INFINITY : (sh.ref[n] + log2f(sum) - kBias) * kLn2;
+      } else {
+        float4* dst = reinterpret_cast<float4*>(a.o_part + (slot * a.rows + n) * kHeadDim + 8 * part);
+        dst[0] = y0;
+        dst[1] = y1;
+        if (part == 0) a.ml_part[slot * a.rows + n] = make_float2(sh.ref[n], sum);
+      }
+    }
+    if (wk.starts && !wk.whole) {              // the range ends inside this group
+      const uint32_t U = (uint32_t)ws.hdr->total_blocks * a.Hkv;
+      const int c1 = (int)Partition(U, min((uint32_t)teams, U)).owner(wk.last);
+      split = make_int4(c1 - vid + 1, wk.qs, wk.h, wk.nq);
+    }
+    if (8 * NG == kN)                          // P rows are refilled; Q goes to the loader
+      fence_proxy_async_smem();
+    named_bar_sync(bar, 128);                  // red, ref, tok, nan and P are free again
+    mbar_arrive(&sh.q_free[seg & 1]);
+    ++seg;
   }
+  if (ttid == 0) a.split[vid] = split;
   tc_fence_before();
   named_bar_arrive(kDone, kDoneCount);
 }
 
 // Merges the partials of the (request, head) groups that lie in several teams'
-// ranges, in team order: block (x, y) takes the group that starts in team x's
-// range and ends behind it, and rows y * kMergeRows .. of it, four warps a
-// row.  Tokens without a valid request get out = 0, lse = -inf.
+// ranges, in team order.  Every block lists the split groups in order, then
+// takes its share of (group, kMergeRows rows), four warps a row.
 constexpr int kMergeRows = 2;
-__global__ void __launch_bounds__(kMergeRows * 128)
-dense_merge_kernel(WsView ws, DenseArgs a, int teams) {
+constexpr int kMergeThreads = kMergeRows * 128;
+__global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a, int teams) {
+  static_assert(kTeamsMax <= 2 * kMergeThreads, "two records a thread");
+  __shared__ int4 list[kTeamsMax];
+  __shared__ int owner[kTeamsMax];
+  __shared__ int counts[kMergeThreads / 32];
   __shared__ float4 part[kMergeRows][4][32];
   __shared__ float part_l[kMergeRows][4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mr = warp >> 2, w4 = warp & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  const int T = ws.hdr->num_tokens, batch = ws.hdr->batch;
-  const int64_t U = (int64_t)ws.hdr->total_blocks * a.Hkv;
-  // idle tokens, and those of requests with more tokens than the config's
-  for (int64_t x = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * kMergeRows * 4 + warp;
-       x < (int64_t)T * a.Hq; x += (int64_t)gridDim.x * gridDim.y * kMergeRows * 4) {
-    const int t = (int)(x / a.Hq);
-    const int r = ws.tok_req[t];
-    if (r >= 0 && ws.req_qstart[r + 1] - ws.req_qstart[r] <= a.q_len) continue;
-    reinterpret_cast<uint2*>(a.out + x * kHeadDim)[lane] = make_uint2(0u, 0u);
-    if (lane == 0) a.lse[x] = -INFINITY;
-  }
-  const int n = (int)min((int64_t)teams, U);
-  const int c0 = blockIdx.x;
-  if (c0 >= n) return;
-  const int64_t lo = range_of(U, c0, n), hi = range_of(U, c0 + 1, n);
-  const int r = request_of(ws.req_cu_nb, ws.req_cu_nb[min(lane, a.max_batch)], batch, a.Hkv,
-                           hi - 1, lane);
-  const int nb = ws.req_nb[r], qs = ws.req_qstart[r], nq = ws.req_qstart[r + 1] - qs;
-  const int64_t first = (int64_t)ws.req_cu_nb[r] * a.Hkv;
-  const int h = (int)((hi - 1 - first) / nb);
-  const int64_t ga = first + (int64_t)h * nb, gb = ga + nb;
-  if (ga < lo || gb <= hi || nq > a.q_len) return;           // block-uniform
-  const int c1 = team_of(U, gb - 1, n), np = c1 - c0 + 1;
-  const int row = blockIdx.y * kMergeRows + mr;
-  const bool on = row < nq * a.G;
-  // partial i: the second slot of c0, the first of c0 + i
-  auto slot_of = [&](int i) { return 2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0); };
-  float M = -INFINITY;
-  if (on)
-    for (int i = lane; i < np; i += 32)
-      M = fmaxf(M, a.ml_part[slot_of(i) * a.rows + row].x);
+  int n = 0;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  if (on) {
-#pragma unroll 4
-    for (int i = w4; i < np; i += 4) {
-      const float2 ml = a.ml_part[slot_of(i) * a.rows + row];
-      const float4 v = *reinterpret_cast<const float4*>(
-          a.o_part + (slot_of(i) * a.rows + row) * kHeadDim + 4 * lane);
-      const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
-      l = fmaf(f, ml.y, l);
-      o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+  for (int half = 0; half < 2; ++half) {
+    const int c = half * kMergeThreads + tid;
+    const int4 rec = c < teams ? a.split[c] : make_int4(0, 0, 0, 0);
+    const unsigned any = __ballot_sync(0xffffffffu, rec.x > 0);
+    if (half) __syncthreads();
+    if (lane == 0) counts[warp] = __popc(any);
+    __syncthreads();
+    int at = n + __popc(any & ((1u << lane) - 1u));
+    for (int i = 0; i < kMergeThreads / 32; ++i) {
+      if (i < warp) at += counts[i];
+      n += counts[i];
+    }
+    if (rec.x > 0) {
+      list[at] = rec;
+      owner[at] = c;
     }
   }
-  part[mr][w4][lane] = o;
-  if (lane == 0) part_l[mr][w4] = l;
   __syncthreads();
-  if (!on || w4 != 0) return;
+  const int chunks = (a.rows + kMergeRows - 1) / kMergeRows;
+  const int mr = warp >> 2, w4 = warp & 3;
+  for (int item = blockIdx.x; item < n * chunks; item += gridDim.x) {
+    const int4 rec = list[item / chunks];
+    const int64_t c0 = owner[item / chunks];
+    const int np = rec.x, row = item % chunks * kMergeRows + mr;
+    const bool on = row < rec.w * a.G;
+    // partial i: the second slot of c0, the first of c0 + i
+    auto at = [&](int i) { return (2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
+    float M = -INFINITY;
+    if (on)
+      for (int i = lane; i < np; i += 32) M = fmaxf(M, a.ml_part[at(i)].x);
 #pragma unroll
-  for (int w = 1; w < 4; ++w) {
-    const float4 v = part[mr][w][lane];
-    o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-    l += part_l[mr][w];
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (on) {
+#pragma unroll 4
+      for (int i = w4; i < np; i += 4) {
+        const float2 ml = a.ml_part[at(i)];
+        const float4 v = *reinterpret_cast<const float4*>(a.o_part + at(i) * kHeadDim + 4 * lane);
+        const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
+        l = fmaf(f, ml.y, l);
+        o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+      }
+    }
+    part[mr][w4][lane] = o;
+    if (lane == 0) part_l[mr][w4] = l;
+    __syncthreads();
+    if (on && w4 == 0) {
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float4 v = part[mr][w][lane];
+        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+        l += part_l[mr][w];
+      }
+      const int64_t hq = a.q_row(rec.y, rec.z, row);
+      const float inv = l == 0.f ? 0.f : a.v_scale / l;
+      reinterpret_cast<uint2*>(a.out + hq * kHeadDim)[lane] =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (lane == 0) a.lse[hq] = l == 0.f ? -INFINITY : (M + log2f(l) - kBias) * kLn2;
+    }
+    __syncthreads();
   }
-  const int64_t hq = (int64_t)(qs + row / a.G) * a.Hq + h * a.G + row % a.G;
-  const float inv = l == 0.f ? 0.f : a.v_scale / l;
-  reinterpret_cast<uint2*>(a.out + hq * kHeadDim)[lane] =
-      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (lane == 0) a.lse[hq] = l == 0.f ? -INFINITY : (M + log2f(l) - kBias) * kLn2;
 }
 
 template <int NG>
@@ -830,17 +914,19 @@ msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cuda
       return MSA_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
   }
-  int64_t grid = sm_count();                   // one CTA an SM
+  const int sms = sm_count();
+  int64_t grid = sms;                          // one CTA an SM
   if (grid > kTeamsMax / S::kTeams) grid = kTeamsMax / S::kTeams;
   if (grid > units) grid = units;
   if (grid <= 0) return MSA_ERR_CUDA;
   const int teams = (int)grid * S::kTeams;
-  msa_status st = launch_pdl(dense_decode_kernel<NG>, dim3((unsigned)grid),
-                             dim3(S::kThreads), S::kSmem, s, v, a);
+  msa_status st = launch_pdl(dense_decode_kernel<NG>, dim3((unsigned)grid), dim3(S::kThreads),
+                             S::kSmem, s, v, a);
   if (st != MSA_OK) return st;
-  return launch_pdl(dense_merge_kernel,
-                    dim3((unsigned)teams, (unsigned)((a.rows + kMergeRows - 1) / kMergeRows)),
-                    dim3(kMergeRows * 128), 0, s, v, a, teams);
+  int64_t blocks = (int64_t)teams * ((a.rows + kMergeRows - 1) / kMergeRows);
+  if (blocks > 4 * sms) blocks = 4 * sms;
+  return launch_pdl(dense_merge_kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a,
+                    teams);
 }
 
 bool dense_supported(const msa_config& c) {
@@ -857,7 +943,7 @@ extern "C" size_t msa_dense_decode_scratch_bytes(const msa_config* cfg) {
   if (check_config(cfg) != MSA_OK || !dense_supported(*cfg)) return 0;
   const size_t rows = (size_t)(cfg->num_q_heads / cfg->num_kv_heads) * cfg->q_len;
   return align_up(2 * (size_t)kTeamsMax * rows * kHeadDim * 4) +
-         align_up(2 * (size_t)kTeamsMax * rows * 8);
+         align_up(2 * (size_t)kTeamsMax * rows * 8) + align_up(kTeamsMax * sizeof(int4));
 }
 
 extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const void* q,
@@ -889,9 +975,12 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   a.out = (__nv_bfloat16*)out;
   a.lse = lse;
   a.o_part = (float*)scratch;
+  a.g_magic = (65536u + a.G - 1) / a.G;        // exact for rows below 128 and G <= 16
   a.ml_part = (float2*)((char*)scratch + align_up(2 * (size_t)kTeamsMax * a.rows * kHeadDim * 4));
+  a.split = (int4*)((char*)a.ml_part + align_up(2 * (size_t)kTeamsMax * a.rows * 8));
   const WsView v = view_of(*cfg, ws);
   const int64_t units = (int64_t)cfg->max_batch * cfg->max_blocks_per_req * a.Hkv;
+  if (units > 0x7fffffff) return MSA_ERR_UNSUPPORTED;   // units are counted in 32 bits
   cudaStream_t s = (cudaStream_t)stream;
   if (a.rows <= 8) return launch_dense<1>(v, a, units, s);
   if (a.rows <= 16) return launch_dense<2>(v, a, units, s);
