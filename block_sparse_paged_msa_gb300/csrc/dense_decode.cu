@@ -234,7 +234,7 @@ __device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
 // K: this thread's key row (72 bytes) -> its TMEM lane, 64 columns of two dims.
 __device__ __forceinline__ void key_row(const uint8_t* row, uint32_t taddr) {
   const uint2 sb = *reinterpret_cast<const uint2*>(row + kHeadDim / 2);
-#pragma unroll 1
+#pragma unroll
   for (int half = 0; half < 2; ++half) {       // 64 dims, 4 blocks
     const uint32_t s4 = half ? sb.y : sb.x;
     const uint32_t sp[2] = {e4m3x2_to_f16x2((uint16_t)(s4 & 0xffffu)),
@@ -262,14 +262,14 @@ __device__ __forceinline__ void key_row(const uint8_t* row, uint32_t taddr) {
 // Keys from ntok on do not exist (their rows may hold anything), and a NaN
 // scale of a key that not every row sees becomes 0 here: 0 * NaN is not 0 (the
 // rows that see it get it back at the end).
+template <bool EDGE>
 __device__ __forceinline__ void value_dims(const uint8_t* vt, uint32_t taddr, int w, int lane,
                                            int ntok, int all) {
   constexpr uint32_t m = 0x0f0f0f0fu;
   const int g = lane >> 2, c = lane & 3;
   const uint8_t* codes = vt + 4 * c * kFp4Row + 16 * w + 2 * g;
   const uint8_t* scales = vt + 4 * c * kFp4Row + kHeadDim / 2 + 2 * w + (g >> 2);
-  const bool edge = all < kBlock;
-#pragma unroll 1
+#pragma unroll
   for (int half = 0; half < 2; ++half) {       // 64 keys
     uint32_t lo[16], hi[16];
 #pragma unroll
@@ -281,7 +281,7 @@ __device__ __forceinline__ void value_dims(const uint8_t* vt, uint32_t taddr, in
         u[i] = *reinterpret_cast<const uint16_t*>(codes + k0 + i * kFp4Row);
         s[i] = scales[k0 + i * kFp4Row];
       }
-      if (edge) {
+      if (EDGE) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = 64 * half + 16 * qq + 4 * c + i;
@@ -412,12 +412,12 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       mbar_init(&st.empty_bar[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&st.q_ready[i], 32);
-      mbar_init(&st.q_free[i], 128);
+      mbar_init(&st.q_ready[i], 1);
+      mbar_init(&st.q_free[i], 4);
     }
-    mbar_init(&st.k_ready, 128);
+    mbar_init(&st.k_ready, 4);
     mbar_init(&st.s_ready, 1);
-    mbar_init(&st.p_ready, 128);
+    mbar_init(&st.p_ready, 4);
     mbar_init(&st.o_ready, 1);
     fence_barrier_init();
   }
@@ -560,7 +560,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         if (__any_sync(0xffffffffu, ovf) && lane == 0)
           set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
         fence_proxy_async_smem();
-        mbar_arrive(&sh.q_ready[b]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_ready[b]);
       }
     }
     // Normally the consumers wait for every copy issued here.  After a wait
@@ -590,9 +591,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     for (int x = ttid; x < S::kOperand / 16; x += 128)
       reinterpret_cast<uint4*>(pbuf)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
-  auto release = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.empty_bar[stage]);
+  auto step = [&]() {
     if (++stage == kStages) { stage = 0; phase ^= 1u; }
   };
   Walk wk;
@@ -626,10 +625,14 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       const int ntok = sh.usable[stage] ? wk.L - j * kBlock : 0;   // keys that exist
       const int all = ntok - wk.nq + 1;                            // and that every row sees
       key_row(ring + stage * kPageBytes + ttid * kFp4Row, tk);
-      release();
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sh.k_ready);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.empty_bar[stage]);
+        mbar_arrive(&sh.k_ready);
+      }
+      step();
       // ---- V -> TMEM, once the last P V has read its predecessor
       if (j > wk.j0) {
         mbar_wait(&sh.o_ready, o_phase, ws.hdr);
@@ -638,7 +641,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       }
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const uint8_t* vt = ring + stage * kPageBytes;
-      value_dims(vt, tv, w, lane, ntok, all);
+      if (all >= kBlock) value_dims<false>(vt, tv, w, lane, ntok, all);
+      else value_dims<true>(vt, tv, w, lane, ntok, all);
       if (all < kBlock) {
         if (ttid >= all && ttid < ntok) {      // NaN scales that only later tokens see
           unsigned bad = 0;
@@ -649,7 +653,9 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
               if (ttid < all + sh.tok[n]) atomicOr(&sh.nan[n], bad);
         }
       }
-      release();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty_bar[stage]);
+      step();
       // ---- softmax of S^T: 8 keys (16 hf + g, + 8) of rows 8 i + 2 c + {0, 1}
       mbar_wait(&sh.s_ready, ph, ws.hdr);
       ph ^= 1u;
@@ -744,7 +750,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sh.p_ready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_ready);
     }
 
     // ---- the segment's result: whole rows, or a partial
@@ -811,7 +818,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     if (8 * NG == kN)                          // P rows are refilled; Q goes to the loader
       fence_proxy_async_smem();
     named_bar_sync(bar, 128);                  // red, ref, tok, nan and P are free again
-    mbar_arrive(&sh.q_free[seg & 1]);
+    if (lane == 0) mbar_arrive(&sh.q_free[seg & 1]);
     ++seg;
   }
   if (ttid == 0) a.split[vid] = split;
