@@ -128,7 +128,13 @@ def _check(fn: str, status: int, detail: str = ""):
         raise MsaError(fn, status, detail)
 
 
+# the current stream's handle without building a Stream object (2.9 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
 
@@ -378,28 +384,90 @@ def cache_write(cfg, ws, k, v, idx_k, k_pages, v_pages, idx_k_pages, out_cache_l
         _stream(stream)))
 
 
-def _need_rows(t, name, T, heads, width):
-    """A projection's rows [>= T, heads, width] bf16: heads contiguous, tokens
-    at any stride that is a multiple of 8.  Returns that stride."""
+class _Layout:
+    """What a config asks of the tensors of a step, taken from it once."""
+
+    def __init__(self, cfg):
+        self.T = max_tokens(cfg)
+        self.heads = (cfg.num_q_heads, cfg.num_kv_heads)
+        self.q_tail = (cfg.num_q_heads, cfg.head_dim)
+        self.kv_tail = (cfg.num_kv_heads, cfg.head_dim)
+        self.idx_tail = (cfg.num_kv_heads, cfg.index_dim)
+        self.lse_tail = (cfg.num_q_heads,)
+        self.pages = cfg.num_pages
+        if cfg.kv_dtype == MSA_KV_NVFP4:    # K and V slots per head, 72-byte rows
+            self.pool_tail = (2 * cfg.num_kv_heads, cfg.block_size,
+                              cfg.head_dim // 2 + cfg.head_dim // 16)
+        else:
+            self.pool_tail = (cfg.num_kv_heads, cfg.block_size, cfg.head_dim)
+        self.idx_pool_tail = (cfg.num_kv_heads, cfg.block_size, cfg.index_dim)
+        self.kv_dtypes = _kv_dtypes(cfg)
+        self.ws_bytes = workspace_bytes(cfg)
+        self.dense_scratch = lib().msa_dense_decode_scratch_bytes(ctypes.byref(cfg))
+
+
+_LAYOUTS = {}
+_BF16, _F32, _I64, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int64,), (torch.uint8,)
+
+
+def _layout(cfg) -> _Layout:
+    key = bytes(cfg)
+    v = _LAYOUTS.get(key)
+    if v is None:
+        v = _LAYOUTS[key] = _Layout(cfg)
+    return v
+
+
+def _device_of(t, name) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    return t.get_device()
+
+
+def _expect(t, name, dtypes, rows, tail, dev) -> int:
+    """The pointer of a contiguous tensor [>= rows, *tail] of one of `dtypes`
+    on device `dev`; ValueError otherwise (the reason by _need)."""
+    if isinstance(t, torch.Tensor):
+        s = t.shape
+        if (t.dtype in dtypes and len(s) and s[0] >= rows and s[1:] == tail
+                and t.is_contiguous() and t.get_device() == dev):
+            return t.data_ptr()
+    _need(t, name, dtypes, len(tail) + 1, rows, tail)
+    raise ValueError(f"{name} is on another device than the step's other tensors")
+
+
+def _expect_rows(t, name, T, tail, dev):
+    """Pointer and token stride (elements) of a projection's rows [>= T, heads,
+    width] bf16: heads contiguous, tokens at any stride that is a multiple
+    of 8."""
+    heads, width = tail
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    s = t.shape
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, the config needs "
-                         f"[{T}, {heads}, {width}]")
-    if t.shape[0] < T:
-        raise ValueError(f"{name} has {t.shape[0]} rows on dim 0, the config needs {T}")
+    if s[1:] != tail or s[0] < T:
+        raise ValueError(f"{name} has shape {tuple(s)}, the config needs "
+                         f"[>= {T}, {heads}, {width}]")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the step's other tensors")
     tok, hd, el = t.stride()
-    if el != 1 or (heads > 1 and hd != width) or (T > 1 and tok % 8) or t.data_ptr() % 16:
+    ptr = t.data_ptr()
+    if el != 1 or (heads > 1 and hd != width) or (T > 1 and tok % 8) or ptr % 16:
         raise ValueError(f"{name}: a token's heads must be contiguous, 16-byte aligned, at a "
                          f"stride that is a multiple of 8 elements")
-    return tok if T > 1 else heads * width
+    return ptr, (tok if T > 1 else heads * width)
 
 
-def _need_table(t, name):
-    _need(t, name, torch.float32, 2)
-    return t.shape[0], t.shape[1]
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current, on `stream` or its current
+    stream."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on device {stream.device.index}, the tensors on {dev}")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return fn(*args, _stream(stream))
+    return fn(*args, _stream(stream))
 
 
 def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, k_pages, v_pages,
@@ -413,42 +481,50 @@ def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, 
     fp32: cosines, then sines; idx_cos_sin the index heads' own table, None =
     cos_sin.  q_out, idx_q_out: the rotated queries, contiguous; each may be its
     input.  positions: [T] int64, None = the plan's."""
-    _need_ws(cfg, ws)
-    T, hq, hkv, d = max_tokens(cfg), cfg.num_q_heads, cfg.num_kv_heads, cfg.index_dim
+    y = _layout(cfg)
+    dev, T = _device_of(q, "q"), y.T
     r = MsaRope()
-    r.q_stride = _need_rows(q, "q", T, hq, cfg.head_dim)
-    r.k_stride = _need_rows(k, "k", T, hkv, cfg.head_dim)
-    r.v_stride = _need_rows(v, "v", T, hkv, cfg.head_dim)
-    r.num_positions, r.rotary_dim = _need_table(cos_sin, "cos_sin")
-    r.cos_sin, r.interleaved = cos_sin.data_ptr(), bool(interleaved)
-    _need_tokens(cfg, T, q=q_out)
+    p_ws = _expect(ws, "ws", _U8, y.ws_bytes, (), dev)
+    p_q, r.q_stride = _expect_rows(q, "q", T, y.q_tail, dev)
+    p_k, r.k_stride = _expect_rows(k, "k", T, y.kv_tail, dev)
+    p_v, r.v_stride = _expect_rows(v, "v", T, y.kv_tail, dev)
+    p_qo = _expect(q_out, "q_out", _BF16, T, y.q_tail, dev)
+    p_kp = _expect(k_pages, "k_pages", y.kv_dtypes, y.pages, y.pool_tail, dev)
+    p_vp = _expect(v_pages, "v_pages", y.kv_dtypes, y.pages, y.pool_tail, dev)
+    rows, width = _table_shape(cos_sin, "cos_sin")
+    r.cos_sin = _expect(cos_sin, "cos_sin", _F32, 1, (width,), dev)
+    r.rotary_dim = r.idx_rotary_dim = width
+    r.interleaved = 1 if interleaved else 0
+    p_iq = p_ik = p_iv = p_iqo = p_ikp = p_ivp = p_pos = p_loc = None
     if idx_q is not None:
-        r.idx_q_stride = _need_rows(idx_q, "idx_q", T, hkv, d)
-        _need_tokens(cfg, T, idx_q=idx_q_out)
+        p_iq, r.idx_q_stride = _expect_rows(idx_q, "idx_q", T, y.idx_tail, dev)
+        p_iqo = _expect(idx_q_out, "idx_q_out", _BF16, T, y.idx_tail, dev)
     if idx_k is not None:
-        r.idx_k_stride = _need_rows(idx_k, "idx_k", T, hkv, d)
-        _need_pools(cfg, idx_k_pages=idx_k_pages)
-        _need(idx_k_pages, "idx_k_pages")
+        p_ik, r.idx_k_stride = _expect_rows(idx_k, "idx_k", T, y.idx_tail, dev)
+        p_ikp = _expect(idx_k_pages, "idx_k_pages", _BF16, y.pages, y.idx_pool_tail, dev)
     if idx_v is not None:
-        r.idx_v_stride = _need_rows(idx_v, "idx_v", T, hkv, d)
-        _need(idx_v_pages, "idx_v_pages", torch.bfloat16, 4, cfg.num_pages,
-              (hkv, cfg.block_size, d))
+        p_iv, r.idx_v_stride = _expect_rows(idx_v, "idx_v", T, y.idx_tail, dev)
+        p_ivp = _expect(idx_v_pages, "idx_v_pages", _BF16, y.pages, y.idx_pool_tail, dev)
     if idx_cos_sin is not None:
-        n, r.idx_rotary_dim = _need_table(idx_cos_sin, "idx_cos_sin")
-        r.num_positions = min(r.num_positions, n)
-        r.idx_cos_sin = idx_cos_sin.data_ptr()
-    else:
-        r.idx_rotary_dim = r.rotary_dim
-    _need_pools(cfg, k_pages, v_pages)
+        n, r.idx_rotary_dim = _table_shape(idx_cos_sin, "idx_cos_sin")
+        r.idx_cos_sin = _expect(idx_cos_sin, "idx_cos_sin", _F32, 1, (r.idx_rotary_dim,), dev)
+        rows = min(rows, n)
+    r.num_positions = rows
     if positions is not None:
-        _need(positions, "positions", torch.int64, 1, T)
+        p_pos = _expect(positions, "positions", _I64, T, (), dev)
     if out_cache_loc is not None:
-        _need(out_cache_loc, "out_cache_loc", torch.int64, 1, T)
-    _check("msa_rope_cache_write", lib().msa_rope_cache_write(
-        ctypes.byref(cfg), _ptr(ws), ctypes.byref(r), _ptr(q), _ptr(k), _ptr(v), _ptr(idx_q),
-        _ptr(idx_k), _ptr(idx_v), _ptr(positions), _ptr(out_cache_loc), _ptr(q_out),
-        _ptr(idx_q_out), _ptr(k_pages), _ptr(v_pages), _ptr(idx_k_pages), _ptr(idx_v_pages),
-        _stream(stream)))
+        p_loc = _expect(out_cache_loc, "out_cache_loc", _I64, T, (), dev)
+    st = _call(lib().msa_rope_cache_write, dev, stream, ctypes.byref(cfg), p_ws, ctypes.byref(r),
+               p_q, p_k, p_v, p_iq, p_ik, p_iv, p_pos, p_loc, p_qo, p_iqo, p_kp, p_vp, p_ikp,
+               p_ivp)
+    if st:
+        _check("msa_rope_cache_write", st)
+
+
+def _table_shape(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a [positions, rotary_dim] tensor")
+    return t.shape
 
 
 def index_attention_scratch_bytes(cfg) -> int:
@@ -575,16 +651,20 @@ def dense_decode(cfg, ws, q, k_pages, v_pages, scratch, out, lse, stream=None):
     NVFP4 pools (msa_dense_decode): the full-attention layers of a model, after
     plan() and the cache write of the step; no combine() follows.  scratch of
     dense_decode_scratch_bytes(cfg) bytes."""
-    _need_ws(cfg, ws)
-    _need_tokens(cfg, max_tokens(cfg), q=q, out=out, lse=lse)
-    _need_pools(cfg, k_pages, v_pages)
-    _need(scratch, "scratch", torch.uint8)
-    n = dense_decode_scratch_bytes(cfg)
-    if scratch.numel() < n:
-        raise ValueError(f"scratch has {scratch.numel()} bytes, the config needs {n}")
-    _check("msa_dense_decode", lib().msa_dense_decode(
-        ctypes.byref(cfg), _ptr(ws), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(scratch),
-        _ptr(out), _ptr(lse), _stream(stream)))
+    y = _layout(cfg)
+    dev, T = _device_of(q, "q"), y.T
+    if y.dense_scratch == 0:
+        dense_decode_scratch_bytes(cfg)                  # raises what the library says
+    st = _call(lib().msa_dense_decode, dev, stream, ctypes.byref(cfg),
+               _expect(ws, "ws", _U8, y.ws_bytes, (), dev),
+               _expect(q, "q", _BF16, T, y.q_tail, dev),
+               _expect(k_pages, "k_pages", y.kv_dtypes, y.pages, y.pool_tail, dev),
+               _expect(v_pages, "v_pages", y.kv_dtypes, y.pages, y.pool_tail, dev),
+               _expect(scratch, "scratch", _U8, y.dense_scratch, (), dev),
+               _expect(out, "out", _BF16, T, y.q_tail, dev),
+               _expect(lse, "lse", _F32, T, y.lse_tail, dev))
+    if st:
+        _check("msa_dense_decode", st)
 
 
 def combine(cfg, ws, out, lse, stream=None):
