@@ -20,31 +20,52 @@
 // Work split.  Eight threads own a row (a head of a token), each two 16-byte
 // chunks: the two halves of its eight pairs, so a rotation needs no exchange
 // between threads, and rows may be rotated in place.  Dims that are only
-// copied, and interleaved pairs, give a thread two neighbouring chunks.  A CTA
-// takes 32 rows of one token, so the smallest steps spread over the machine
-// and every load of the step is in flight at once.
+// copied, and interleaved pairs, give a thread two neighbouring chunks.  The
+// rows of all tokens are one list (q | k | v | idx_q | idx_k | idx_v per
+// token), 32 of it to a CTA whatever the head counts are.  One row a thread:
+// two, three or four in flight per thread were slower (fewer threads fit).
 #include "kv_quant.cuh"
 
 namespace msa {
 namespace {
 
 constexpr int kRowThreads = 8;
-constexpr int kRowsPerCta = 32;
+constexpr int kSlots = 32;     // threads / kRowThreads of a CTA
+constexpr int kKinds = 6;      // q, k, v, idx_q, idx_k, idx_v
+
+// x / d for x < 2^31 by one multiplication.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d_) : d(d_), shift(0) {
+    while ((1u << shift) < d) ++shift;         // ceil(log2 d)
+    mul = (uint32_t)((((uint64_t)1 << (31 + shift)) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    return (uint32_t)(((uint64_t)x * mul) >> (31 + shift));
+  }
+};
+
+// One kind of row: where it comes from, its rotation, where it goes.
+struct Kind {
+  const __nv_bfloat16* src;    // null: the step has none
+  int64_t stride;              // elements between tokens
+  const float* cs;             // [num_positions, rot]: cosines, then sines
+  uint8_t* dst;                // rows by token, or a pool
+  int width, rot;
+  int pool;                    // kv dtype of the pool, -1 = rows by token (bf16)
+  int fp4_slot;                // NVFP4: 0 = keys, 1 = values
+  float scale;
+};
 
 struct RopeArgs {
-  int Hq, Hkv, d, max_blocks, kv, interleaved;
-  int rot, idx_rot;              // rotary dims of the heads and of the index heads
+  FastDiv R;                   // rows a token
+  uint32_t items;              // tokens * rows
+  int Hq, Hkv, max_blocks, fp4, interleaved;
   int64_t num_positions, pool_slots;
-  int64_t qs, ks, vs, iqs, iks, ivs;    // elements between tokens
-  float k_scale, v_scale;
-  const float* cs;               // [num_positions, rot]: cosines, then sines
-  const float* idx_cs;
-  const int64_t* positions;      // or null: the plan's
-  const int64_t* loc;            // or null: the plan's
-  const __nv_bfloat16 *q, *k, *v, *iq, *ik, *iv;
-  __nv_bfloat16 *q_out, *iq_out;
-  uint8_t *k_pages, *v_pages;    // may be one allocation (NVFP4)
-  __nv_bfloat16 *ik_pages, *iv_pages;
+  const int64_t* positions;    // or null: the plan's
+  const int64_t* loc;          // or null: the plan's
+  Kind kinds[kKinds];
 };
 
 // Not the non-coherent path: q_out may be q.
@@ -62,81 +83,68 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16(f[6], f[7]));
 }
 
-__global__ void __launch_bounds__(kRowsPerCta* kRowThreads)
-rope_write_kernel(WsView ws, RopeArgs a) {
-  const int t = blockIdx.x;
+__global__ void __launch_bounds__(kSlots* kRowThreads, 5)
+rope_write_kernel(WsView ws, const __grid_constant__ RopeArgs a) {
   const int sub = threadIdx.x & (kRowThreads - 1);
-  int row = blockIdx.y * kRowsPerCta + (threadIdx.x >> 3);
   griddep_launch_dependents();
-  griddep_wait();            // the plan of this step, and readers of the last one
-  if (t >= ws.hdr->num_tokens) return;
-  const int r = ws.tok_req[t];
-  if (r < 0) return;         // idle request: nothing to rotate or store
-  const int plan_pos = ws.tok_pos[t];
-
-  // the row's kind, head and source: q | k | v | idx_q | idx_k | idx_v
-  enum { kQ, kK, kV, kIq, kIk, kIv, kNone };
-  int kind = kNone, h = row;
-  const __nv_bfloat16* src = nullptr;
-  if (h < a.Hq) {
-    kind = kQ;
-    src = a.q + t * a.qs;
-  } else {
+  const uint32_t item = blockIdx.x * kSlots + (threadIdx.x >> 3);
+  const int t = (int)a.R(item);
+  int h = (int)(item - (uint32_t)t * a.R.d), kind = 0, heads = a.Hq;
+  if (h >= a.Hq) {
     h -= a.Hq;
-    const int n = h / a.Hkv;
-    h -= n * a.Hkv;
-    if (n == 0) kind = kK, src = a.k + t * a.ks;
-    else if (n == 1) kind = kV, src = a.v + t * a.vs;
-    else if (n == 2 && a.iq != nullptr) kind = kIq, src = a.iq + t * a.iqs;
-    else if (n == 3 && a.ik != nullptr) kind = kIk, src = a.ik + t * a.iks;
-    else if (n == 4 && a.iv != nullptr) kind = kIv, src = a.iv + t * a.ivs;
+    heads = a.Hkv;
+    kind = 1 + (h >= a.Hkv) + (h >= 2 * a.Hkv) + (h >= 3 * a.Hkv) + (h >= 4 * a.Hkv);
+    h -= (kind - 1) * a.Hkv;
   }
-  const bool idx = kind >= kIq;
-  const int width = idx ? a.d : kHeadDim;
-  const bool on = kind != kNone && sub < width / 16;
-  const int rot = (kind == kV || kind == kIv) ? 0 : (idx ? a.idx_rot : a.rot);
-  const bool turn = sub < rot / 16;
-  const bool split = turn && !a.interleaved;
+  const Kind& kd = a.kinds[kind];
+  const int width = kd.width, rot = kd.rot;
+  const bool turn = sub < rot / 16, split = turn && !a.interleaved;
   // this thread's two chunks of eight elements
   const int ca = split ? sub : 2 * sub, cb = split ? sub + rot / 16 : 2 * sub + 1;
-
-  float x[8], y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
-  const int64_t pos = a.positions != nullptr ? a.positions[t] : plan_pos;
-  if (pos < 0 || pos >= a.num_positions) {     // beyond the table: the token is skipped
-    if (threadIdx.x == 0) set_error(ws.hdr, MSA_DEVERR_POSITION);
-    return;
+  bool live = item < a.items && kd.src != nullptr && sub < width / 16;
+  griddep_wait();              // the projection, the plan, readers of the last step
+  uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
+  int req = -1, plan_pos = 0;
+  int64_t pos = 0, slot = 0;
+  if (live) {
+    const __nv_bfloat16* src = kd.src + t * kd.stride + h * width;
+    xa = ld_once(src + 8 * ca);
+    xb = ld_once(src + 8 * cb);
+    req = ws.tok_req[t];       // -1: idle, or behind the step's tokens
+    plan_pos = ws.tok_pos[t];
+    pos = a.positions != nullptr ? a.positions[t] : plan_pos;
+    if (a.loc != nullptr && kd.pool >= 0) slot = a.loc[t];
+    live = req >= 0;
+    if (live && (uint64_t)pos >= (uint64_t)a.num_positions) {     // beyond the table: skipped
+      set_error(ws.hdr, MSA_DEVERR_POSITION);
+      live = false;
+    }
   }
-  if (on) {
-    src += h * width;
-    const uint4 wa = ld_once(src + 8 * ca), wb = ld_once(src + 8 * cb);
-    bf16x8_to_f32(wa, x);
-    bf16x8_to_f32(wb, y);
-    if (turn) {
-      const float4* tab =
-          reinterpret_cast<const float4*>((idx ? a.idx_cs : a.cs) + pos * rot + 8 * sub);
-      const float4 c0 = __ldg(tab), c1 = __ldg(tab + 1);
-      const float4 s0 = __ldg(tab + rot / 8), s1 = __ldg(tab + rot / 8 + 1);
-      const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-      const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-      if (split) {
+  float x[8], y[8];
+  bf16x8_to_f32(xa, x);
+  bf16x8_to_f32(xb, y);
+  if (live && turn) {
+    const float4* tab = reinterpret_cast<const float4*>(kd.cs + pos * rot + 8 * sub);
+    const float4 c0 = __ldg(tab), c1 = __ldg(tab + 1);
+    const float4 s0 = __ldg(tab + rot / 8), s1 = __ldg(tab + rot / 8 + 1);
+    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    if (split) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float u = x[i], w = y[i];
-          x[i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
-          y[i] = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
-        }
-      } else {
+      for (int i = 0; i < 8; ++i) {
+        const float p = x[i], q = y[i];
+        x[i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(q, s[i]));
+        y[i] = __fadd_rn(__fmul_rn(q, c[i]), __fmul_rn(p, s[i]));
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = x[2 * i], w = x[2 * i + 1];
-          x[2 * i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
-          x[2 * i + 1] = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
-          const float u2 = y[2 * i], w2 = y[2 * i + 1];
-          y[2 * i] = __fsub_rn(__fmul_rn(u2, c[i + 4]), __fmul_rn(w2, s[i + 4]));
-          y[2 * i + 1] = __fadd_rn(__fmul_rn(w2, c[i + 4]), __fmul_rn(u2, s[i + 4]));
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float p = x[2 * i], q = x[2 * i + 1];
+        x[2 * i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(q, s[i]));
+        x[2 * i + 1] = __fadd_rn(__fmul_rn(q, c[i]), __fmul_rn(p, s[i]));
+        const float p2 = y[2 * i], q2 = y[2 * i + 1];
+        y[2 * i] = __fsub_rn(__fmul_rn(p2, c[i + 4]), __fmul_rn(q2, s[i + 4]));
+        y[2 * i + 1] = __fadd_rn(__fmul_rn(q2, c[i + 4]), __fmul_rn(p2, s[i + 4]));
       }
     }
   }
@@ -144,74 +152,57 @@ rope_write_kernel(WsView ws, RopeArgs a) {
   // neighbour's chunks when the halves are split (rot / 16 is even), else both
   // chunks are one block
   float ma = 0.f, mb = 0.f;
-  if (a.kv == MSA_KV_NVFP4) {
+  if (a.fp4) {                 // all lanes: the shuffles are warp-wide
     const float pa = amax8(x), pb = amax8(y);
     const float na = __shfl_xor_sync(0xffffffffu, pa, 1);
     const float nb = __shfl_xor_sync(0xffffffffu, pb, 1);
     ma = split ? fmaxf(pa, na) : fmaxf(pa, pb);
     mb = split ? fmaxf(pb, nb) : ma;
   }
-  if (!on) return;
-
-  if (kind == kQ) {
-    __nv_bfloat16* dst = a.q_out + ((int64_t)t * a.Hq + h) * kHeadDim;
-    reinterpret_cast<uint4*>(dst)[ca] = pack8(x);
-    reinterpret_cast<uint4*>(dst)[cb] = pack8(y);
-    return;
-  }
-  if (kind == kIq) {
-    __nv_bfloat16* dst = a.iq_out + ((int64_t)t * a.Hkv + h) * a.d;
-    reinterpret_cast<uint4*>(dst)[ca] = pack8(x);
-    reinterpret_cast<uint4*>(dst)[cb] = pack8(y);
-    return;
-  }
-  int64_t slot;
-  if (a.loc != nullptr) {
-    slot = a.loc[t];
+  if (!live) return;
+  int64_t line;                // destination row
+  if (kd.pool < 0) {
+    line = (int64_t)t * heads + h;
   } else {
-    const int page = ws.block_table[(int64_t)r * a.max_blocks + plan_pos / kBlock];
-    slot = page < 0 ? -1 : (int64_t)page * kBlock + plan_pos % kBlock;
+    if (a.loc == nullptr) {
+      const int page = ws.block_table[(int64_t)req * a.max_blocks + plan_pos / kBlock];
+      slot = page < 0 ? -1 : (int64_t)page * kBlock + plan_pos % kBlock;
+    }
+    if ((uint64_t)slot >= (uint64_t)a.pool_slots) {
+      set_error(ws.hdr, MSA_DEVERR_PAGE_RANGE);
+      return;
+    }
+    int64_t head = (slot >> 7) * heads + h;
+    if (kd.pool == MSA_KV_NVFP4) head = 2 * head + kd.fp4_slot;   // a slot each for K and V
+    line = head * kBlock + (slot & (kBlock - 1));
   }
-  if (slot < 0 || slot >= a.pool_slots) {
-    if (sub == 0) set_error(ws.hdr, MSA_DEVERR_PAGE_RANGE);
-    return;
-  }
-  const int64_t line = (slot / kBlock * a.Hkv + h) * kBlock + slot % kBlock;
-  if (idx) {
-    uint4* dst = reinterpret_cast<uint4*>((kind == kIk ? a.ik_pages : a.iv_pages) + line * a.d);
+  static_assert(kBlock == 128, "slot arithmetic");
+  if (kd.pool == MSA_KV_NVFP4) {
+    uint8_t* dst = kd.dst + line * kFp4Row;
+    uint8_t sa, sb;
+    const uint32_t wa = nvfp4_codes8(x, ma, kd.scale, sa), wb = nvfp4_codes8(y, mb, kd.scale, sb);
+    reinterpret_cast<uint32_t*>(dst)[ca] = wa;
+    reinterpret_cast<uint32_t*>(dst)[cb] = wb;
+    if (!split) {
+      dst[kHeadDim / 2 + sub] = sa;
+    } else if ((sub & 1) == 0) {
+      dst[kHeadDim / 2 + ca / 2] = sa;
+      dst[kHeadDim / 2 + cb / 2] = sb;
+    }
+  } else if (kd.pool == MSA_KV_FP8_E4M3) {
+    const float g = kd.scale;
+    uint2* dst = reinterpret_cast<uint2*>(kd.dst + line * width);
+    dst[ca] = make_uint2(e4m3x2_of(x[0], x[1], g) | e4m3x2_of(x[2], x[3], g) << 16,
+                         e4m3x2_of(x[4], x[5], g) | e4m3x2_of(x[6], x[7], g) << 16);
+    dst[cb] = make_uint2(e4m3x2_of(y[0], y[1], g) | e4m3x2_of(y[2], y[3], g) << 16,
+                         e4m3x2_of(y[4], y[5], g) | e4m3x2_of(y[6], y[7], g) << 16);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(kd.dst + line * (2 * width));
     dst[ca] = pack8(x);
     dst[cb] = pack8(y);
-  } else {
-    const int half = kind == kV;
-    uint8_t* pool = half ? a.v_pages : a.k_pages;
-    const float g = half ? a.v_scale : a.k_scale;
-    if (a.kv == MSA_KV_BF16) {
-      uint4* dst = reinterpret_cast<uint4*>(pool) + line * 16;
-      dst[ca] = pack8(x);
-      dst[cb] = pack8(y);
-    } else if (a.kv == MSA_KV_NVFP4) {
-      const int64_t l4 = ((slot / kBlock * a.Hkv + h) * 2 + half) * kBlock + slot % kBlock;
-      uint8_t* dst = pool + l4 * kFp4Row;
-      uint8_t sa, sb;
-      const uint32_t wa = nvfp4_codes8(x, ma, g, sa), wb = nvfp4_codes8(y, mb, g, sb);
-      reinterpret_cast<uint32_t*>(dst)[ca] = wa;
-      reinterpret_cast<uint32_t*>(dst)[cb] = wb;
-      if (!split) {
-        dst[kHeadDim / 2 + sub] = sa;
-      } else if ((sub & 1) == 0) {
-        dst[kHeadDim / 2 + ca / 2] = sa;
-        dst[kHeadDim / 2 + cb / 2] = sb;
-      }
-    } else {
-      uint2* dst = reinterpret_cast<uint2*>(pool) + line * 16;
-      dst[ca] = make_uint2(e4m3x2_of(x[0], x[1], g) | e4m3x2_of(x[2], x[3], g) << 16,
-                           e4m3x2_of(x[4], x[5], g) | e4m3x2_of(x[6], x[7], g) << 16);
-      dst[cb] = make_uint2(e4m3x2_of(y[0], y[1], g) | e4m3x2_of(y[2], y[3], g) << 16,
-                           e4m3x2_of(y[4], y[5], g) | e4m3x2_of(y[6], y[7], g) << 16);
-    }
   }
-  // the step's later kernels read these rows with TMA (async proxy)
-  asm volatile("fence.proxy.async.global;" ::: "memory");
+  // the step's later kernels read the pools with TMA (async proxy)
+  if (kd.pool >= 0) asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
 bool rows_ok(const void* p, int64_t stride, int64_t row) {
@@ -261,46 +252,37 @@ extern "C" msa_status msa_rope_cache_write(const msa_config* cfg, void* ws, cons
     return MSA_ERR_INVALID_ARG;
   const int64_t T = max_tokens_of(*cfg);
   if (T <= 0) return MSA_OK;
+  const int64_t kinds = idx_v ? 5 : (idx_k ? 4 : (idx_q ? 3 : 2));   // row groups past q
+  const int64_t rows = Hq + kinds * Hkv;
+  if (T * rows >= (int64_t)1 << 31) return MSA_ERR_UNSUPPORTED;      // rows count in 31 bits
+  const bool scaled = cfg->kv_dtype != MSA_KV_BF16;
+  const int D = cfg->head_dim, di = cfg->index_dim, kv = cfg->kv_dtype;
+  auto kind = [](const void* src, int64_t stride, const float* cs, void* dst, int width, int rot,
+                 int pool, int fp4_slot, float scale) {
+    return Kind{(const __nv_bfloat16*)src, stride, cs, (uint8_t*)dst, width, rot, pool, fp4_slot,
+                scale};
+  };
   RopeArgs a;
+  a.R = FastDiv((uint32_t)rows);
+  a.items = (uint32_t)(T * rows);
   a.Hq = cfg->num_q_heads;
   a.Hkv = cfg->num_kv_heads;
-  a.d = cfg->index_dim;
   a.max_blocks = cfg->max_blocks_per_req;
-  a.kv = cfg->kv_dtype;
+  a.fp4 = kv == MSA_KV_NVFP4;
   a.interleaved = rope->interleaved != 0;
-  a.rot = rot;
-  a.idx_rot = idx_rot;
   a.num_positions = rope->num_positions;
   a.pool_slots = (int64_t)cfg->num_pages * kBlock;
-  a.qs = rope->q_stride;
-  a.ks = rope->k_stride;
-  a.vs = rope->v_stride;
-  a.iqs = rope->idx_q_stride;
-  a.iks = rope->idx_k_stride;
-  a.ivs = rope->idx_v_stride;
-  const bool scaled = cfg->kv_dtype != MSA_KV_BF16;
-  a.k_scale = scaled ? cfg->k_scale : 1.f;
-  a.v_scale = scaled ? cfg->v_scale : 1.f;
-  a.cs = rope->cos_sin;
-  a.idx_cs = idx_cs;
   a.positions = positions;
   a.loc = out_cache_loc;
-  a.q = (const __nv_bfloat16*)q;
-  a.k = (const __nv_bfloat16*)k;
-  a.v = (const __nv_bfloat16*)v;
-  a.iq = (const __nv_bfloat16*)idx_q;
-  a.ik = (const __nv_bfloat16*)idx_k;
-  a.iv = (const __nv_bfloat16*)idx_v;
-  a.q_out = (__nv_bfloat16*)q_out;
-  a.iq_out = (__nv_bfloat16*)idx_q_out;
-  a.k_pages = (uint8_t*)k_pages;
-  a.v_pages = (uint8_t*)v_pages;
-  a.ik_pages = (__nv_bfloat16*)idx_k_pages;
-  a.iv_pages = (__nv_bfloat16*)idx_v_pages;
-  const int64_t kinds = idx_v ? 5 : (idx_k ? 4 : (idx_q ? 3 : 2));   // row groups past q
-  const int64_t chunks = (Hq + kinds * Hkv + kRowsPerCta - 1) / kRowsPerCta;
-  if (chunks > 65535) return MSA_ERR_UNSUPPORTED;
-  return launch_pdl(rope_write_kernel, dim3((unsigned)T, (unsigned)chunks),
-                    dim3(kRowsPerCta * kRowThreads), 0, (cudaStream_t)stream,
-                    view_of(*cfg, ws), a);
+  a.kinds[0] = kind(q, rope->q_stride, rope->cos_sin, q_out, D, rot, -1, 0, 1.f);
+  a.kinds[1] = kind(k, rope->k_stride, rope->cos_sin, k_pages, D, rot, kv, 0,
+                    scaled ? cfg->k_scale : 1.f);
+  a.kinds[2] = kind(v, rope->v_stride, nullptr, v_pages, D, 0, kv, 1, scaled ? cfg->v_scale : 1.f);
+  a.kinds[3] = kind(idx_q, rope->idx_q_stride, idx_cs, idx_q_out, di, idx_rot, -1, 0, 1.f);
+  a.kinds[4] = kind(idx_k, rope->idx_k_stride, idx_cs, idx_k_pages, di, idx_rot, MSA_KV_BF16, 0,
+                    1.f);
+  a.kinds[5] = kind(idx_v, rope->idx_v_stride, nullptr, idx_v_pages, di, 0, MSA_KV_BF16, 0, 1.f);
+  const unsigned grid = (a.items + kSlots - 1) / kSlots;
+  return launch_pdl(rope_write_kernel, dim3(grid), dim3(kSlots * kRowThreads), 0,
+                    (cudaStream_t)stream, view_of(*cfg, ws), a);
 }
