@@ -35,7 +35,7 @@ namespace msa {
 namespace {
 
 constexpr int kMaxRows = 64;                   // query rows (tokens x group) of a KV head
-constexpr int kTeamsMax = 512;                 // partial slots: two per team
+constexpr int kTeamsMax = 640;                 // partial slots: two per team
 constexpr int kPageBytes = kBlock * kFp4Row;   // one K or V slot, 9216 bytes
 constexpr float kBias = 7.f;                   // exponent offset of the probabilities
 constexpr float kSlack = 8.f;                  // 2^(kBias + kSlack) is below fp16's largest
@@ -231,82 +231,77 @@ __device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
 }
 
 // ---------------------------------------------------------------- dequantisation
-// K: this thread's key row (72 bytes) -> its TMEM lane, 64 columns of two dims.
-__device__ __forceinline__ void key_row(const uint8_t* row, uint32_t taddr) {
-  const uint2 sb = *reinterpret_cast<const uint2*>(row + kHeadDim / 2);
+// K: 64 dims (half 0 or 1) of this thread's key row (72 bytes) -> its TMEM
+// lane, 32 columns of two dims.
+__device__ __forceinline__ void key_half(const uint8_t* row, uint32_t taddr, int half) {
+  const uint32_t s4 = *reinterpret_cast<const uint32_t*>(row + kHeadDim / 2 + 4 * half);
+  const uint32_t sp[2] = {e4m3x2_to_f16x2((uint16_t)(s4 & 0xffffu)),
+                          e4m3x2_to_f16x2((uint16_t)(s4 >> 16))};
+  uint32_t h[32];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {       // 64 dims, 4 blocks
-    const uint32_t s4 = half ? sb.y : sb.x;
-    const uint32_t sp[2] = {e4m3x2_to_f16x2((uint16_t)(s4 & 0xffffu)),
-                            e4m3x2_to_f16x2((uint16_t)(s4 >> 16))};
-    uint32_t h[32];
+  for (int b = 0; b < 4; ++b) {
+    const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * half + 8 * b);
+    const uint32_t sc = __byte_perm(sp[b >> 1], 0u, b & 1 ? 0x3232u : 0x1010u);
+    uint32_t lo[4], hi[4];
+    e2m1x8_to_f16x2(x.x, lo);
+    e2m1x8_to_f16x2(x.y, hi);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * half + 8 * b);
-      const uint32_t sc = __byte_perm(sp[b >> 1], 0u, b & 1 ? 0x3232u : 0x1010u);
-      uint32_t lo[4], hi[4];
-      e2m1x8_to_f16x2(x.x, lo);
-      e2m1x8_to_f16x2(x.y, hi);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[8 * b + e] = hmul2_u32(lo[e], sc);
-        h[8 * b + 4 + e] = hmul2_u32(hi[e], sc);
-      }
+    for (int e = 0; e < 4; ++e) {
+      h[8 * b + e] = hmul2_u32(lo[e], sc);
+      h[8 * b + 4 + e] = hmul2_u32(hi[e], sc);
     }
-    tmem_st32(taddr + 32 * half, h);
   }
+  tmem_st32(taddr, h);
 }
 
-// V, transposed: this warp's dims 32 w .. 32 w + 31 of the tile's 128 keys ->
-// TMEM lanes 32 w + 8 i + g = dim 32 w + 4 g + i, 64 columns of two keys.
+// V, transposed: this warp's dims 32 w .. 32 w + 31 of 64 keys (half 0 or 1 of
+// the tile) -> TMEM lanes 32 w + 8 i + g = dim 32 w + 4 g + i, 32 columns of
+// two keys.
 // Keys from ntok on do not exist (their rows may hold anything), and a NaN
 // scale of a key that not every row sees becomes 0 here: 0 * NaN is not 0 (the
 // rows that see it get it back at the end).
 template <bool EDGE>
-__device__ __forceinline__ void value_dims(const uint8_t* vt, uint32_t taddr, int w, int lane,
-                                           int ntok, int all) {
+__device__ __forceinline__ void value_half(const uint8_t* vt, uint32_t taddr, int half, int w,
+                                           int lane, int ntok, int all) {
   constexpr uint32_t m = 0x0f0f0f0fu;
   const int g = lane >> 2, c = lane & 3;
   const uint8_t* codes = vt + 4 * c * kFp4Row + 16 * w + 2 * g;
   const uint8_t* scales = vt + 4 * c * kFp4Row + kHeadDim / 2 + 2 * w + (g >> 2);
+  uint32_t lo[16], hi[16];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {       // 64 keys
-    uint32_t lo[16], hi[16];
+  for (int qq = 0; qq < 4; ++qq) {
+    const int k0 = (64 * half + 16 * qq) * kFp4Row;   // keys 64 half + 16 qq + 4 c + 0..3
+    uint32_t u[4], s[4];
 #pragma unroll
-    for (int qq = 0; qq < 4; ++qq) {
-      const int k0 = (64 * half + 16 * qq) * kFp4Row;   // keys 64 half + 16 qq + 4 c + 0..3
-      uint32_t u[4], s[4];
+    for (int i = 0; i < 4; ++i) {
+      u[i] = *reinterpret_cast<const uint16_t*>(codes + k0 + i * kFp4Row);
+      s[i] = scales[k0 + i * kFp4Row];
+    }
+    if (EDGE) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        u[i] = *reinterpret_cast<const uint16_t*>(codes + k0 + i * kFp4Row);
-        s[i] = scales[k0 + i * kFp4Row];
+        const int key = 64 * half + 16 * qq + 4 * c + i;
+        if (key >= ntok || (key >= all && (s[i] & 0x7f) == 0x7f)) s[i] = 0;
       }
-      if (EDGE) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = 64 * half + 16 * qq + 4 * c + i;
-          if (key >= ntok || (key >= all && (s[i] & 0x7f) == 0x7f)) s[i] = 0;
-        }
-      }
-      const uint32_t a = __byte_perm(u[0], u[2], 0x5410), b = __byte_perm(u[1], u[3], 0x5410);
-      const uint32_t even = (a & m) | ((b << 4) & ~m), odd = ((a >> 4) & m) | (b & ~m);
-      const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(s[0] | s[1] << 8));
-      const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(s[2] | s[3] << 8));
-      uint32_t e[4], o[4];                     // dims 0, 2 | 1, 3 of keys 0 1, then of 2 3
-      e2m1x8_to_f16x2(even, e);
-      e2m1x8_to_f16x2(odd, o);
-      lo[4 * qq] = hmul2_u32(e[0], s01);
-      lo[4 * qq + 1] = hmul2_u32(e[2], s23);
-      lo[4 * qq + 2] = hmul2_u32(o[0], s01);
-      lo[4 * qq + 3] = hmul2_u32(o[2], s23);
-      hi[4 * qq] = hmul2_u32(e[1], s01);
-      hi[4 * qq + 1] = hmul2_u32(e[3], s23);
-      hi[4 * qq + 2] = hmul2_u32(o[1], s01);
-      hi[4 * qq + 3] = hmul2_u32(o[3], s23);
     }
-    tmem_st_16x256_x4(taddr + 32 * half, lo);
-    tmem_st_16x256_x4(taddr + 32 * half + (16u << 16), hi);
+    const uint32_t a = __byte_perm(u[0], u[2], 0x5410), b = __byte_perm(u[1], u[3], 0x5410);
+    const uint32_t even = (a & m) | ((b << 4) & ~m), odd = ((a >> 4) & m) | (b & ~m);
+    const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(s[0] | s[1] << 8));
+    const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(s[2] | s[3] << 8));
+    uint32_t e[4], o[4];                     // dims 0, 2 | 1, 3 of keys 0 1, then of 2 3
+    e2m1x8_to_f16x2(even, e);
+    e2m1x8_to_f16x2(odd, o);
+    lo[4 * qq] = hmul2_u32(e[0], s01);
+    lo[4 * qq + 1] = hmul2_u32(e[2], s23);
+    lo[4 * qq + 2] = hmul2_u32(o[0], s01);
+    lo[4 * qq + 3] = hmul2_u32(o[2], s23);
+    hi[4 * qq] = hmul2_u32(e[1], s01);
+    hi[4 * qq + 1] = hmul2_u32(e[3], s23);
+    hi[4 * qq + 2] = hmul2_u32(o[1], s01);
+    hi[4 * qq + 3] = hmul2_u32(o[3], s23);
   }
+  tmem_st_16x256_x4(taddr, lo);
+  tmem_st_16x256_x4(taddr + (16u << 16), hi);
 }
 
 // The tiles (pages) of a range, one after the other, for a role that walks
@@ -342,20 +337,25 @@ struct Tiles {
 };
 
 // A CTA is kTeams independent teams of four consumer warps, each with its own
-// range of units, ring, TMEM columns, loader warp and MMA warp; one more warp
-// keeps the TMEM allocation.  NG: groups of 8 query rows.
+// range of units, ring, TMEM columns, loader warp and MMA warp.  NG: groups of
+// 8 query rows.
 template <int NG>
 struct Shape {
   static constexpr int kN = NG < 2 ? 16 : 8 * NG;                 // MMA N
-  static constexpr int kTeams = NG <= 2 ? 3 : 2;
+  static constexpr int kTeams = NG <= 2 ? 4 : (NG == 4 ? 3 : 2);
   static constexpr int kThreads = kTeams * 128 + 256;
-  // 640 x 96 = 384 x 128 + 256 x 48; 512 x 128 = 256 x 200 + 256 x 56
-  static constexpr int kConsumerRegs = NG <= 2 ? 128 : 200, kMiscRegs = NG <= 2 ? 48 : 56;
-  static constexpr int kCols = 128 + 2 * kN;                      // K | V | S | O
-  static constexpr int kStages = NG <= 2 ? 6 : (NG == 4 ? 8 : 6);
+  // threads x launch registers = consumers x theirs + 256 x the others':
+  // 768 x 80 = 512 x 96 + 256 x 48; 640 x 96 = 384 x 128 + 256 x 48;
+  // 512 x 128 = 256 x 200 + 256 x 56
+  static constexpr int kConsumerRegs = NG <= 2 ? 96 : (NG == 4 ? 128 : 200);
+  static constexpr int kMiscRegs = NG <= 4 ? 48 : 56;
+  // TMEM columns of a team: K (64 dims) | V | S | O
+  static constexpr int kCols = 96 + 2 * kN;
+  static constexpr int kStages = NG <= 2 ? 4 : (NG == 4 ? 5 : 6);
   static constexpr int kOperand = kN * kHeadDim * 2;              // a Q buffer, and P
   static constexpr int kTeamSmem = 3 * kOperand + kStages * kPageBytes;
   static constexpr int kSmem = kTeams * kTeamSmem;
+  static_assert(kTeams * kCols <= 512, "TMEM");
 };
 
 // Phase parity of the use number t of buffer t & 1.
@@ -368,7 +368,8 @@ struct TeamShared {
   float alpha[S::kN], ref[S::kN];              // rescaling, final references
   uint64_t full_bar[S::kStages], empty_bar[S::kStages];
   uint64_t q_ready[2], q_free[2];              // Q written by the loader; buffer free again
-  uint64_t k_ready, s_ready;   // K written; S written and K read
+  uint64_t k_ready, k_free;    // a half of K written (two a tile); the first half read
+  uint64_t s_ready;            // S written, K read
   uint64_t p_ready, o_ready;   // P and V written; O updated and P and V read
   int usable[S::kStages];      // K slots: 0 = the plan flagged the page
   int tok[S::kN];              // token of each row within the request
@@ -402,9 +403,9 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   __shared__ uint32_t tmem_base;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
-  const int extra = warp - 4 * S::kTeams;      // loaders, MMA warps, keeper
+  const int extra = warp - 4 * S::kTeams;      // loaders, then MMA warps
   const int team = extra < 0 ? warp / 4 : (extra < S::kTeams ? extra : extra - S::kTeams);
-  const bool keeper = extra == 2 * S::kTeams;  // of the TMEM allocation
+  const bool keeper = extra == S::kTeams;      // MMA warp 0 keeps the TMEM allocation
   if (tid < S::kTeams) {
     TeamShared<NG>& st = shared[tid];
     for (int i = 0; i < kStages; ++i) {
@@ -416,6 +417,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       mbar_init(&st.q_free[i], 4);
     }
     mbar_init(&st.k_ready, 4);
+    mbar_init(&st.k_free, 1);
     mbar_init(&st.s_ready, 1);
     mbar_init(&st.p_ready, 4);
     mbar_init(&st.o_ready, 1);
@@ -425,31 +427,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   griddep_wait();
   constexpr int kDone = 15;                    // named barrier: every consumer, and the keeper
   constexpr int kDoneCount = S::kTeams * 128 + 32;
-  constexpr int kAlloc = 14;                   // the same and the MMA warps
-  constexpr int kAllocCount = S::kTeams * 160 + 32;
+  constexpr int kAlloc = 14;                   // every consumer and MMA warp
+  constexpr int kAllocCount = S::kTeams * 160;
   if (extra >= 0) regs_down<S::kMiscRegs>();
-  if (extra >= 2 * S::kTeams) {
-    if (!keeper) return;
-    tmem_alloc(&tmem_base, 512);
-    tmem_relinquish();
-    tc_fence_before();
-    named_bar_sync(kAlloc, kAllocCount);
-    tc_fence_after();
-    griddep_launch_dependents();               // only now: a dependent may want TMEM too
-    // tokens of no request, and of requests with more tokens than the config's
-    const int T = ws.hdr->num_tokens;
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
-      const int r = ws.tok_req[t];
-      if (r >= 0 && ws.req_qstart[r + 1] - ws.req_qstart[r] <= a.q_len) continue;
-      for (int x = lane; x < a.Hq * (kHeadDim / 8); x += 32)
-        reinterpret_cast<uint4*>(a.out + (int64_t)t * a.Hq * kHeadDim)[x] = make_uint4(0, 0, 0, 0);
-      for (int x = lane; x < a.Hq; x += 32) a.lse[(int64_t)t * a.Hq + x] = -INFINITY;
-    }
-    named_bar_sync(kDone, kDoneCount);
-    tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
-    return;
-  }
+  if (extra >= 2 * S::kTeams) return;
   TeamShared<NG>& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
   const int teams = S::kTeams * (int)gridDim.x;
@@ -465,27 +446,37 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     constexpr uint32_t idesc = idesc_f16(0, 128, kN);
     const uint64_t dq = kstep_desc(smem_u32(qbuf), 0, kN), dp = kstep_desc(smem_u32(pbuf), 0, kN);
     const uint32_t plo = (uint32_t)dp, hi = (uint32_t)(dq >> 32);
+    if (keeper) {
+      tmem_alloc(&tmem_base, 512);
+      tmem_relinquish();
+      tc_fence_before();
+    }
     Tiles tl;
-    const bool any = tl.open(ws, a, vid, teams, lane);
+    bool more = tl.open(ws, a, vid, teams, lane) && tl.next(ws, a);
     named_bar_sync(kAlloc, kAllocCount);
     tc_fence_after();
-    const uint32_t tk = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols, tv = tk + 64,
-                   ts = tk + 128, to = tk + 128 + kN;
-    if (!any) return;
-    for (uint32_t ph = 0; tl.next(ws, a); ph ^= 1u) {
+    griddep_launch_dependents();               // only now: a dependent may want TMEM too
+    const uint32_t tk = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols, tv = tk + 32,
+                   ts = tk + 96, to = ts + kN;
+    for (uint32_t ph = 0; more; ph ^= 1u) {
       const uint32_t qlo = (uint32_t)dq + (tl.seg & 1) * (S::kOperand >> 4);
       if (tl.first) mbar_wait(&sh.q_ready[tl.seg & 1], par(tl.seg), ws.hdr);
-      mbar_wait(&sh.k_ready, ph, ws.hdr);
-      __syncwarp();
-      tc_fence_after();
-      if (elect_one()) {                       // S^T = K Q^T (128 keys x rows)
-        umma_ts<false>(ts, tk, qlo, hi, idesc);
 #pragma unroll
-        for (int ks = 1; ks < 8; ++ks)
-          umma_ts<true>(ts, tk + 8 * ks, qlo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, hi, idesc);
-        umma_commit(&sh.s_ready);
+      for (int half = 0; half < 2; ++half) {   // S^T = K Q^T (128 keys x rows), 64 dims at a time
+        mbar_wait(&sh.k_ready, half, ws.hdr);
+        __syncwarp();
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t b = qlo + half * (kN * 8) + ks * 2;
+            if (half == 0 && ks == 0) umma_ts<false>(ts, tk, b, hi, idesc);
+            else umma_ts<true>(ts, tk + 8 * ks, b, hi, idesc);
+          }
+          umma_commit(half ? &sh.s_ready : &sh.k_free);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       mbar_wait(&sh.p_ready, ph, ws.hdr);
       __syncwarp();
       tc_fence_after();
@@ -498,6 +489,12 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         umma_commit(&sh.o_ready);
       }
       __syncwarp();
+      more = tl.next(ws, a);
+    }
+    if (keeper) {
+      named_bar_sync(kDone, kDoneCount);
+      tc_fence_after();
+      tmem_dealloc(tmem_base, 512);
     }
     return;
   }
@@ -508,10 +505,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     // K and V slot; of the last page only the rows that exist.  Each segment's
     // Q rows, bf16 -> fp16, go to the B operand after its first page.
     Tiles tl;
-    if (!tl.open(ws, a, vid, teams, lane)) return;
+    const bool any = tl.open(ws, a, vid, teams, lane);
     int arms = 0, stage = 0, mine = 0;
     uint32_t phase = 0;
-    while (tl.next(ws, a)) {
+    while (any && tl.next(ws, a)) {
       const Walk& wk = tl.wk;
       const int at = (tl.j - wk.j0) & 31;
       if (at == 0)
@@ -564,6 +561,15 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         if (lane == 0) mbar_arrive(&sh.q_ready[b]);
       }
     }
+    // tokens of no request, and of requests with more tokens than the config's
+    const int T = ws.hdr->num_tokens;
+    for (int t = vid; t < T; t += teams) {
+      const int r = ws.tok_req[t];
+      if (r >= 0 && ws.req_qstart[r + 1] - ws.req_qstart[r] <= a.q_len) continue;
+      for (int x = lane; x < a.Hq * (kHeadDim / 8); x += 32)
+        reinterpret_cast<uint4*>(a.out + (int64_t)t * a.Hq * kHeadDim)[x] = make_uint4(0, 0, 0, 0);
+      for (int x = lane; x < a.Hq; x += 32) a.lse[(int64_t)t * a.Hq + x] = -INFINITY;
+    }
     // Normally the consumers wait for every copy issued here.  After a wait
     // gave up they may not have: let the copies in flight land.
     if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
@@ -591,6 +597,12 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     for (int x = ttid; x < S::kOperand / 16; x += 128)
       reinterpret_cast<uint4*>(pbuf)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
+  auto written = [&](uint64_t* bar_) {         // this warp's TMEM stores are done
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_);
+  };
   auto step = [&]() {
     if (++stage == kStages) { stage = 0; phase ^= 1u; }
   };
@@ -599,7 +611,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   named_bar_sync(kAlloc, kAllocCount);
   tc_fence_after();
   const uint32_t tm = tmem_base + team * S::kCols + lanes;
-  const uint32_t tk = tm, tv = tm + 64, ts = tm + 128, to = tm + 128 + kN;
+  const uint32_t tk = tm, tv = tm + 32, ts = tm + 96, to = ts + kN;
   int4 split = make_int4(0, 0, 0, 0);
   for (int seg = 0; any && wk.next(ws, a.Hkv);) {
     if (wk.nq > a.q_len || wk.nq == 0) {       // more tokens than the config's, or none
@@ -620,29 +632,32 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       l[i][0] = l[i][1] = 0.f;
     }
     for (int j = wk.j0; j < wk.j1; ++j) {
-      // ---- K -> TMEM, S^T = K Q^T (128 keys x rows)
+      // ---- K and V -> TMEM by halves, in turns: the first half of K is read
+      // by its MMAs (S^T = K Q^T) while the first half of V is written
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const int ntok = sh.usable[stage] ? wk.L - j * kBlock : 0;   // keys that exist
       const int all = ntok - wk.nq + 1;                            // and that every row sees
-      key_row(ring + stage * kPageBytes + ttid * kFp4Row, tk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh.empty_bar[stage]);
-        mbar_arrive(&sh.k_ready);
-      }
+      const int kst = stage;
+      const uint8_t* kt = ring + kst * kPageBytes + ttid * kFp4Row;
       step();
-      // ---- V -> TMEM, once the last P V has read its predecessor
-      if (j > wk.j0) {
+      key_half(kt, tk, 0);
+      written(&sh.k_ready);
+      if (j > wk.j0) {                         // the last P V has read V
         mbar_wait(&sh.o_ready, o_phase, ws.hdr);
         o_phase ^= 1u;
         tc_fence_after();
       }
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const uint8_t* vt = ring + stage * kPageBytes;
-      if (all >= kBlock) value_dims<false>(vt, tv, w, lane, ntok, all);
-      else value_dims<true>(vt, tv, w, lane, ntok, all);
+      if (all >= kBlock) value_half<false>(vt, tv, 0, w, lane, ntok, all);
+      else value_half<true>(vt, tv, 0, w, lane, ntok, all);
+      mbar_wait(&sh.k_free, ph, ws.hdr);
+      tc_fence_after();
+      key_half(kt, tk, 1);
+      written(&sh.k_ready);
+      if (lane == 0) mbar_arrive(&sh.empty_bar[kst]);
+      if (all >= kBlock) value_half<false>(vt, tv + 32, 1, w, lane, ntok, all);
+      else value_half<true>(vt, tv + 32, 1, w, lane, ntok, all);
       if (all < kBlock) {
         if (ttid >= all && ttid < ntok) {      // NaN scales that only later tokens see
           unsigned bad = 0;
@@ -748,10 +763,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         stsm_x4_t(paddr + i * 1024, p[0], p[1], p[2], p[3]);
       }
       fence_proxy_async_smem();
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_ready);
+      written(&sh.p_ready);
     }
 
     // ---- the segment's result: whole rows, or a partial
@@ -832,7 +844,6 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 constexpr int kMergeRows = 2;
 constexpr int kMergeThreads = kMergeRows * 128;
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a, int teams) {
-  static_assert(kTeamsMax <= 2 * kMergeThreads, "two records a thread");
   __shared__ int4 list[kTeamsMax];
   __shared__ int owner[kTeamsMax];
   __shared__ int counts[kMergeThreads / 32];
@@ -842,12 +853,11 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
   griddep_launch_dependents();
   griddep_wait();
   int n = 0;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int c = half * kMergeThreads + tid;
+  for (int c0 = 0; c0 < teams; c0 += kMergeThreads) {
+    const int c = c0 + tid;
     const int4 rec = c < teams ? a.split[c] : make_int4(0, 0, 0, 0);
     const unsigned any = __ballot_sync(0xffffffffu, rec.x > 0);
-    if (half) __syncthreads();
+    __syncthreads();
     if (lane == 0) counts[warp] = __popc(any);
     __syncthreads();
     int at = n + __popc(any & ((1u << lane) - 1u));
