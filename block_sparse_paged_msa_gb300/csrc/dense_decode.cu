@@ -23,10 +23,29 @@
 //
 // Work split.  One unit of work is a 128-key page of one (request, KV head).
 // The step's units, request by request and head by head, are cut into equal
-// contiguous ranges, one per team of warps, whatever the lengths are; a (request,
-// head) whose units lie in several ranges leaves one partial per team in the
-// scratch, merged in team order by the second kernel.  All G * q_len query rows of a
-// head share each read of a key.
+// contiguous ranges, one per team of warps, whatever the lengths are; a
+// (request, head) whose units lie in several ranges leaves one partial per team
+// in the scratch, merged in team order by the second kernel.  All G * q_len
+// query rows of a head share each read of a key.
+//
+// Layout.  A thread dequantises one key row (its TMEM lane) and four value dims
+// of 32 keys (V transposed: 16 lanes x 256 bits is the fragment in which a
+// thread's pairs of neighbouring keys go out); both are the A operands of
+//     S^T = K Q^T (128 keys x rows)   and   O^T += V^T P (128 dims x rows),
+// so that N is the number of query rows and no MMA row is padding.  S^T comes
+// back in the same fragment, a thread holding 8 keys of 2 rows in 8; stmatrix
+// transposes the probabilities into the B operand.  K passes through TMEM in
+// two halves, in turns with V's: 128 columns a team, four teams an SM.
+//
+// What bounds it.  32 requests of 8k-32k tokens, 64 + 8 heads (754 MB): 142 us,
+// 5.3 TB/s, 0.79 of the measured copy bandwidth; per page and SM about 1000
+// cycles, 670 of them issue slots (2680 warp instructions: 1024 conversions
+// and scalings that nothing can leave out), the rest the waits of a tile's
+// chain that four teams do not cover.  With mma.sync in place of tcgen05 the
+// same dequantisation took 192 us: an mma.sync holds the issue port for about
+// 8 cycles, 256 of them a page.  16 requests of 32772 tokens with 4 new ones
+// each (32 rows): 166 us, 3.7 TB/s, against 295 us by mma.sync.  Two requests
+// of 1.5k tokens, one head: 8 us, the chain of one tile and two launches.
 #include <atomic>
 
 #include "tcgen05.cuh"
@@ -74,17 +93,22 @@ struct Partition {
 };
 
 // The request that holds unit u: the last r with cu[r] * Hkv <= u (requests
-// without blocks hold none).  One warp, 32 probes at a time; `first` is this
-// lane's cu[min(lane, max_batch)], so that a batch of up to 32 needs no load.
-__device__ __forceinline__ int request_of(const int32_t* cu, int first, int batch, uint32_t Hkv,
-                                          uint32_t u, int lane) {
+// without blocks hold none).  One warp: up to 128 requests from `first`, this
+// lane's cu[4 lane .. 4 lane + 3]; more by 32 probes at a time.
+__device__ __forceinline__ int request_of(const int32_t* cu, const int4& first, int batch,
+                                          uint32_t Hkv, uint32_t u, int lane) {
+  if (batch <= 128) {
+    const int at[4] = {first.x, first.y, first.z, first.w};
+    int below = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) below += 4 * lane + i < batch && (uint32_t)at[i] * Hkv <= u;
+    return __reduce_add_sync(0xffffffffu, below) - 1;
+  }
   int lo = 0, n = batch;                       // the answer lies in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lo + lane * step;
-    const bool in = i < lo + n;
-    const int at = batch <= 32 ? first : (in ? cu[i] : 0);
-    const bool below = in && (uint32_t)at * Hkv <= u;
+    const bool below = i < lo + n && (uint32_t)cu[i] * Hkv <= u;
     const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));   // lane 0 is always below
     const int end = lo + n;
     lo += k * step;
@@ -100,12 +124,14 @@ struct Walk {
   // the current segment
   int h, j0, j1, nq, qs, L;
   uint32_t last;               // its group's last unit
+  int page;                    // kPages: this lane's page, of block j0 + lane
   bool starts, whole;          // it starts its group; it is all of its group
 
   // The range of team vid; false if it has none.  One warp, all lanes alike.
   __device__ __forceinline__ bool open(const WsView& ws, const DenseArgs& a, int vid, int teams,
                                        int lane) {
-    const int first = ws.req_cu_nb[min(lane, a.max_batch)];
+    // the region is padded to 256 bytes: the last int4 of the list is whole
+    const int4 first = reinterpret_cast<const int4*>(ws.req_cu_nb)[min(lane, a.max_batch / 4)];
     const int batch = ws.hdr->batch;
     const uint32_t U = (uint32_t)ws.hdr->total_blocks * a.Hkv;
     const uint32_t n = min((uint32_t)teams, U);
@@ -116,9 +142,12 @@ struct Walk {
     r = request_of(ws.req_cu_nb, first, batch, a.Hkv, u, lane);
     return true;
   }
-  // The next segment; false at the end of the range.
-  __device__ __forceinline__ bool next(const WsView& ws, uint32_t Hkv) {
+  // The next segment; false at the end of the range.  kPages: with its first 32
+  // pages (loaded beside the rest, the request alone being known).
+  template <bool kPages = false>
+  __device__ __forceinline__ bool next(const WsView& ws, const DenseArgs& a, int lane = 0) {
     if (u >= end) return false;
+    const uint32_t Hkv = a.Hkv;
     uint32_t cu0 = ws.req_cu_nb[r], cu1 = ws.req_cu_nb[r + 1];   // u is below the last request's end
     while (cu1 * Hkv <= u) {
       ++r;
@@ -137,6 +166,8 @@ struct Walk {
     starts = j0 == 0;
     whole = starts && j1 == (int)nb;
     u = ga + j1;
+    if (kPages)
+      page = j0 + lane < j1 ? ws.block_table[(int64_t)r * a.max_blocks + j0 + lane] : -1;
     return true;
   }
 };
@@ -320,11 +351,12 @@ struct Tiles {
   }
   // Skips the segments of requests without new tokens, or with more than the
   // config's (the consumers flag those).
-  __device__ __forceinline__ bool next(const WsView& ws, const DenseArgs& a) {
+  template <bool kPages = false>
+  __device__ __forceinline__ bool next(const WsView& ws, const DenseArgs& a, int lane = 0) {
     first = last;
     if (last) {
       do {
-        if (!wk.next(ws, a.Hkv)) return false;
+        if (!wk.next<kPages>(ws, a, lane)) return false;
       } while (wk.nq > a.q_len || wk.nq == 0);
       ++seg;
       j = wk.j0;
@@ -339,19 +371,20 @@ struct Tiles {
 // A CTA is kTeams independent teams of four consumer warps, each with its own
 // range of units, ring, TMEM columns, loader warp and MMA warp.  NG: groups of
 // 8 query rows.
-template <int NG>
+template <int NG, int TEAMS>
 struct Shape {
   static constexpr int kN = NG < 2 ? 16 : 8 * NG;                 // MMA N
-  static constexpr int kTeams = NG <= 2 ? 4 : (NG == 4 ? 3 : 2);
+  static constexpr int kTeams = TEAMS;
   static constexpr int kThreads = kTeams * 128 + 256;
   // threads x launch registers = consumers x theirs + 256 x the others':
   // 768 x 80 = 512 x 96 + 256 x 48; 640 x 96 = 384 x 128 + 256 x 48;
   // 512 x 128 = 256 x 200 + 256 x 56
-  static constexpr int kConsumerRegs = NG <= 2 ? 96 : (NG == 4 ? 128 : 200);
-  static constexpr int kMiscRegs = NG <= 4 ? 48 : 56;
+  static constexpr int kConsumerRegs = TEAMS == 4 ? 96 : (TEAMS == 3 ? 128 : 200);
+  static constexpr int kMiscRegs = TEAMS >= 3 ? 48 : 56;
   // TMEM columns of a team: K (64 dims) | V | S | O
   static constexpr int kCols = 96 + 2 * kN;
-  static constexpr int kStages = NG <= 2 ? 4 : (NG == 4 ? 5 : 6);
+  static constexpr int kFit = (222 * 1024 / kTeams - 3 * kN * kHeadDim * 2) / kPageBytes;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kOperand = kN * kHeadDim * 2;              // a Q buffer, and P
   static constexpr int kTeamSmem = 3 * kOperand + kStages * kPageBytes;
   static constexpr int kSmem = kTeams * kTeamSmem;
@@ -361,13 +394,13 @@ struct Shape {
 // Phase parity of the use number t of buffer t & 1.
 __device__ __forceinline__ uint32_t par(int t) { return (uint32_t)(t >> 1) & 1u; }
 
-template <int NG>
+template <int NG, int TEAMS>
 struct TeamShared {
-  using S = Shape<NG>;
+  using S = Shape<NG, TEAMS>;
   float red[4][S::kN];         // per warp: row maxima, row sums
   float alpha[S::kN], ref[S::kN];              // rescaling, final references
   uint64_t full_bar[S::kStages], empty_bar[S::kStages];
-  uint64_t q_ready[2], q_free[2];              // Q written by the loader; buffer free again
+  uint64_t q_free[2];          // Q buffer free again
   uint64_t k_ready, k_free;    // a half of K written (two a tile); the first half read
   uint64_t s_ready;            // S written, K read
   uint64_t p_ready, o_ready;   // P and V written; O updated and P and V read
@@ -393,13 +426,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-template <int NG>
-__global__ void __launch_bounds__(Shape<NG>::kThreads, 1)
+template <int NG, int TEAMS>
+__global__ void __launch_bounds__(Shape<NG, TEAMS>::kThreads, 1)
 dense_decode_kernel(WsView ws, DenseArgs a) {
-  using S = Shape<NG>;
+  using S = Shape<NG, TEAMS>;
   constexpr int kN = S::kN, kStages = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(16) TeamShared<NG> shared[S::kTeams];
+  __shared__ __align__(16) TeamShared<NG, TEAMS> shared[S::kTeams];
   __shared__ uint32_t tmem_base;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
@@ -407,13 +440,12 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   const int team = extra < 0 ? warp / 4 : (extra < S::kTeams ? extra : extra - S::kTeams);
   const bool keeper = extra == S::kTeams;      // MMA warp 0 keeps the TMEM allocation
   if (tid < S::kTeams) {
-    TeamShared<NG>& st = shared[tid];
+    TeamShared<NG, TEAMS>& st = shared[tid];
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&st.full_bar[i], 1);
       mbar_init(&st.empty_bar[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&st.q_ready[i], 1);
       mbar_init(&st.q_free[i], 4);
     }
     mbar_init(&st.k_ready, 4);
@@ -423,15 +455,22 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     mbar_init(&st.o_ready, 1);
     fence_barrier_init();
   }
+  if (keeper) {
+    // before the wait: kernels of this library that use TMEM let their
+    // dependents start only once they hold theirs
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
   __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();                 // (as this one does)
   griddep_wait();
-  constexpr int kDone = 15;                    // named barrier: every consumer, and the keeper
-  constexpr int kDoneCount = S::kTeams * 128 + 32;
-  constexpr int kAlloc = 14;                   // every consumer and MMA warp
-  constexpr int kAllocCount = S::kTeams * 160;
+  constexpr int kDone = 15;                    // named barrier: every consumer and MMA warp
+  constexpr int kDoneCount = S::kTeams * 160;
   if (extra >= 0) regs_down<S::kMiscRegs>();
   if (extra >= 2 * S::kTeams) return;
-  TeamShared<NG>& sh = shared[team];
+  TeamShared<NG, TEAMS>& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
   const int teams = S::kTeams * (int)gridDim.x;
   uint8_t* qbuf = smem + team * S::kTeamSmem;  // Q x 2 and P: K-major, 128-byte swizzle
@@ -446,21 +485,41 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     constexpr uint32_t idesc = idesc_f16(0, 128, kN);
     const uint64_t dq = kstep_desc(smem_u32(qbuf), 0, kN), dp = kstep_desc(smem_u32(pbuf), 0, kN);
     const uint32_t plo = (uint32_t)dp, hi = (uint32_t)(dq >> 32);
-    if (keeper) {
-      tmem_alloc(&tmem_base, 512);
-      tmem_relinquish();
-      tc_fence_before();
-    }
     Tiles tl;
     bool more = tl.open(ws, a, vid, teams, lane) && tl.next(ws, a);
-    named_bar_sync(kAlloc, kAllocCount);
-    tc_fence_after();
-    griddep_launch_dependents();               // only now: a dependent may want TMEM too
     const uint32_t tk = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols, tv = tk + 32,
                    ts = tk + 96, to = ts + kN;
-    for (uint32_t ph = 0; more; ph ^= 1u) {
+    const bool issued = more;
+    uint32_t ph = 0;
+    for (; more; ph ^= 1u) {
       const uint32_t qlo = (uint32_t)dq + (tl.seg & 1) * (S::kOperand >> 4);
-      if (tl.first) mbar_wait(&sh.q_ready[tl.seg & 1], par(tl.seg), ws.hdr);
+      if (tl.first) {
+        // the segment's Q, bf16 -> fp16 rows of the B operand, zero past the last
+        const Walk& wk = tl.wk;
+        const int nrows = wk.nq * a.G, b = tl.seg & 1;
+        if (tl.seg >= 2) mbar_wait(&sh.q_free[b], par(tl.seg - 2), ws.hdr);
+        bool ovf = false;
+        for (int x = nrows * 16 + lane; x < kN * 16; x += 32)
+          *reinterpret_cast<uint4*>(qbuf + b * S::kOperand + kmaj_off(x >> 4, x & 15, kN)) =
+              make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
+        for (int x = lane; x < nrows * 16; x += 32) {
+          const int n = x >> 4, ch = x & 15;
+          uint4 v =
+              *reinterpret_cast<const uint4*>(a.q + a.q_row(wk.qs, wk.h, n) * kHeadDim + 8 * ch);
+          v.x = bf16x2_to_f16x2(v.x);
+          v.y = bf16x2_to_f16x2(v.y);
+          v.z = bf16x2_to_f16x2(v.z);
+          v.w = bf16x2_to_f16x2(v.w);
+          ovf |= f16x2_has_inf(v.x) | f16x2_has_inf(v.y) | f16x2_has_inf(v.z) |
+                 f16x2_has_inf(v.w);
+          *reinterpret_cast<uint4*>(qbuf + b * S::kOperand + kmaj_off(n, ch, kN)) = v;
+        }
+        if (__any_sync(0xffffffffu, ovf) && lane == 0)
+          set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {   // S^T = K Q^T (128 keys x rows), 64 dims at a time
         mbar_wait(&sh.k_ready, half, ws.hdr);
@@ -491,10 +550,17 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       __syncwarp();
       more = tl.next(ws, a);
     }
+    // Normally the consumers have waited for the last MMAs.  After a wait gave
+    // up they may not have: let them finish before TMEM goes.
+    if (issued && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
+      mbar_drain(&sh.o_ready, ph ^ 1u);
+    __syncwarp();
     if (keeper) {
       named_bar_sync(kDone, kDoneCount);
       tc_fence_after();
       tmem_dealloc(tmem_base, 512);
+    } else {
+      named_bar_arrive(kDone, kDoneCount);
     }
     return;
   }
@@ -502,16 +568,17 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   if (extra >= 0) {
     // ---------------------------------------------------------------- loader
     // The pages of a segment 32 at a time (a lane each), one bulk copy per
-    // K and V slot; of the last page only the rows that exist.  Each segment's
-    // Q rows, bf16 -> fp16, go to the B operand after its first page.
+    // K and V slot; of the last page only the rows that exist.
     Tiles tl;
     const bool any = tl.open(ws, a, vid, teams, lane);
     int arms = 0, stage = 0, mine = 0;
     uint32_t phase = 0;
-    while (any && tl.next(ws, a)) {
+    while (any && tl.next<true>(ws, a, lane)) {
       const Walk& wk = tl.wk;
       const int at = (tl.j - wk.j0) & 31;
-      if (at == 0)
+      if (tl.first)
+        mine = wk.page;
+      else if (at == 0)
         mine = tl.j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + tl.j + lane]
                                    : -1;
       const int page = __shfl_sync(0xffffffffu, mine, at);
@@ -535,30 +602,6 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         __syncwarp();
         ++arms;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
-      }
-      if (tl.first) {
-        const int nrows = wk.nq * a.G, b = tl.seg & 1;
-        if (tl.seg >= 2) mbar_wait(&sh.q_free[b], par(tl.seg - 2), ws.hdr);
-        bool ovf = false;
-#pragma unroll 4
-        for (int x = lane; x < kN * 16; x += 32) {
-          const int n = x >> 4, ch = x & 15;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);                   // rows past the last: zero
-          if (n < nrows)
-            v = *reinterpret_cast<const uint4*>(a.q + a.q_row(wk.qs, wk.h, n) * kHeadDim + 8 * ch);
-          v.x = bf16x2_to_f16x2(v.x);
-          v.y = bf16x2_to_f16x2(v.y);
-          v.z = bf16x2_to_f16x2(v.z);
-          v.w = bf16x2_to_f16x2(v.w);
-          ovf |= f16x2_has_inf(v.x) | f16x2_has_inf(v.y) | f16x2_has_inf(v.z) |
-                 f16x2_has_inf(v.w);
-          *reinterpret_cast<uint4*>(qbuf + b * S::kOperand + kmaj_off(n, ch, kN)) = v;
-        }
-        if (__any_sync(0xffffffffu, ovf) && lane == 0)
-          set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_ready[b]);
       }
     }
     // tokens of no request, and of requests with more tokens than the config's
@@ -608,12 +651,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   };
   Walk wk;
   const bool any = wk.open(ws, a, vid, teams, lane);
-  named_bar_sync(kAlloc, kAllocCount);
-  tc_fence_after();
   const uint32_t tm = tmem_base + team * S::kCols + lanes;
   const uint32_t tk = tm, tv = tm + 32, ts = tm + 96, to = ts + kN;
   int4 split = make_int4(0, 0, 0, 0);
-  for (int seg = 0; any && wk.next(ws, a.Hkv);) {
+  for (int seg = 0; any && wk.next(ws, a);) {
     if (wk.nq > a.q_len || wk.nq == 0) {       // more tokens than the config's, or none
       if (ttid == 0 && wk.nq > 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
       continue;
@@ -827,7 +868,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       const int c1 = (int)Partition(U, min((uint32_t)teams, U)).owner(wk.last);
       split = make_int4(c1 - vid + 1, wk.qs, wk.h, wk.nq);
     }
-    if (8 * NG == kN)                          // P rows are refilled; Q goes to the loader
+    if (8 * NG == kN)                          // P rows are refilled; Q goes to the MMA warp
       fence_proxy_async_smem();
     named_bar_sync(bar, 128);                  // red, ref, tok, nan and P are free again
     if (lane == 0) mbar_arrive(&sh.q_free[seg & 1]);
@@ -840,19 +881,22 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 
 // Merges the partials of the (request, head) groups that lie in several teams'
 // ranges, in team order.  Every block lists the split groups in order, then
-// takes its share of (group, kMergeRows rows), four warps a row.
-constexpr int kMergeRows = 2;
-constexpr int kMergeThreads = kMergeRows * 128;
+// takes its share of (group, two rows), four warps a row; rows of many
+// partials then get a whole block each.
+constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
+constexpr int kMergeRows = 2, kRowWarps = kMergeWarps / kMergeRows;
+constexpr int kMany = 32;
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a, int teams) {
   __shared__ int4 list[kTeamsMax];
   __shared__ int owner[kTeamsMax];
-  __shared__ int counts[kMergeThreads / 32];
-  __shared__ float4 part[kMergeRows][4][32];
-  __shared__ float part_l[kMergeRows][4];
+  __shared__ int counts[kMergeWarps], many;
+  __shared__ float4 part[kMergeWarps][32];
+  __shared__ float part_l[kMergeWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
   griddep_wait();
   int n = 0;
+  if (tid == 0) many = 0;
   for (int c0 = 0; c0 < teams; c0 += kMergeThreads) {
     const int c = c0 + tid;
     const int4 rec = c < teams ? a.split[c] : make_int4(0, 0, 0, 0);
@@ -861,22 +905,20 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
     if (lane == 0) counts[warp] = __popc(any);
     __syncthreads();
     int at = n + __popc(any & ((1u << lane) - 1u));
-    for (int i = 0; i < kMergeThreads / 32; ++i) {
+    for (int i = 0; i < kMergeWarps; ++i) {
       if (i < warp) at += counts[i];
       n += counts[i];
     }
     if (rec.x > 0) {
       list[at] = rec;
       owner[at] = c;
+      if (rec.x > kMany) many = 1;
     }
   }
   __syncthreads();
-  const int chunks = (a.rows + kMergeRows - 1) / kMergeRows;
-  const int mr = warp >> 2, w4 = warp & 3;
-  for (int item = blockIdx.x; item < n * chunks; item += gridDim.x) {
-    const int4 rec = list[item / chunks];
-    const int64_t c0 = owner[item / chunks];
-    const int np = rec.x, row = item % chunks * kMergeRows + mr;
+  // one row by `warps` warps of the block, this one the w-th, from warp w0 on
+  auto merge_row = [&](const int4& rec, int64_t c0, int row, int w, int warps, int w0) {
+    const int np = rec.x;
     const bool on = row < rec.w * a.G;
     // partial i: the second slot of c0, the first of c0 + i
     auto at = [&](int i) { return (2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
@@ -888,8 +930,8 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     if (on) {
-#pragma unroll 4
-      for (int i = w4; i < np; i += 4) {
+#pragma unroll 8
+      for (int i = w; i < np; i += warps) {
         const float2 ml = a.ml_part[at(i)];
         const float4 v = *reinterpret_cast<const float4*>(a.o_part + at(i) * kHeadDim + 4 * lane);
         const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
@@ -898,15 +940,14 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
         o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
       }
     }
-    part[mr][w4][lane] = o;
-    if (lane == 0) part_l[mr][w4] = l;
+    part[warp][lane] = o;
+    if (lane == 0) part_l[warp] = l;
     __syncthreads();
-    if (on && w4 == 0) {
-#pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const float4 v = part[mr][w][lane];
+    if (on && w == 0) {
+      for (int i = 1; i < warps; ++i) {
+        const float4 v = part[w0 + i][lane];
         o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-        l += part_l[mr][w];
+        l += part_l[w0 + i];
       }
       const int64_t hq = a.q_row(rec.y, rec.z, row);
       const float inv = l == 0.f ? 0.f : a.v_scale / l;
@@ -915,17 +956,30 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
       if (lane == 0) a.lse[hq] = l == 0.f ? -INFINITY : (M + log2f(l) - kBias) * kLn2;
     }
     __syncthreads();
+  };
+  const int chunks = (a.rows + kMergeRows - 1) / kMergeRows;
+  for (int item = blockIdx.x; item < n * chunks; item += gridDim.x) {
+    const int gi = item / chunks;
+    if (list[gi].x <= kMany)
+      merge_row(list[gi], owner[gi], (item - gi * chunks) * kMergeRows + warp / kRowWarps,
+                warp % kRowWarps, kRowWarps, warp / kRowWarps * kRowWarps);
+  }
+  if (!many) return;
+  for (int item = blockIdx.x; item < n * a.rows; item += gridDim.x) {
+    const int gi = item / a.rows;
+    if (list[gi].x > kMany)
+      merge_row(list[gi], owner[gi], item - gi * a.rows, warp, kMergeWarps, 0);
   }
 }
 
-template <int NG>
+template <int NG, int TEAMS>
 msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cudaStream_t s) {
-  using S = Shape<NG>;
+  using S = Shape<NG, TEAMS>;
   static std::atomic<bool> ready[64];          // shared-memory limit raised, per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MSA_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(dense_decode_kernel<NG>,
+    if (cudaFuncSetAttribute(dense_decode_kernel<NG, TEAMS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::kSmem) != cudaSuccess)
       return MSA_ERR_CUDA;
@@ -934,10 +988,10 @@ msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cuda
   const int sms = sm_count();
   int64_t grid = sms;                          // one CTA an SM
   if (grid > kTeamsMax / S::kTeams) grid = kTeamsMax / S::kTeams;
-  if (grid > units) grid = units;
   if (grid <= 0) return MSA_ERR_CUDA;
+  if (grid > units) grid = units;
   const int teams = (int)grid * S::kTeams;
-  msa_status st = launch_pdl(dense_decode_kernel<NG>, dim3((unsigned)grid), dim3(S::kThreads),
+  msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS>, dim3((unsigned)grid), dim3(S::kThreads),
                              S::kSmem, s, v, a);
   if (st != MSA_OK) return st;
   int64_t blocks = (int64_t)teams * ((a.rows + kMergeRows - 1) / kMergeRows);
@@ -975,7 +1029,7 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
       ((uintptr_t)scratch & 255) != 0 || ((uintptr_t)lse & 3) != 0)
     return MSA_ERR_INVALID_ARG;
   const int64_t T = max_tokens_of(*cfg);
-  if (T <= 0) return MSA_OK;
+  if (T <= 0 || cfg->max_batch == 0) return MSA_OK;
   DenseArgs a;
   a.Hkv = cfg->num_kv_heads;
   a.Hq = cfg->num_q_heads;
@@ -999,8 +1053,17 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   const int64_t units = (int64_t)cfg->max_batch * cfg->max_blocks_per_req * a.Hkv;
   if (units > 0x7fffffff) return MSA_ERR_UNSUPPORTED;   // units are counted in 32 bits
   cudaStream_t s = (cudaStream_t)stream;
-  if (a.rows <= 8) return launch_dense<1>(v, a, units, s);
-  if (a.rows <= 16) return launch_dense<2>(v, a, units, s);
-  if (a.rows <= 32) return launch_dense<4>(v, a, units, s);
-  return launch_dense<8>(v, a, units, s);
+  // Teams an SM.  A fourth one hides more of a tile's chain of waits (32
+  // requests of 8k-32k tokens, 8 heads: 142 us, with three 155 us); but it cuts
+  // a short step into more partials and prefetches less of each range (61
+  // requests of up to 6001 tokens, one head: 23 us, with three 19 us; two
+  // requests of 1.5k: 8.7 and 8.0 us).  One request of 131071 tokens, 54 pages
+  // an SM, takes 42 us either way.  32 rows fit three teams, 64 rows two (TMEM).
+  const bool many = units >= (int64_t)64 * sm_count();
+  if (a.rows <= 8)
+    return many ? launch_dense<1, 4>(v, a, units, s) : launch_dense<1, 3>(v, a, units, s);
+  if (a.rows <= 16)
+    return many ? launch_dense<2, 4>(v, a, units, s) : launch_dense<2, 3>(v, a, units, s);
+  if (a.rows <= 32) return launch_dense<4, 3>(v, a, units, s);
+  return launch_dense<8, 2>(v, a, units, s);
 }
