@@ -385,25 +385,22 @@ def cache_write(cfg, ws, k, v, idx_k, k_pages, v_pages, idx_k_pages, out_cache_l
 
 
 class _Layout:
-    """What a config asks of the tensors of a step, taken from it once."""
+    """What a config asks of the tensors of a step, taken from it once: the
+    least shape of each (more rows on dim 0 are fine)."""
 
     def __init__(self, cfg):
-        self.T = max_tokens(cfg)
-        self.heads = (cfg.num_q_heads, cfg.num_kv_heads)
-        self.q_tail = (cfg.num_q_heads, cfg.head_dim)
-        self.kv_tail = (cfg.num_kv_heads, cfg.head_dim)
-        self.idx_tail = (cfg.num_kv_heads, cfg.index_dim)
-        self.lse_tail = (cfg.num_q_heads,)
-        self.pages = cfg.num_pages
+        T, hq, hkv = max_tokens(cfg), cfg.num_q_heads, cfg.num_kv_heads
+        P, D, d = cfg.block_size, cfg.head_dim, cfg.index_dim
+        self.q, self.kv, self.idx = (T, hq, D), (T, hkv, D), (T, hkv, d)
+        self.lse, self.tokens = (T, hq), (T,)
         if cfg.kv_dtype == MSA_KV_NVFP4:    # K and V slots per head, 72-byte rows
-            self.pool_tail = (2 * cfg.num_kv_heads, cfg.block_size,
-                              cfg.head_dim // 2 + cfg.head_dim // 16)
+            self.pool = (cfg.num_pages, 2 * hkv, P, D // 2 + D // 16)
         else:
-            self.pool_tail = (cfg.num_kv_heads, cfg.block_size, cfg.head_dim)
-        self.idx_pool_tail = (cfg.num_kv_heads, cfg.block_size, cfg.index_dim)
+            self.pool = (cfg.num_pages, hkv, P, D)
+        self.idx_pool = (cfg.num_pages, hkv, P, d)
         self.kv_dtypes = _kv_dtypes(cfg)
-        self.ws_bytes = workspace_bytes(cfg)
-        self.dense_scratch = lib().msa_dense_decode_scratch_bytes(ctypes.byref(cfg))
+        self.ws = (workspace_bytes(cfg),)
+        self.dense_scratch = (lib().msa_dense_decode_scratch_bytes(ctypes.byref(cfg)),)
 
 
 _LAYOUTS = {}
@@ -424,31 +421,30 @@ def _device_of(t, name) -> int:
     return t.get_device()
 
 
-def _expect(t, name, dtypes, rows, tail, dev) -> int:
-    """The pointer of a contiguous tensor [>= rows, *tail] of one of `dtypes`
-    on device `dev`; ValueError otherwise (the reason by _need)."""
+def _expect(t, name, dtypes, shape, dev) -> int:
+    """The pointer of a contiguous tensor of one of `dtypes` on device `dev`, of
+    `shape` or with more rows; ValueError otherwise (the reason by _need)."""
     if isinstance(t, torch.Tensor):
         s = t.shape
-        if (t.dtype in dtypes and len(s) and s[0] >= rows and s[1:] == tail
-                and t.is_contiguous() and t.get_device() == dev):
+        if ((s == shape or (len(s) == len(shape) and s[0] >= shape[0] and s[1:] == shape[1:]))
+                and t.dtype in dtypes and t.is_contiguous() and t.get_device() == dev):
             return t.data_ptr()
-    _need(t, name, dtypes, len(tail) + 1, rows, tail)
+    _need(t, name, dtypes, len(shape), shape[0], shape[1:])
     raise ValueError(f"{name} is on another device than the step's other tensors")
 
 
-def _expect_rows(t, name, T, tail, dev):
-    """Pointer and token stride (elements) of a projection's rows [>= T, heads,
-    width] bf16: heads contiguous, tokens at any stride that is a multiple
+def _expect_rows(t, name, shape, dev):
+    """Pointer and token stride (elements) of a projection's bf16 rows [T, heads,
+    width] or more: heads contiguous, tokens at any stride that is a multiple
     of 8."""
-    heads, width = tail
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    T, heads, width = shape
     s = t.shape
+    if s != shape and (len(s) != 3 or s[0] < T or s[1:] != shape[1:]):
+        raise ValueError(f"{name} has shape {tuple(s)}, the config needs {shape}")
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
-    if s[1:] != tail or s[0] < T:
-        raise ValueError(f"{name} has shape {tuple(s)}, the config needs "
-                         f"[>= {T}, {heads}, {width}]")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on another device than the step's other tensors")
     tok, hd, el = t.stride()
@@ -482,41 +478,39 @@ def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, 
     cos_sin.  q_out, idx_q_out: the rotated queries, contiguous; each may be its
     input.  positions: [T] int64, None = the plan's."""
     y = _layout(cfg)
-    dev, T = _device_of(q, "q"), y.T
-    r = MsaRope()
-    p_ws = _expect(ws, "ws", _U8, y.ws_bytes, (), dev)
-    p_q, r.q_stride = _expect_rows(q, "q", T, y.q_tail, dev)
-    p_k, r.k_stride = _expect_rows(k, "k", T, y.kv_tail, dev)
-    p_v, r.v_stride = _expect_rows(v, "v", T, y.kv_tail, dev)
-    p_qo = _expect(q_out, "q_out", _BF16, T, y.q_tail, dev)
-    p_kp = _expect(k_pages, "k_pages", y.kv_dtypes, y.pages, y.pool_tail, dev)
-    p_vp = _expect(v_pages, "v_pages", y.kv_dtypes, y.pages, y.pool_tail, dev)
-    rows, width = _table_shape(cos_sin, "cos_sin")
-    r.cos_sin = _expect(cos_sin, "cos_sin", _F32, 1, (width,), dev)
-    r.rotary_dim = r.idx_rotary_dim = width
-    r.interleaved = 1 if interleaved else 0
-    p_iq = p_ik = p_iv = p_iqo = p_ikp = p_ivp = p_pos = p_loc = None
-    if idx_q is not None:
-        p_iq, r.idx_q_stride = _expect_rows(idx_q, "idx_q", T, y.idx_tail, dev)
-        p_iqo = _expect(idx_q_out, "idx_q_out", _BF16, T, y.idx_tail, dev)
-    if idx_k is not None:
-        p_ik, r.idx_k_stride = _expect_rows(idx_k, "idx_k", T, y.idx_tail, dev)
-        p_ikp = _expect(idx_k_pages, "idx_k_pages", _BF16, y.pages, y.idx_pool_tail, dev)
-    if idx_v is not None:
-        p_iv, r.idx_v_stride = _expect_rows(idx_v, "idx_v", T, y.idx_tail, dev)
-        p_ivp = _expect(idx_v_pages, "idx_v_pages", _BF16, y.pages, y.idx_pool_tail, dev)
+    dev = _device_of(q, "q")
+    p_q, s_q = _expect_rows(q, "q", y.q, dev)
+    p_k, s_k = _expect_rows(k, "k", y.kv, dev)
+    p_v, s_v = _expect_rows(v, "v", y.kv, dev)
+    rows, rot = _table_shape(cos_sin, "cos_sin")
+    p_cs = _expect(cos_sin, "cos_sin", _F32, (rows, rot), dev)
+    p_ics, irot = None, rot
     if idx_cos_sin is not None:
-        n, r.idx_rotary_dim = _table_shape(idx_cos_sin, "idx_cos_sin")
-        r.idx_cos_sin = _expect(idx_cos_sin, "idx_cos_sin", _F32, 1, (r.idx_rotary_dim,), dev)
+        n, irot = _table_shape(idx_cos_sin, "idx_cos_sin")
+        p_ics = _expect(idx_cos_sin, "idx_cos_sin", _F32, (n, irot), dev)
         rows = min(rows, n)
-    r.num_positions = rows
-    if positions is not None:
-        p_pos = _expect(positions, "positions", _I64, T, (), dev)
-    if out_cache_loc is not None:
-        p_loc = _expect(out_cache_loc, "out_cache_loc", _I64, T, (), dev)
-    st = _call(lib().msa_rope_cache_write, dev, stream, ctypes.byref(cfg), p_ws, ctypes.byref(r),
-               p_q, p_k, p_v, p_iq, p_ik, p_iv, p_pos, p_loc, p_qo, p_iqo, p_kp, p_vp, p_ikp,
-               p_ivp)
+    p_iq = p_ik = p_iv = p_iqo = p_ikp = p_ivp = None
+    s_iq = s_ik = s_iv = 0
+    if idx_q is not None:
+        p_iq, s_iq = _expect_rows(idx_q, "idx_q", y.idx, dev)
+        p_iqo = _expect(idx_q_out, "idx_q_out", _BF16, y.idx, dev)
+    if idx_k is not None:
+        p_ik, s_ik = _expect_rows(idx_k, "idx_k", y.idx, dev)
+        p_ikp = _expect(idx_k_pages, "idx_k_pages", _BF16, y.idx_pool, dev)
+    if idx_v is not None:
+        p_iv, s_iv = _expect_rows(idx_v, "idx_v", y.idx, dev)
+        p_ivp = _expect(idx_v_pages, "idx_v_pages", _BF16, y.idx_pool, dev)
+    rope = MsaRope(p_cs, p_ics, rot, irot, 1 if interleaved else 0, rows, s_q, s_k, s_v, s_iq,
+                   s_ik, s_iv)
+    st = _call(lib().msa_rope_cache_write, dev, stream, ctypes.byref(cfg),
+               _expect(ws, "ws", _U8, y.ws, dev), ctypes.byref(rope), p_q, p_k, p_v, p_iq, p_ik,
+               p_iv,
+               None if positions is None else _expect(positions, "positions", _I64, y.tokens, dev),
+               None if out_cache_loc is None
+               else _expect(out_cache_loc, "out_cache_loc", _I64, y.tokens, dev),
+               _expect(q_out, "q_out", _BF16, y.q, dev), p_iqo,
+               _expect(k_pages, "k_pages", y.kv_dtypes, y.pool, dev),
+               _expect(v_pages, "v_pages", y.kv_dtypes, y.pool, dev), p_ikp, p_ivp)
     if st:
         _check("msa_rope_cache_write", st)
 
@@ -652,17 +646,15 @@ def dense_decode(cfg, ws, q, k_pages, v_pages, scratch, out, lse, stream=None):
     plan() and the cache write of the step; no combine() follows.  scratch of
     dense_decode_scratch_bytes(cfg) bytes."""
     y = _layout(cfg)
-    dev, T = _device_of(q, "q"), y.T
-    if y.dense_scratch == 0:
+    dev = _device_of(q, "q")
+    if y.dense_scratch[0] == 0:
         dense_decode_scratch_bytes(cfg)                  # raises what the library says
     st = _call(lib().msa_dense_decode, dev, stream, ctypes.byref(cfg),
-               _expect(ws, "ws", _U8, y.ws_bytes, (), dev),
-               _expect(q, "q", _BF16, T, y.q_tail, dev),
-               _expect(k_pages, "k_pages", y.kv_dtypes, y.pages, y.pool_tail, dev),
-               _expect(v_pages, "v_pages", y.kv_dtypes, y.pages, y.pool_tail, dev),
-               _expect(scratch, "scratch", _U8, y.dense_scratch, (), dev),
-               _expect(out, "out", _BF16, T, y.q_tail, dev),
-               _expect(lse, "lse", _F32, T, y.lse_tail, dev))
+               _expect(ws, "ws", _U8, y.ws, dev), _expect(q, "q", _BF16, y.q, dev),
+               _expect(k_pages, "k_pages", y.kv_dtypes, y.pool, dev),
+               _expect(v_pages, "v_pages", y.kv_dtypes, y.pool, dev),
+               _expect(scratch, "scratch", _U8, y.dense_scratch, dev),
+               _expect(out, "out", _BF16, y.q, dev), _expect(lse, "lse", _F32, y.lse, dev))
     if st:
         _check("msa_dense_decode", st)
 

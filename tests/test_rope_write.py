@@ -94,7 +94,7 @@ def test_refused_on_the_host(bad, status):
 
 def test_rows_layouts_refused_by_the_binding():
     with pytest.raises(ValueError, match="CUDA"):
-        ops._expect_rows(torch.zeros(2, 1, 128, dtype=torch.bfloat16), "q", 2, (1, 128), 0)
+        ops._expect_rows(torch.zeros(2, 1, 128, dtype=torch.bfloat16), "q", (2, 1, 128), 0)
 
 
 # ------------------------------------------------------------ parity (GPU)
