@@ -272,7 +272,9 @@ __device__ __forceinline__ void key_half(const uint8_t* row, uint32_t taddr, int
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const uint2 x = *reinterpret_cast<const uint2*>(row + 32 * half + 8 * b);
-    const uint32_t sc = __byte_perm(sp[b >> 1], 0u, b & 1 ? 0x3232u : 0x1010u);
+    const __half2 sh2 = *reinterpret_cast<const __half2*>(&sp[b >> 1]);
+    const __half2 sc2 = b & 1 ? __high2half2(sh2) : __low2half2(sh2);
+    const uint32_t sc = *reinterpret_cast<const uint32_t*>(&sc2);
     uint32_t lo[4], hi[4];
     e2m1x8_to_f16x2(x.x, lo);
     e2m1x8_to_f16x2(x.y, hi);
@@ -287,49 +289,58 @@ __device__ __forceinline__ void key_half(const uint8_t* row, uint32_t taddr, int
 
 // V, transposed: this warp's dims 32 w .. 32 w + 31 of 64 keys (half 0 or 1 of
 // the tile) -> TMEM lanes 32 w + 8 i + g = dim 32 w + 4 g + i, 32 columns of
-// two keys.
+// two keys.  The warp's two scale blocks go through `pairs` (64 words): a lane
+// converts those of two keys, all read them as (key, key + 1).
 // Keys from ntok on do not exist (their rows may hold anything), and a NaN
 // scale of a key that not every row sees becomes 0 here: 0 * NaN is not 0 (the
 // rows that see it get it back at the end).
-template <bool EDGE>
-__device__ __forceinline__ void value_half(const uint8_t* vt, uint32_t taddr, int half, int w,
-                                           int lane, int ntok, int all) {
+__device__ __forceinline__ void value_half(const uint8_t* vt, uint32_t taddr, int half,
+                                           uint32_t* pairs, int w, int lane, int ntok, int all) {
   constexpr uint32_t m = 0x0f0f0f0fu;
   const int g = lane >> 2, c = lane & 3;
-  const uint8_t* codes = vt + 4 * c * kFp4Row + 16 * w + 2 * g;
-  const uint8_t* scales = vt + 4 * c * kFp4Row + kHeadDim / 2 + 2 * w + (g >> 2);
-  uint32_t lo[16], hi[16];
+  const uint8_t* codes = vt + (64 * half + 4 * c) * kFp4Row + 16 * w + 2 * g;
+  {
+    const int key = 64 * half + 2 * lane;
+    const uint8_t* at = vt + key * kFp4Row + kHeadDim / 2 + 2 * w;
+    uint32_t s[2] = {*reinterpret_cast<const uint16_t*>(at),
+                     *reinterpret_cast<const uint16_t*>(at + kFp4Row)};
+    if (all < kBlock) {
 #pragma unroll
-  for (int qq = 0; qq < 4; ++qq) {
-    const int k0 = (64 * half + 16 * qq) * kFp4Row;   // keys 64 half + 16 qq + 4 c + 0..3
-    uint32_t u[4], s[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u[i] = *reinterpret_cast<const uint16_t*>(codes + k0 + i * kFp4Row);
-      s[i] = scales[k0 + i * kFp4Row];
-    }
-    if (EDGE) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 64 * half + 16 * qq + 4 * c + i;
-        if (key >= ntok || (key >= all && (s[i] & 0x7f) == 0x7f)) s[i] = 0;
+      for (int i = 0; i < 2; ++i) {
+        if (key + i >= ntok) s[i] = 0;
+        if (key + i >= all) {
+          if ((s[i] & 0x7fu) == 0x7fu) s[i] &= 0xff00u;
+          if ((s[i] & 0x7f00u) == 0x7f00u) s[i] &= 0xffu;
+        }
       }
     }
+    const uint32_t h0 = e4m3x2_to_f16x2((uint16_t)s[0]), h1 = e4m3x2_to_f16x2((uint16_t)s[1]);
+    pairs[lane] = __byte_perm(h0, h1, 0x5410);
+    pairs[32 + lane] = __byte_perm(h0, h1, 0x7632);
+    __syncwarp();
+  }
+  const uint32_t* sp = pairs + (g >> 2) * 32 + 2 * c;
+  uint32_t lo[16], hi[16];
+#pragma unroll
+  for (int qq = 0; qq < 4; ++qq) {             // keys 64 half + 16 qq + 4 c + 0..3
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u[i] = *reinterpret_cast<const uint16_t*>(codes + (16 * qq + i) * kFp4Row);
+    const uint2 s = *reinterpret_cast<const uint2*>(sp + 8 * qq);
     const uint32_t a = __byte_perm(u[0], u[2], 0x5410), b = __byte_perm(u[1], u[3], 0x5410);
     const uint32_t even = (a & m) | ((b << 4) & ~m), odd = ((a >> 4) & m) | (b & ~m);
-    const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(s[0] | s[1] << 8));
-    const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(s[2] | s[3] << 8));
-    uint32_t e[4], o[4];                     // dims 0, 2 | 1, 3 of keys 0 1, then of 2 3
+    uint32_t e[4], o[4];                       // dims 0, 2 | 1, 3 of keys 0 1, then of 2 3
     e2m1x8_to_f16x2(even, e);
     e2m1x8_to_f16x2(odd, o);
-    lo[4 * qq] = hmul2_u32(e[0], s01);
-    lo[4 * qq + 1] = hmul2_u32(e[2], s23);
-    lo[4 * qq + 2] = hmul2_u32(o[0], s01);
-    lo[4 * qq + 3] = hmul2_u32(o[2], s23);
-    hi[4 * qq] = hmul2_u32(e[1], s01);
-    hi[4 * qq + 1] = hmul2_u32(e[3], s23);
-    hi[4 * qq + 2] = hmul2_u32(o[1], s01);
-    hi[4 * qq + 3] = hmul2_u32(o[3], s23);
+    lo[4 * qq] = hmul2_u32(e[0], s.x);
+    lo[4 * qq + 1] = hmul2_u32(e[2], s.y);
+    lo[4 * qq + 2] = hmul2_u32(o[0], s.x);
+    lo[4 * qq + 3] = hmul2_u32(o[2], s.y);
+    hi[4 * qq] = hmul2_u32(e[1], s.x);
+    hi[4 * qq + 1] = hmul2_u32(e[3], s.y);
+    hi[4 * qq + 2] = hmul2_u32(o[1], s.x);
+    hi[4 * qq + 3] = hmul2_u32(o[3], s.y);
   }
   tmem_st_16x256_x4(taddr, lo);
   tmem_st_16x256_x4(taddr + (16u << 16), hi);
@@ -383,7 +394,7 @@ struct Shape {
   static constexpr int kMiscRegs = TEAMS >= 3 ? 48 : 56;
   // TMEM columns of a team: K (64 dims) | V | S | O
   static constexpr int kCols = 96 + 2 * kN;
-  static constexpr int kFit = (222 * 1024 / kTeams - 3 * kN * kHeadDim * 2) / kPageBytes;
+  static constexpr int kFit = (218 * 1024 / kTeams - 3 * kN * kHeadDim * 2) / kPageBytes;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kOperand = kN * kHeadDim * 2;              // a Q buffer, and P
   static constexpr int kTeamSmem = 3 * kOperand + kStages * kPageBytes;
@@ -399,6 +410,7 @@ struct TeamShared {
   using S = Shape<NG, TEAMS>;
   float red[4][S::kN];         // per warp: row maxima, row sums
   float alpha[S::kN], ref[S::kN];              // rescaling, final references
+  uint32_t pairs[4][64];       // per warp: scales of V (value_half)
   uint64_t full_bar[S::kStages], empty_bar[S::kStages];
   uint64_t q_free[2];          // Q buffer free again
   uint64_t k_ready, k_free;    // a half of K written (two a tile); the first half read
@@ -690,15 +702,13 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       }
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const uint8_t* vt = ring + stage * kPageBytes;
-      if (all >= kBlock) value_half<false>(vt, tv, 0, w, lane, ntok, all);
-      else value_half<true>(vt, tv, 0, w, lane, ntok, all);
+      value_half(vt, tv, 0, sh.pairs[w], w, lane, ntok, all);
       mbar_wait(&sh.k_free, ph, ws.hdr);
       tc_fence_after();
       key_half(kt, tk, 1);
       written(&sh.k_ready);
       if (lane == 0) mbar_arrive(&sh.empty_bar[kst]);
-      if (all >= kBlock) value_half<false>(vt, tv + 32, 1, w, lane, ntok, all);
-      else value_half<true>(vt, tv + 32, 1, w, lane, ntok, all);
+      value_half(vt, tv + 32, 1, sh.pairs[w], w, lane, ntok, all);
       if (all < kBlock) {
         if (ttid >= all && ttid < ntok) {      // NaN scales that only later tokens see
           unsigned bad = 0;
