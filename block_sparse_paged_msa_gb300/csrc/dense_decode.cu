@@ -37,15 +37,15 @@
 // transposes the probabilities into the B operand.  K passes through TMEM in
 // two halves, in turns with V's: 128 columns a team, four teams an SM.
 //
-// What bounds it.  32 requests of 8k-32k tokens, 64 + 8 heads (754 MB): 142 us,
-// 5.3 TB/s, 0.79 of the measured copy bandwidth; per page and SM about 1000
-// cycles, 670 of them issue slots (2680 warp instructions: 1024 conversions
-// and scalings that nothing can leave out), the rest the waits of a tile's
-// chain that four teams do not cover.  With mma.sync in place of tcgen05 the
-// same dequantisation took 192 us: an mma.sync holds the issue port for about
-// 8 cycles, 256 of them a page.  16 requests of 32772 tokens with 4 new ones
-// each (32 rows): 166 us, 3.7 TB/s, against 295 us by mma.sync.  Two requests
-// of 1.5k tokens, one head: 8 us, the chain of one tile and two launches.
+// What bounds it.  32 requests of 8k-32k tokens, 64 + 8 heads (754 MB): 140 us,
+// 5.4 TB/s, 0.81 of the measured copy bandwidth; a page takes an SM about 1000
+// cycles, of them 630 issue slots a scheduler (2510 warp instructions, 1024 of
+// them the conversions and scalings of its 32768 codes), the rest waits of a
+// tile's chain that four teams do not cover.  The same dequantisation in front
+// of mma.sync took 192 us: an mma.sync holds its scheduler for about 8 cycles,
+// 64 of them a page and warp.  16 requests of 32772 tokens with 4 new ones each
+// (32 rows): 150 us, 4.0 TB/s, against 295 us by mma.sync.  Two requests of
+// 1.5k tokens, one head: 8 us, the chain of one tile and two launches.
 #include <atomic>
 
 #include "tcgen05.cuh"
@@ -148,7 +148,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const WsView& ws, const DenseArgs& a, int lane = 0) {
     if (u >= end) return false;
     const uint32_t Hkv = a.Hkv;
-    uint32_t cu0 = ws.req_cu_nb[r], cu1 = ws.req_cu_nb[r + 1];   // u is below the last request's end
+    uint32_t cu0 = ws.req_cu_nb[r], cu1 = ws.req_cu_nb[r + 1];   // u is before the last one's end
     while (cu1 * Hkv <= u) {
       ++r;
       cu0 = cu1;
@@ -867,7 +867,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         if (part == 0)
           a.lse[row] = sum == 0.f ? -INFINITY : (sh.ref[n] + log2f(sum) - kBias) * kLn2;
       } else {
-        float4* dst = reinterpret_cast<float4*>(a.o_part + (slot * a.rows + n) * kHeadDim + 8 * part);
+        float4* dst =
+            reinterpret_cast<float4*>(a.o_part + (slot * a.rows + n) * kHeadDim + 8 * part);
         dst[0] = y0;
         dst[1] = y1;
         if (part == 0) a.ml_part[slot * a.rows + n] = make_float2(sh.ref[n], sum);
@@ -1001,8 +1002,8 @@ msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cuda
   if (grid <= 0) return MSA_ERR_CUDA;
   if (grid > units) grid = units;
   const int teams = (int)grid * S::kTeams;
-  msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS>, dim3((unsigned)grid), dim3(S::kThreads),
-                             S::kSmem, s, v, a);
+  msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS>, dim3((unsigned)grid),
+                             dim3(S::kThreads), S::kSmem, s, v, a);
   if (st != MSA_OK) return st;
   int64_t blocks = (int64_t)teams * ((a.rows + kMergeRows - 1) / kMergeRows);
   if (blocks > 4 * sms) blocks = 4 * sms;
@@ -1063,17 +1064,17 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   const int64_t units = (int64_t)cfg->max_batch * cfg->max_blocks_per_req * a.Hkv;
   if (units > 0x7fffffff) return MSA_ERR_UNSUPPORTED;   // units are counted in 32 bits
   cudaStream_t s = (cudaStream_t)stream;
-  // Teams an SM.  A fourth one hides more of a tile's chain of waits (32
-  // requests of 8k-32k tokens, 8 heads: 142 us, with three 155 us); but it cuts
-  // a short step into more partials and prefetches less of each range (61
-  // requests of up to 6001 tokens, one head: 23 us, with three 19 us; two
-  // requests of 1.5k: 8.7 and 8.0 us).  One request of 131071 tokens, 54 pages
-  // an SM, takes 42 us either way.  32 rows fit three teams, 64 rows two (TMEM).
-  const bool many = units >= (int64_t)64 * sm_count();
-  if (a.rows <= 8)
-    return many ? launch_dense<1, 4>(v, a, units, s) : launch_dense<1, 3>(v, a, units, s);
+  // Teams an SM: as many as TMEM holds, four up to 16 rows, three up to 32, two
+  // up to 64.  With 9 to 16 rows a fourth team pays off only on long steps
+  // (32 requests of 16384 tokens, 8 heads, 216 pages an SM: 130 us, with three
+  // 135 us) and costs time on short ones (8 requests, 54 pages an SM: 46 and
+  // 42 us; 61 requests of up to 6001 tokens, one head: 22 and 18 us); the limit
+  // lies between, in pages of the config's largest step.  Up to 8 rows four
+  // teams are never slower (216 pages an SM: 114 and 122 us; 54: 38 and 38 us).
+  if (a.rows <= 8) return launch_dense<1, 4>(v, a, units, s);
   if (a.rows <= 16)
-    return many ? launch_dense<2, 4>(v, a, units, s) : launch_dense<2, 3>(v, a, units, s);
+    return units >= (int64_t)128 * sm_count() ? launch_dense<2, 4>(v, a, units, s)
+                                              : launch_dense<2, 3>(v, a, units, s);
   if (a.rows <= 32) return launch_dense<4, 3>(v, a, units, s);
   return launch_dense<8, 2>(v, a, units, s);
 }
