@@ -791,20 +791,22 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
           tmem_st_wait();
         }
       }
-      // ---- P = 2^(s' - m + bias) as the B operand [row][key]
+      // ---- P = 2^(s' - m + bias) as the B operand [row][key].  s' is rounded as
+      // it was for m (no fma), and bias - m downwards: so P stays within fp16 for
+      // scores past 2^24 too, where a step of fp32 is more than the slack.
       const uint64_t sl = f2(a.scale_log2, a.scale_log2);
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const uint64_t off = f2(kBias - (m[i][0] == -INFINITY ? 0.f : m[i][0]),
-                                kBias - (m[i][1] == -INFINITY ? 0.f : m[i][1]));
+        const uint64_t off = f2(__fsub_rd(kBias, m[i][0] == -INFINITY ? 0.f : m[i][0]),
+                                __fsub_rd(kBias, m[i][1] == -INFINITY ? 0.f : m[i][1]));
         uint64_t sum = f2(l[i][0], l[i][1]);
         uint32_t p[4];
 #pragma unroll
         for (int o = 0; o < 4; ++o) {          // keys 8 o + g
           float p0, p1;
-          f2_split(fma_f2(f2u(x[o >> 1][4 * i + 2 * (o & 1)], x[o >> 1][4 * i + 2 * (o & 1) + 1]),
-                          sl, off),
-                   p0, p1);
+          const uint64_t s2 =
+              f2u(x[o >> 1][4 * i + 2 * (o & 1)], x[o >> 1][4 * i + 2 * (o & 1) + 1]);
+          f2_split(add_f2(mul_f2(s2, sl), off), p0, p1);
           p0 = ex2_approx(p0);
           p1 = ex2_approx(p1);
           sum = add_f2(sum, f2(p0, p1));
@@ -1050,6 +1052,7 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   a.max_batch = cfg->max_batch;
   a.rows = a.G * a.q_len;
   a.scale_log2 = cfg->softmax_scale * cfg->k_scale * kLog2e;
+  if (!(a.scale_log2 > 0.f && a.scale_log2 < INFINITY)) return MSA_ERR_INVALID_ARG;
   a.v_scale = cfg->v_scale;
   a.q = (const __nv_bfloat16*)q;
   a.k_pool = (const uint8_t*)k_pages;

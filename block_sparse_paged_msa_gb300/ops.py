@@ -411,6 +411,8 @@ def _layout(cfg) -> _Layout:
     key = bytes(cfg)
     v = _LAYOUTS.get(key)
     if v is None:
+        if len(_LAYOUTS) >= 256:            # a program of ever new configs
+            _LAYOUTS.clear()
         v = _LAYOUTS[key] = _Layout(cfg)
     return v
 

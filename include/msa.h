@@ -284,7 +284,8 @@ typedef struct msa_rope {
  * position lies outside the table is skipped and sets MSA_DEVERR_POSITION; a
  * slot outside the pool leaves the pools as they are (q_out and idx_q_out are
  * written) and sets MSA_DEVERR_PAGE_RANGE.  Pointers 16-byte aligned.  Either
- * mode, every KV dtype.
+ * mode, every KV dtype; MSA_ERR_UNSUPPORTED if max tokens * head rows of a token
+ * reach 2^31.
  */
 msa_status msa_rope_cache_write(const msa_config* cfg, void* ws, const msa_rope* rope,
                                 const void* q, const void* k, const void* v, const void* idx_q,
@@ -416,11 +417,12 @@ msa_status msa_paged_decode(const msa_config* cfg, void* ws, const void* q, cons
  *   scratch  msa_dense_decode_scratch_bytes(cfg) bytes, 256-byte aligned, no
  *            initialisation needed; calls that overlap on the GPU need one each
  *   out [T, H_q, D] bf16 (16-byte aligned), lse [T, H_q] float
- * NVFP4 KV only, and H_q / H_kv * q_len <= 64, else MSA_ERR_UNSUPPORTED.  A
- * request with more new tokens than cfg->q_len (possible through cu_seqlens_q)
- * sets MSA_DEVERR_SEQ_LEN; it and idle requests get out = 0, lse = -inf.  Pages
- * that the plan flagged are skipped.  Rows of out and lse from T on are left as
- * they are.
+ * NVFP4 KV only, H_q / H_kv * q_len <= 64 and max_batch * max_blocks_per_req *
+ * H_kv < 2^31, else MSA_ERR_UNSUPPORTED; softmax_scale * k_scale has to be a
+ * positive finite float.  A request with more new tokens than cfg->q_len
+ * (possible through cu_seqlens_q) sets MSA_DEVERR_SEQ_LEN; it and idle requests
+ * get out = 0, lse = -inf.  Pages that the plan flagged are skipped.  Rows of
+ * out and lse from T on are left as they are.
  */
 size_t msa_dense_decode_scratch_bytes(const msa_config* cfg);
 msa_status msa_dense_decode(const msa_config* cfg, void* ws, const void* q, const void* k_pages,

@@ -66,6 +66,28 @@ def test_refused_on_the_host():
     assert call(_cfg(8, 1, 2, 8, 16, mode="prefill", max_q_tokens=64), good) == INVALID
 
 
+def test_limits_refused_on_the_host():
+    P, lib = ctypes.c_void_p, ops.lib()
+
+    def call(c):
+        return lib.msa_dense_decode(ctypes.byref(c), *[P(256)] * 7, None)
+
+    # units (pages x KV heads of the largest step) are counted in 31 bits
+    assert call(_cfg(8, 8, 65536, 8192, 16)) == UNSUPPORTED
+    # softmax_scale * k_scale: 0 or infinite in fp32
+    assert call(_cfg(8, 1, 2, 8, 16, softmax_scale=1e-30, k_scale=1e-30)) == INVALID
+    assert call(_cfg(8, 1, 2, 8, 16, softmax_scale=1e30, k_scale=1e30)) == INVALID
+    # a config of no requests has nothing to do
+    assert call(_cfg(8, 1, 0, 8, 16)) == 0
+    assert call(_cfg(8, 1, 0, 8, 16, max_q_tokens=4)) == 0
+
+
+def test_layouts_of_many_configs_are_not_kept_for_ever():
+    for n in range(600):
+        ops._layout(_cfg(8, 1, 2, 8, 16 + n))
+    assert len(ops._LAYOUTS) <= 256
+
+
 # ------------------------------------------------------------ oracle pin (CPU)
 def test_oracle_dense_attention_is_the_sparse_one_over_every_block():
     spec = wl.small("nvfp4_decode", batch=2, seq_len_range=(300, 700), num_pages=16,
@@ -337,6 +359,60 @@ def test_repeats_and_graph_replays_are_bit_equal():
         torch.cuda.synchronize()
         assert msa.check_device_error(d.ws) == 0
         assert torch.equal(d.out, eager.out) and torch.equal(d.lse, eager.lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,q_len,L", [(8, 1, 1, 900), (16, 1, 1, 70000), (8, 1, 4, 5000),
+                                            (16, 1, 4, 300)])
+def test_scores_past_24_bits(hq, hkv, q_len, L):
+    """Scores of 10^8, where a step of fp32 is more than any bias of the exponent.
+    The first key is 2688 in every dim, with the signs of q; no other is larger
+    than 6 there, so that this key has all the weight and the output is its
+    value, rounded once."""
+    c = Case(hq, hkv, [L], q_len=q_len, seed=21)
+    c.q.copy_(torch.sign(c.q.float()) * 16384.0)
+    c.q[c.q == 0] = 16384.0
+    c.q[:] = c.q[:1, :1].clone()                           # all queries alike
+    page = int(c.block_table[0, 0])
+    sign = (to_np(c.q[0, 0]) < 0).astype(np.uint8)
+    codes = 7 + 8 * sign                                   # +-6
+    c.pool[page, 0, 0, :64] = torch.from_numpy(codes[0::2] + 16 * codes[1::2]).cuda()
+    c.pool[page, 0, 0, 64:] = 0x7e                         # 448
+    d = c.run()
+    torch.cuda.synchronize()
+    assert msa.check_device_error(d.ws) == 0
+    v = oracle.nvfp4_dequant(c.pool[page].cpu().numpy()[None], 128)[0] * c.cfg.v_scale
+    want = oracle.bf16_round(v[1, 0].astype(np.float32))
+    got = to_np(d.out)
+    assert np.array_equal(got, np.broadcast_to(want, got.shape))
+    top = 128 * 16384.0 * 2688 * c.cfg.k_scale * c.cfg.softmax_scale
+    # the score's products and sums, the scale and its rounding, ln 2's: 2^-24 each
+    assert np.all(np.abs(to_np(d.lse) - top) <= (128 + 4) * 2.0 ** -24 * top)
+
+
+@pytest.mark.gpu
+def test_two_graphs_that_share_their_buffers():
+    """Two captured steps of one layer's buffers (workspace, scratch, output),
+    replayed in any order on one stream."""
+    a, b = (Case(8, 2, lens, seed=s, max_blocks=40, extra_pages=e) for s, lens, e in
+            ((30, [5000, 40, 700], 3), (31, [3, 2900, 1], 25)))
+    assert bytes(a.cfg) == bytes(b.cfg)
+    for x in (a, b):
+        x.want = x.run()
+    d = a.layer()
+    graphs = []
+    for x in (a, b):
+        x.run(d)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.run(d)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        d.out.fill_(7.0)
+        graphs[i].replay()
+        want = (a, b)[i].want
+        assert torch.equal(d.out, want.out) and torch.equal(d.lse, want.lse)
 
 
 @pytest.mark.gpu

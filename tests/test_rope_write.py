@@ -92,6 +92,18 @@ def test_refused_on_the_host(bad, status):
     assert _call(cfg, _args(**bad)) == UNSUPPORTED           # the config is checked first
 
 
+def test_limits_refused_on_the_host():
+    """Head rows of the largest step are counted in 31 bits."""
+    kw = dict(init_blocks=1, local_blocks=1, topk_blocks=1, index_dim=64, max_batch=1,
+              max_blocks_per_req=8192, num_pages=8192)
+    cfg = msa.make_config(num_q_heads=1024, num_kv_heads=1024, max_q_tokens=1 << 20, **kw)
+    wide = 1024 * 128
+    assert _call(cfg, _args(qs=wide, ks=wide, vs=wide, iqs=wide, iks=wide)) == UNSUPPORTED
+    cfg.max_batch = 0                          # a config of no tokens has nothing to do
+    cfg.max_q_tokens = 0
+    assert _call(cfg, _args(qs=wide, ks=wide, vs=wide, iqs=wide, iks=wide)) == 0
+
+
 def test_rows_layouts_refused_by_the_binding():
     with pytest.raises(ValueError, match="CUDA"):
         ops._expect_rows(torch.zeros(2, 1, 128, dtype=torch.bfloat16), "q", (2, 1, 128), 0)
