@@ -898,34 +898,45 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 // partials then get a whole block each.
 constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
 constexpr int kMergeRows = 2, kRowWarps = kMergeWarps / kMergeRows;
+constexpr int kMergeChunks = (kTeamsMax + kMergeThreads - 1) / kMergeThreads;
 constexpr int kMany = 32;
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a, int teams) {
   __shared__ int4 list[kTeamsMax];
   __shared__ int owner[kTeamsMax];
-  __shared__ int counts[kMergeWarps], many;
+  __shared__ int counts[kMergeChunks * kMergeWarps], many;
   __shared__ float4 part[kMergeWarps][32];
   __shared__ float part_l[kMergeWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  int n = 0;
+  int4 rec[kMergeChunks];
+  unsigned starts[kMergeChunks];
+#pragma unroll
+  for (int k = 0; k < kMergeChunks; ++k) {          // all loads in flight together
+    const int c = k * kMergeThreads + tid;
+    rec[k] = c < teams ? a.split[c] : make_int4(0, 0, 0, 0);
+  }
   if (tid == 0) many = 0;
-  for (int c0 = 0; c0 < teams; c0 += kMergeThreads) {
-    const int c = c0 + tid;
-    const int4 rec = c < teams ? a.split[c] : make_int4(0, 0, 0, 0);
-    const unsigned any = __ballot_sync(0xffffffffu, rec.x > 0);
-    __syncthreads();
-    if (lane == 0) counts[warp] = __popc(any);
-    __syncthreads();
-    int at = n + __popc(any & ((1u << lane) - 1u));
+#pragma unroll
+  for (int k = 0; k < kMergeChunks; ++k) {
+    starts[k] = __ballot_sync(0xffffffffu, rec[k].x > 0);
+    if (lane == 0) counts[k * kMergeWarps + warp] = __popc(starts[k]);
+  }
+  __syncthreads();
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < kMergeChunks; ++k) {
+    int at = n + __popc(starts[k] & ((1u << lane) - 1u));
+#pragma unroll
     for (int i = 0; i < kMergeWarps; ++i) {
-      if (i < warp) at += counts[i];
-      n += counts[i];
+      const int cnt = counts[k * kMergeWarps + i];
+      if (i < warp) at += cnt;
+      n += cnt;
     }
-    if (rec.x > 0) {
-      list[at] = rec;
-      owner[at] = c;
-      if (rec.x > kMany) many = 1;
+    if (rec[k].x > 0) {
+      list[at] = rec[k];
+      owner[at] = k * kMergeThreads + tid;
+      if (rec[k].x > kMany) many = 1;
     }
   }
   __syncthreads();
