@@ -38,13 +38,13 @@
 // two halves, in turns with V's: 128 columns a team, four teams an SM.
 //
 // What bounds it.  32 requests of 8k-32k tokens, 64 + 8 heads (754 MB): 140 us,
-// 5.4 TB/s, 0.81 of the measured copy bandwidth; a page takes an SM about 1000
-// cycles, of them 630 issue slots a scheduler (2510 warp instructions, 1024 of
+// 5.4 TB/s, 0.80 of the measured copy bandwidth; a page takes an SM about 1000
+// cycles, of them 655 issue slots a scheduler (2620 warp instructions, 1024 of
 // them the conversions and scalings of its 32768 codes), the rest waits of a
 // tile's chain that four teams do not cover.  The same dequantisation in front
 // of mma.sync took 192 us: an mma.sync holds its scheduler for about 8 cycles,
 // 64 of them a page and warp.  16 requests of 32772 tokens with 4 new ones each
-// (32 rows): 150 us, 4.0 TB/s, against 295 us by mma.sync.  Two requests of
+// (32 rows): 152 us, 4.0 TB/s, against 295 us by mma.sync.  Two requests of
 // 1.5k tokens, one head: 8 us, the chain of one tile and two launches.
 #include <atomic>
 
@@ -894,8 +894,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 
 // Merges the partials of the (request, head) groups that lie in several teams'
 // ranges, in team order.  Every block lists the split groups in order, then
-// takes its share of (group, two rows), four warps a row; rows of many
-// partials then get a whole block each.
+// takes its share of (group, two rows), four warps a row.  Rows of more than
+// kMany partials then get a whole block each: one request of 131071 tokens, 76
+// partials a row, 39.5 us in all against 41.6 without; from 9 partials on it
+// costs time instead, 61 requests of up to 6001 tokens 20.8 us against 18.0.
 constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
 constexpr int kMergeRows = 2, kRowWarps = kMergeWarps / kMergeRows;
 constexpr int kMergeChunks = (kTeamsMax + kMergeThreads - 1) / kMergeThreads;
