@@ -428,6 +428,81 @@ def test_another_stream():
 
 
 @pytest.mark.gpu
+def test_two_calls_at_once():
+    """Two layers with their own buffers on two streams."""
+    cases = [Case(8, 2, [9000, 40, 3000], seed=40), Case(16, 2, [2500, 6000], q_len=3, seed=41)]
+    want = [c.run() for c in cases]
+    layers = [c.layer() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for c, d, st in zip(cases, layers, streams):
+            d.run(c.seq_lens, c.block_table, c.q, c.pool, c.pool, stream=st)
+    torch.cuda.synchronize()
+    for d, w in zip(layers, want):
+        assert msa.check_device_error(d.ws) == 0
+        assert torch.equal(d.out, w.out) and torch.equal(d.lse, w.lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,q_len", [(8, 1, 1), (16, 2, 2)])
+def test_a_nan_query_stays_in_its_row(hq, hkv, q_len):
+    c = Case(hq, hkv, [6000, 70, 1 + q_len], q_len=q_len, seed=42)
+    want = c.run()
+    rows = [(0, 1), (q_len, hq - 1), (2 * q_len, 0)]
+    for t, h in rows:
+        c.q[t, h, 17] = float("nan")
+    d = c.run()
+    assert msa.check_device_error(d.ws) == 0
+    clean = torch.ones_like(d.lse, dtype=torch.bool)
+    for t, h in rows:
+        clean[t, h] = False
+        assert bool(d.out[t, h].isnan().all()) and bool(d.lse[t, h].isnan())
+    assert torch.equal(d.out[clean], want.out[clean])
+    assert torch.equal(d.lse[clean], want.lse[clean])
+
+
+@pytest.mark.gpu
+def test_a_captured_step_of_growing_requests():
+    """One graph of rotate, append, attend; between replays the requests grow by
+    a token each, across page ends, in the same buffers."""
+    c = Case(8, 2, [126, 255, 1, 700], seed=43, max_blocks=8)
+    free = c.cfg.num_pages - sum(-(-n // 128) for n in c.lens)
+    assert free == 3                                 # the pages the first three grow into
+    spare = sorted(set(range(c.cfg.num_pages)) - set(c.block_table[c.block_table >= 0].tolist()))
+    table = c.block_table.clone()
+    table[0, 1], table[1, 2], table[2, 1] = spare
+    c.pool[spare, :, :, 64:] = 0x30
+    tab = torch.randn((1024, 64), device="cuda").clamp(-1, 1)
+    g = torch.Generator(device="cuda").manual_seed(44)
+    new = [torch.randn((4, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+           for _ in range(2)]
+    d = msa.DenseAttention(c.cfg, rope=msa.Rope(tab, interleaved=True))
+    e = msa.DenseAttention(c.cfg, rope=msa.Rope(tab, interleaved=True))
+    pool2 = c.pool.clone()
+
+    def step(layer, pool):
+        layer.run(c.seq_lens, table, c.q, pool, pool, new_kv=new)
+
+    step(d, c.pool)                                  # the first step, eagerly on both
+    step(e, pool2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(d, c.pool)
+    for _ in range(6):
+        c.seq_lens += 1
+        for x in (*new, c.q):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda").to(torch.bfloat16))
+        graph.replay()
+        step(e, pool2)
+        torch.cuda.synchronize()
+        assert msa.check_device_error(d.ws) == 0 and msa.check_device_error(e.ws) == 0
+        assert torch.equal(d.out, e.out) and torch.equal(d.lse, e.lse)
+        assert torch.equal(c.pool, pool2)
+
+
+@pytest.mark.gpu
 def test_pages_past_4_gib():
     """Pages whose byte offset in the pool passes 2^32."""
     c = Case(8, 8, [700], seed=12)

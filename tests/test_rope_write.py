@@ -301,3 +301,65 @@ def test_sparse_step_with_a_rope_equals_rotation_then_write(name):
     assert torch.equal(a.out[:T], b.out[:T]) and torch.equal(a.lse[:T], b.lse[:T])
     with pytest.raises(ValueError, match="new_kv"):
         a.run(w1.seq_lens, w1.block_table, iq, w1.idx_k_pages, q, w1.k_pages, w1.v_pages)
+
+
+@pytest.mark.gpu
+def test_dense_sparse_step_with_a_rope():
+    """The compacted form of the step takes the rotated queries too."""
+    spec = wl.small("medium_decode", batch=3)
+    cfg = msa.config_for(spec)
+    runs = []
+    for dense_sparse in (False, True):
+        w = wl.make_workload(spec, device="cuda")
+        q, k, v, iq, ik, _ = _fused(spec, w.num_tokens, 25)
+        sa = msa.SparseAttention(cfg, dense_sparse=dense_sparse,
+                                 rope=msa.Rope(_table(int(w.seq_lens.max()), 128)))
+        sa.run(w.seq_lens, w.block_table, iq, w.idx_k_pages, q, w.k_pages, w.v_pages,
+               new_kv=(k, v, ik))
+        torch.cuda.synchronize()
+        assert msa.check_device_error(sa.ws) == 0
+        runs.append(sa)
+    a, b = runs
+    T = w.num_tokens
+    assert torch.equal(a.selected[:T], b.selected[:T])
+    # the same keys, in splits of their own: the bound of the dense-sparse form
+    assert (a.out[:T].float() - b.out[:T].float()).abs().max() <= 1e-2
+    assert (a.lse[:T] - b.lse[:T]).abs().max() <= 1e-3
+
+
+@pytest.mark.gpu
+def test_token_strides_and_pools_past_32_bits():
+    """Rows 2^31 elements apart, and pages whose byte offset passes 2^32."""
+    pages = 140000                                 # of 32 KiB
+    far = [139999, 131072]
+    cfg = msa.make_config(num_q_heads=2, num_kv_heads=1, init_blocks=0, local_blocks=1,
+                          topk_blocks=1, index_dim=64, max_batch=2, max_blocks_per_req=1,
+                          num_pages=pages)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    wide = torch.empty((1 << 31) + 1024, dtype=torch.bfloat16, device="cuda")
+    rows = torch.randn((2, 4, 128), generator=g, device="cuda").to(torch.bfloat16)
+    fused = wide.as_strided((2, 4, 128), (1 << 31, 128, 1))
+    fused.copy_(rows)
+    q, k, v = fused[:, :2], fused[:, 2:3], fused[:, 3:]
+    tab = _table(128, 128)
+    kp, vp = (torch.zeros((pages, 1, 128, 128), dtype=torch.bfloat16, device="cuda")
+              for _ in range(2))
+    ws = torch.empty(msa.workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    q_out = torch.empty((2, 2, 128), dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([5, 128], dtype=torch.int32, device="cuda")
+    table = torch.tensor(far, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    msa.plan(cfg, lens, table, ws)
+    msa.rope_cache_write(cfg, ws, q, k, v, None, None, tab, q_out, None, kp, vp, None)
+    assert msa.check_device_error(ws) == 0
+    cs = tab[[4, 127]].cpu().numpy()
+
+    def turned(x):
+        return oracle.bf16_round(oracle.rotate_rows(to_np(x), cs[:, :64], cs[:, 64:], False))
+
+    assert np.array_equal(to_np(q_out), turned(rows[:, :2]))
+    for t, (page, row) in enumerate(zip(far, (4, 127))):
+        assert np.array_equal(to_np(kp[page, 0, row]), turned(rows[:, 2:3])[t, 0])
+        assert np.array_equal(to_np(vp[page, 0, row]), to_np(rows[t, 3]))
+        for x in (kp, vp):
+            assert int((x[page] != 0).any(-1).sum()) == 1
+    assert int((kp != 0).any(-1).sum()) == 2 and int((vp != 0).any(-1).sum()) == 2
