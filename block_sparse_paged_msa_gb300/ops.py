@@ -130,6 +130,7 @@ def _check(fn: str, status: int, detail: str = ""):
 
 # the current stream's handle without building a Stream object (2.9 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None) -> int:
@@ -404,6 +405,7 @@ class _Layout:
 
 
 _LAYOUTS = {}
+_Tensor = torch.Tensor
 _BF16, _F32, _I64, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int64,), (torch.uint8,)
 
 
@@ -418,7 +420,7 @@ def _layout(cfg) -> _Layout:
 
 
 def _device_of(t, name) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.get_device()
 
@@ -426,12 +428,23 @@ def _device_of(t, name) -> int:
 def _expect(t, name, dtypes, shape, dev) -> int:
     """The pointer of a contiguous tensor of one of `dtypes` on device `dev`, of
     `shape` or with more rows; ValueError otherwise (the reason by _need)."""
-    if isinstance(t, torch.Tensor):
+    if (isinstance(t, _Tensor) and t.dtype in dtypes and t.is_contiguous()
+            and t.get_device() == dev):
         s = t.shape
-        if ((s == shape or (len(s) == len(shape) and s[0] >= shape[0] and s[1:] == shape[1:]))
-                and t.dtype in dtypes and t.is_contiguous() and t.get_device() == dev):
+        if s == shape or (len(s) == len(shape) and s[0] >= shape[0] and s[1:] == shape[1:]):
             return t.data_ptr()
     _need(t, name, dtypes, len(shape), shape[0], shape[1:])
+    raise ValueError(f"{name} is on another device than the step's other tensors")
+
+
+def _expect_table(t, name, dev):
+    """Pointer, rows and width of a contiguous fp32 table."""
+    if (isinstance(t, _Tensor) and t.dtype is torch.float32 and t.is_contiguous()
+            and t.get_device() == dev):
+        s = t.shape
+        if len(s) == 2:
+            return t.data_ptr(), s[0], s[1]
+    _need(t, name, torch.float32, 2)
     raise ValueError(f"{name} is on another device than the step's other tensors")
 
 
@@ -439,16 +452,16 @@ def _expect_rows(t, name, shape, dev):
     """Pointer and token stride (elements) of a projection's bf16 rows [T, heads,
     width] or more: heads contiguous, tokens at any stride that is a multiple
     of 8."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if not isinstance(t, _Tensor) or t.get_device() != dev:
+        if not isinstance(t, _Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on another device than the step's other tensors")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
     T, heads, width = shape
     s = t.shape
     if s != shape and (len(s) != 3 or s[0] < T or s[1:] != shape[1:]):
         raise ValueError(f"{name} has shape {tuple(s)}, the config needs {shape}")
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on another device than the step's other tensors")
     tok, hd, el = t.stride()
     ptr = t.data_ptr()
     if el != 1 or (heads > 1 and hd != width) or (T > 1 and tok % 8) or ptr % 16:
@@ -460,12 +473,13 @@ def _expect_rows(t, name, shape, dev):
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with device `dev` current, on `stream` or its current
     stream."""
-    if stream is not None and stream.device.index != dev:
+    if stream is None:
+        if _raw_stream is not None and dev == _device():
+            return fn(*args, _raw_stream(dev))
+    elif stream.device.index != dev:
         raise ValueError(f"the stream is on device {stream.device.index}, the tensors on {dev}")
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return fn(*args, _stream(stream))
-    return fn(*args, _stream(stream))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(stream))
 
 
 def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, k_pages, v_pages,
@@ -484,12 +498,10 @@ def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, 
     p_q, s_q = _expect_rows(q, "q", y.q, dev)
     p_k, s_k = _expect_rows(k, "k", y.kv, dev)
     p_v, s_v = _expect_rows(v, "v", y.kv, dev)
-    rows, rot = _table_shape(cos_sin, "cos_sin")
-    p_cs = _expect(cos_sin, "cos_sin", _F32, (rows, rot), dev)
+    p_cs, rows, rot = _expect_table(cos_sin, "cos_sin", dev)
     p_ics, irot = None, rot
     if idx_cos_sin is not None:
-        n, irot = _table_shape(idx_cos_sin, "idx_cos_sin")
-        p_ics = _expect(idx_cos_sin, "idx_cos_sin", _F32, (n, irot), dev)
+        p_ics, n, irot = _expect_table(idx_cos_sin, "idx_cos_sin", dev)
         rows = min(rows, n)
     p_iq = p_ik = p_iv = p_iqo = p_ikp = p_ivp = None
     s_iq = s_ik = s_iv = 0
@@ -515,12 +527,6 @@ def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, 
                _expect(v_pages, "v_pages", y.kv_dtypes, y.pool, dev), p_ikp, p_ivp)
     if st:
         _check("msa_rope_cache_write", st)
-
-
-def _table_shape(t, name):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a [positions, rotary_dim] tensor")
-    return t.shape
 
 
 def index_attention_scratch_bytes(cfg) -> int:
