@@ -1086,7 +1086,8 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   // 135 us) and costs time on short ones (8 requests, 54 pages an SM: 46 and
   // 42 us; 61 requests of up to 6001 tokens, one head: 22 and 18 us); the limit
   // lies between, in pages of the config's largest step.  Up to 8 rows four
-  // teams are never slower (216 pages an SM: 114 and 122 us; 54: 38 and 38 us).
+  // teams cost next to nothing on short ones (216 pages an SM: 114 and 122 us;
+  // 54: 37.9 and 38.3; 2 requests of 1.5k tokens, one head: 8.1 and 8.0).
   if (a.rows <= 8) return launch_dense<1, 4>(v, a, units, s);
   if (a.rows <= 16)
     return units >= (int64_t)128 * sm_count() ? launch_dense<2, 4>(v, a, units, s)

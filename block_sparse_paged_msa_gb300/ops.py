@@ -491,7 +491,7 @@ def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, 
     idx_q, idx_k, idx_v [T, H_kv, d] bf16 with any token stride (slices of a
     fused projection), idx_* may be None.  cos_sin [positions, rotary_dim]
     fp32: cosines, then sines; idx_cos_sin the index heads' own table, None =
-    cos_sin.  q_out, idx_q_out: the rotated queries, contiguous; each may be its
+    cos_sin, one of width 0 = their rows are not rotated.  q_out, idx_q_out: the rotated queries, contiguous; each may be its
     input.  positions: [T] int64, None = the plan's."""
     y = _layout(cfg)
     dev = _device_of(q, "q")

@@ -363,3 +363,25 @@ def test_token_strides_and_pools_past_32_bits():
         for x in (kp, vp):
             assert int((x[page] != 0).any(-1).sum()) == 1
     assert int((kp != 0).any(-1).sum()) == 2 and int((vp != 0).any(-1).sum()) == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["medium_decode", "tiny_decode"])
+def test_index_rows_without_rotation(name):
+    """An index table of width 0: the index rows are stored as they are."""
+    spec = wl.small(name)
+    w = wl.make_workload(spec, device="cuda")
+    cfg = msa.config_for(spec)
+    sa = msa.SparseAttention(cfg)
+    T = w.num_tokens
+    q, k, v, iq, ik, _ = _fused(spec, T, 33)
+    n = int(w.seq_lens.max())
+    iq_out = torch.zeros_like(iq, memory_format=torch.contiguous_format)
+    rope = msa.Rope(_table(n, 64), idx_cos_sin=torch.zeros((n, 0), device="cuda"))
+    msa.plan(cfg, w.seq_lens, w.block_table, sa.ws)
+    rope.write(cfg, sa.ws, q, k, v, iq, ik, sa.out, iq_out, w.k_pages, w.v_pages, w.idx_k_pages)
+    assert msa.check_device_error(sa.ws) == 0
+    assert torch.equal(iq_out, iq)
+    slots = oracle.cache_slots(to_np(w.seq_lens), to_np(w.q_lens), to_np(w.block_table), 128)
+    for t, s in enumerate(slots):
+        assert torch.equal(w.idx_k_pages[s // 128, :, s % 128], ik[t])
