@@ -64,7 +64,7 @@ struct Kind {
 struct RopeArgs {
   FastDiv R;                   // rows a token
   uint32_t items;              // tokens * rows
-  int Hq, Hkv, max_blocks, fp4, interleaved;
+  int Hq, Hkv, max_blocks, interleaved;
   int64_t num_positions, pool_slots;
   const int64_t* positions;    // or null: the plan's
   const int64_t* loc;          // or null: the plan's
@@ -155,7 +155,7 @@ rope_write_kernel(WsView ws, const __grid_constant__ RopeArgs a) {
   // neighbour's chunks when the halves are split (rot / 16 is even), else both
   // chunks are one block
   float ma = 0.f, mb = 0.f;
-  if (a.fp4) {                 // all lanes: the shuffles are warp-wide
+  if (__any_sync(0xffffffffu, kd.pool == MSA_KV_NVFP4)) {   // the shuffles are warp-wide
     const float pa = amax8(x), pb = amax8(y);
     const float na = __shfl_xor_sync(0xffffffffu, pa, 1);
     const float nb = __shfl_xor_sync(0xffffffffu, pb, 1);
@@ -271,7 +271,6 @@ extern "C" msa_status msa_rope_cache_write(const msa_config* cfg, void* ws, cons
   a.Hq = cfg->num_q_heads;
   a.Hkv = cfg->num_kv_heads;
   a.max_blocks = cfg->max_blocks_per_req;
-  a.fp4 = kv == MSA_KV_NVFP4;
   a.interleaved = rope->interleaved != 0;
   a.num_positions = rope->num_positions;
   a.pool_slots = (int64_t)cfg->num_pages * kBlock;
