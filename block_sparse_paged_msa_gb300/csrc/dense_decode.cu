@@ -19,7 +19,9 @@
 // probabilities are rounded to fp16 for P V (2^-11 relative, below the bf16
 // rounding of the output); they are carried as 2^(s' - m + 7) so that fp16's
 // normal range reaches 2^-21 below the running maximum.  Their sum is taken
-// before that rounding.
+// before that rounding.  m is kept as an unscaled score and the scale applied to
+// the difference, which is exact near the maximum: scores past 2^24, where a
+// step of fp32 is more than 7, keep their weights too.
 //
 // Work split.  One unit of work is a 128-key page of one (request, KV head).
 // The step's units, request by request and head by head, are cut into equal
@@ -37,7 +39,7 @@
 // transposes the probabilities into the B operand.  K passes through TMEM in
 // two halves, in turns with V's: 128 columns a team, four teams an SM.
 //
-// What bounds it.  32 requests of 8k-32k tokens, 64 + 8 heads (754 MB): 140 us,
+// What bounds it.  32 requests of 8k-32k tokens, 64 + 8 heads (754 MB): 139 us,
 // 5.4 TB/s, 0.80 of the measured copy bandwidth; a page takes an SM about 1000
 // cycles, of them 655 issue slots a scheduler (2620 warp instructions, 1024 of
 // them the conversions and scalings of its 32768 codes), the rest waits of a
@@ -47,6 +49,7 @@
 // (32 rows): 152 us, 4.0 TB/s, against 295 us by mma.sync.  Two requests of
 // 1.5k tokens, one head: 8 us, the chain of one tile and two launches.
 #include <atomic>
+#include <cfloat>
 
 #include "tcgen05.cuh"
 
@@ -62,7 +65,7 @@ constexpr float kSlack = 8.f;                  // 2^(kBias + kSlack) is below fp
 struct DenseArgs {
   int Hkv, Hq, G, q_len, max_blocks, max_batch, rows;   // rows = G * q_len
   uint32_t g_magic;                            // row / G = row * g_magic >> 16
-  float scale_log2, v_scale;
+  float scale_log2, v_scale, slack;            // slack: kSlack in unscaled scores
   const __nv_bfloat16* q;
   const uint8_t *k_pool, *v_pool;
   __nv_bfloat16* out;
@@ -747,9 +750,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       for (int i = 0; i < NG; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          mx[i][k] = fmaxf(fmax3(xf(0, i, k), xf(0, i, k + 2), xf(1, i, k)), xf(1, i, k + 2)) *
-                     a.scale_log2;
-          move |= mx[i][k] > m[i][k] + kSlack;
+          mx[i][k] = fmaxf(fmax3(xf(0, i, k), xf(0, i, k + 2), xf(1, i, k)), xf(1, i, k + 2));
+          move |= mx[i][k] > m[i][k] + a.slack;
         }
       if (named_bar_any(bar, 128, move)) {
         // new references: the row maxima over the team's keys
@@ -770,7 +772,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
             const int n = 8 * i + 2 * c + k;
             const float mn = fmaxf(fmax3(m[i][k], sh.red[0][n], sh.red[1][n]),
                                    fmaxf(sh.red[2][n], sh.red[3][n]));
-            const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m[i][k] - mn);
+            const float alpha =
+                mn == -INFINITY ? 1.f : ex2_approx((m[i][k] - mn) * a.scale_log2);
             m[i][k] = mn;
             l[i][k] *= alpha;
             if (w == 0 && g == 0) sh.alpha[n] = alpha;
@@ -791,14 +794,12 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
           tmem_st_wait();
         }
       }
-      // ---- P = 2^(s' - m + bias) as the B operand [row][key].  s' is rounded as
-      // it was for m (no fma), and bias - m downwards: so P stays within fp16 for
-      // scores past 2^24 too, where a step of fp32 is more than the slack.
-      const uint64_t sl = f2(a.scale_log2, a.scale_log2);
+      // ---- P = 2^((s - m) scale + bias) as the B operand [row][key]
+      const uint64_t sl = f2(a.scale_log2, a.scale_log2), bias = f2(kBias, kBias);
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const uint64_t off = f2(__fsub_rd(kBias, m[i][0] == -INFINITY ? 0.f : m[i][0]),
-                                __fsub_rd(kBias, m[i][1] == -INFINITY ? 0.f : m[i][1]));
+        const uint64_t ref = f2(m[i][0] == -INFINITY ? 0.f : -m[i][0],
+                                m[i][1] == -INFINITY ? 0.f : -m[i][1]);
         uint64_t sum = f2(l[i][0], l[i][1]);
         uint32_t p[4];
 #pragma unroll
@@ -806,7 +807,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
           float p0, p1;
           const uint64_t s2 =
               f2u(x[o >> 1][4 * i + 2 * (o & 1)], x[o >> 1][4 * i + 2 * (o & 1) + 1]);
-          f2_split(add_f2(mul_f2(s2, sl), off), p0, p1);
+          f2_split(fma_f2(add_f2(s2, ref), sl, bias), p0, p1);
           p0 = ex2_approx(p0);
           p1 = ex2_approx(p1);
           sum = add_f2(sum, f2(p0, p1));
@@ -867,7 +868,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
             make_uint4(pack_bf16(y0.x * inv, y0.y * inv), pack_bf16(y0.z * inv, y0.w * inv),
                        pack_bf16(y1.x * inv, y1.y * inv), pack_bf16(y1.z * inv, y1.w * inv));
         if (part == 0)
-          a.lse[row] = sum == 0.f ? -INFINITY : (sh.ref[n] + log2f(sum) - kBias) * kLn2;
+          a.lse[row] =
+              sum == 0.f ? -INFINITY : (sh.ref[n] * a.scale_log2 + log2f(sum) - kBias) * kLn2;
       } else {
         float4* dst =
             reinterpret_cast<float4*>(a.o_part + (slot * a.rows + n) * kHeadDim + 8 * part);
@@ -960,7 +962,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
       for (int i = w; i < np; i += warps) {
         const float2 ml = a.ml_part[at(i)];
         const float4 v = *reinterpret_cast<const float4*>(a.o_part + at(i) * kHeadDim + 4 * lane);
-        const float f = M == -INFINITY ? 1.f : ex2_approx(ml.x - M);
+        const float f = M == -INFINITY ? 1.f : ex2_approx((ml.x - M) * a.scale_log2);
         l = fmaf(f, ml.y, l);
         o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
         o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
@@ -979,7 +981,8 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
       const float inv = l == 0.f ? 0.f : a.v_scale / l;
       reinterpret_cast<uint2*>(a.out + hq * kHeadDim)[lane] =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      if (lane == 0) a.lse[hq] = l == 0.f ? -INFINITY : (M + log2f(l) - kBias) * kLn2;
+      if (lane == 0)
+        a.lse[hq] = l == 0.f ? -INFINITY : (M * a.scale_log2 + log2f(l) - kBias) * kLn2;
     }
     __syncthreads();
   };
@@ -1066,6 +1069,7 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   a.rows = a.G * a.q_len;
   a.scale_log2 = cfg->softmax_scale * cfg->k_scale * kLog2e;
   if (!(a.scale_log2 > 0.f && a.scale_log2 < INFINITY)) return MSA_ERR_INVALID_ARG;
+  a.slack = fminf(kSlack / a.scale_log2, FLT_MAX);
   a.v_scale = cfg->v_scale;
   a.q = (const __nv_bfloat16*)q;
   a.k_pool = (const uint8_t*)k_pages;

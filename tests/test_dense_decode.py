@@ -368,11 +368,13 @@ def test_scores_past_24_bits(hq, hkv, q_len, L):
     """Scores of 10^8, where a step of fp32 is more than any bias of the exponent.
     The first key is 2688 in every dim, with the signs of q; no other is larger
     than 6 there, so that this key has all the weight and the output is its
-    value, rounded once."""
+    value, rounded once.  Every row has a magnitude of its own: the rounding of
+    its score, up to half a step, must not reach the weight."""
     c = Case(hq, hkv, [L], q_len=q_len, seed=21)
     c.q.copy_(torch.sign(c.q.float()) * 16384.0)
     c.q[c.q == 0] = 16384.0
-    c.q[:] = c.q[:1, :1].clone()                           # all queries alike
+    size = 16384.0 + 128.0 * torch.arange(c.T * hq, device="cuda").view(c.T, hq, 1)
+    c.q.copy_(torch.sign(c.q[:1, :1].float()) * size)      # multiples of 2^7: bf16
     page = int(c.block_table[0, 0])
     sign = (to_np(c.q[0, 0]) < 0).astype(np.uint8)
     codes = 7 + 8 * sign                                   # +-6
@@ -385,7 +387,7 @@ def test_scores_past_24_bits(hq, hkv, q_len, L):
     want = oracle.bf16_round(v[1, 0].astype(np.float32))
     got = to_np(d.out)
     assert np.array_equal(got, np.broadcast_to(want, got.shape))
-    top = 128 * 16384.0 * 2688 * c.cfg.k_scale * c.cfg.softmax_scale
+    top = 128 * to_np(size)[..., 0] * 2688 * c.cfg.k_scale * c.cfg.softmax_scale
     # the score's products and sums, the scale and its rounding, ln 2's: 2^-24 each
     assert np.all(np.abs(to_np(d.lse) - top) <= (128 + 4) * 2.0 ** -24 * top)
 
