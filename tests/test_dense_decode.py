@@ -393,6 +393,29 @@ def test_scores_past_24_bits(hq, hkv, q_len, L):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,L", [(8, 900), (16, 70000)])
+def test_equal_scores_past_24_bits(hq, L):
+    """Two keys of the same huge score, in different pages (of one range, and of
+    two that are merged), have half the weight each."""
+    c = Case(hq, 1, [L], seed=22)
+    size = 16384.0 + 128.0 * torch.arange(hq, device="cuda").view(1, hq, 1)
+    c.q.copy_(torch.sign(c.q[:1, :1].float()) * size)
+    sign = (to_np(c.q[0, 0]) < 0).astype(np.uint8)
+    codes = torch.from_numpy((7 + 8 * sign)[0::2] + 16 * (7 + 8 * sign)[1::2]).cuda()
+    v = []
+    for u in (5, L - 200):
+        page = int(c.block_table[0, u // 128])
+        c.pool[page, 0, u % 128, :64] = codes
+        c.pool[page, 0, u % 128, 64:] = 0x7e
+        v.append(oracle.nvfp4_dequant(c.pool[page].cpu().numpy()[None], 128)[0, 1, u % 128])
+    d = c.run()
+    assert msa.check_device_error(d.ws) == 0
+    want = oracle.bf16_round(((v[0] + v[1]) / 2 * c.cfg.v_scale).astype(np.float32))
+    got = to_np(d.out)
+    assert np.array_equal(got, np.broadcast_to(want, got.shape))
+
+
+@pytest.mark.gpu
 def test_two_graphs_that_share_their_buffers():
     """Two captured steps of one layer's buffers (workspace, scratch, output),
     replayed in any order on one stream."""
