@@ -595,6 +595,29 @@ def test_rotate_append_and_attend(hq, hkv, q_len):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+def test_new_rows_without_a_rope(given):
+    """new_kv alone goes through cache_write; slots from the plan, or given."""
+    c = Case(8, 2, [300, 129, 1], seed=15)
+    g = torch.Generator(device="cuda").manual_seed(16)
+    new = [torch.randn((3, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+           for _ in range(2)]
+    slots = oracle.cache_slots(c.lens, c.q_lens, to_np(c.block_table), 128)
+    loc = torch.tensor(slots, dtype=torch.int64, device="cuda") if given else None
+    want = oracle.cache_write_nvfp4(c.pool.cpu().numpy(), slots, to_np(new[0]), c.cfg.k_scale, 0)
+    want = oracle.cache_write_nvfp4(want, slots, to_np(new[1]), c.cfg.v_scale, 1)
+    d = c.layer()
+    d.run(c.seq_lens, c.block_table, c.q, c.pool, c.pool, new_kv=new, out_cache_loc=loc)
+    assert msa.check_device_error(d.ws) == 0
+    assert np.array_equal(c.pool.cpu().numpy(), want)
+    c.check(d)
+    again = d.out.clone()
+    d.out.fill_(7.0)
+    d.run(None, None, c.q, c.pool, c.pool, planned=True)     # a second layer of the step
+    assert torch.equal(d.out, again)
+
+
+@pytest.mark.gpu
 def test_sparse_and_dense_layers_share_a_plan():
     """A hybrid model's step: one plan and one workspace, a sparse layer, then a
     dense one that equals its own planned run."""
