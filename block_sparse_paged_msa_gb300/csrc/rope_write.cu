@@ -24,9 +24,11 @@
 // rows of all tokens are one list (q | k | v | idx_q | idx_k | idx_v per
 // token), 16 of it to a CTA whatever the head counts are.  What bounds it is the
 // number of loads in flight: one row a thread at ten CTAs an SM moves the 407 MB
-// of 8192 tokens (64 + 8 heads, bf16) in 68 us, 0.90 of the measured copy
-// bandwidth; CTAs of 32 rows take 71 us, of 8 rows 100 us, two rows a thread
-// 86 us, and without the streaming stores it is 73 us.  One token takes 1.9 us.
+// of 8192 tokens (64 + 8 heads, bf16) in 69.0 us, 5.9 TB/s, 0.87 of the measured
+// copy bandwidth; one token takes 2.0 us.  1.4 and 0.2 us of that wait for the
+// step's token count before the first row is read (the grid is the config's, the
+// inputs end with the step).  Before that wait, at 67.6 us: CTAs of 32 rows 71
+// us, of 8 rows 100 us, two rows a thread 86 us, without the streaming stores 73.
 #include "kv_quant.cuh"
 
 namespace msa {
@@ -106,6 +108,8 @@ rope_write_kernel(WsView ws, const __grid_constant__ RopeArgs a) {
   const int ca = split ? sub : 2 * sub, cb = split ? sub + rot / 16 : 2 * sub + 1;
   bool live = item < a.items && kd.src != nullptr && sub < width / 16;
   griddep_wait();              // the projection, the plan, readers of the last step
+  // the inputs have rows for the step's tokens only, the grid for the config's
+  live = live && t < ws.hdr->num_tokens;
   uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
   int req = -1, plan_pos = 0;
   int64_t pos = 0, slot = 0;
@@ -113,7 +117,7 @@ rope_write_kernel(WsView ws, const __grid_constant__ RopeArgs a) {
     const __nv_bfloat16* src = kd.src + t * kd.stride + h * width;
     xa = ld_once(src + 8 * ca);
     xb = ld_once(src + 8 * cb);
-    req = ws.tok_req[t];       // -1: idle, or behind the step's tokens
+    req = ws.tok_req[t];       // -1: idle
     plan_pos = ws.tok_pos[t];
     pos = a.positions != nullptr ? a.positions[t] : plan_pos;
     if (a.loc != nullptr && kd.pool >= 0) slot = a.loc[t];

@@ -385,3 +385,47 @@ def test_index_rows_without_rotation(name):
     slots = oracle.cache_slots(to_np(w.seq_lens), to_np(w.q_lens), to_np(w.block_table), 128)
     for t, s in enumerate(slots):
         assert torch.equal(w.idx_k_pages[s // 128, :, s % 128], ik[t])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["medium_decode", "nvfp4_decode"])
+def test_inputs_of_exactly_the_steps_tokens(name):
+    """By the C call the inputs, positions and slots hold the step's tokens and no
+    more, whatever the config's maxima are."""
+    spec = wl.small(name, batch=3)
+    w1, w2 = (wl.make_workload(spec, device="cuda") for _ in range(2))
+    cfg = msa.config_for(spec, max_batch=3 + 200)
+    T, most = w1.num_tokens, ops.max_tokens(cfg)
+    rows = [x.contiguous() for x in _fused(spec, T, 41)[:5]]
+    tab = _table(int(w1.seq_lens.max()), 64)
+    pos = torch.tensor([p for _, p in oracle.query_positions(to_np(w1.seq_lens),
+                                                             to_np(w1.q_lens))], device="cuda")
+    slots = torch.tensor(oracle.cache_slots(to_np(w1.seq_lens), to_np(w1.q_lens),
+                                            to_np(w1.block_table), 128), device="cuda")
+    a = msa.SparseAttention(cfg)
+    msa.plan(cfg, w1.seq_lens, w1.block_table, a.ws)
+
+    def pad(x, n=most):
+        y = torch.zeros((n, *x.shape[1:]), dtype=x.dtype, device="cuda")
+        y[:len(x)] = x
+        return y
+
+    full = [pad(x) for x in rows]
+    outs = torch.empty_like(full[0]), torch.empty_like(full[3])
+    msa.rope_cache_write(cfg, a.ws, *full, tab, *outs, w1.k_pages, w1.v_pages, w1.idx_k_pages,
+                         positions=pad(pos), out_cache_loc=pad(slots))
+    rope = ops.MsaRope(tab.data_ptr(), None, 64, 64, 0, tab.shape[0],
+                       *[x.stride(0) for x in rows], 0)
+    exact = torch.empty_like(rows[0]), torch.empty_like(rows[3])
+    P = ctypes.c_void_p
+    assert ops.lib().msa_rope_cache_write(
+        ctypes.byref(cfg), P(a.ws.data_ptr()), ctypes.byref(rope),
+        *[P(x.data_ptr()) for x in rows], None, P(pos.data_ptr()), P(slots.data_ptr()),
+        P(exact[0].data_ptr()), P(exact[1].data_ptr()), P(w2.k_pages.data_ptr()),
+        P(w2.v_pages.data_ptr()), P(w2.idx_k_pages.data_ptr()), None,
+        P(torch.cuda.current_stream().cuda_stream)) == 0
+    assert msa.check_device_error(a.ws) == 0
+    assert torch.equal(exact[0], outs[0][:T]) and torch.equal(exact[1], outs[1][:T])
+    for x, y in ((w1.k_pages, w2.k_pages), (w1.v_pages, w2.v_pages),
+                 (w1.idx_k_pages, w2.idx_k_pages)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
