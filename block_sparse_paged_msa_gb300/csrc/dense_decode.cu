@@ -1058,7 +1058,7 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   if (!dense_supported(*cfg)) return MSA_ERR_UNSUPPORTED;
   if (!ws || !q || !k_pages || !v_pages || !scratch || !out || !lse) return MSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
-      ((uintptr_t)scratch & 255) != 0 || ((uintptr_t)lse & 3) != 0)
+      ((uintptr_t)ws & 255) != 0 || ((uintptr_t)scratch & 255) != 0 || ((uintptr_t)lse & 3) != 0)
     return MSA_ERR_INVALID_ARG;
   const int64_t T = max_tokens_of(*cfg);
   if (T <= 0 || cfg->max_batch == 0) return MSA_OK;

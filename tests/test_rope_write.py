@@ -104,6 +104,19 @@ def test_limits_refused_on_the_host():
     assert _call(cfg, _args(qs=wide, ks=wide, vs=wide, iqs=wide, iks=wide)) == 0
 
 
+def test_a_misaligned_workspace_is_refused():
+    """The kernels read the plan in words of 16 bytes: a workspace that msa_plan
+    would refuse (256-byte alignment) is refused here too."""
+    P, lib = ctypes.c_void_p, ops.lib()
+    cfg = msa.make_config(num_q_heads=8, num_kv_heads=1, init_blocks=1, local_blocks=2,
+                          topk_blocks=4, index_dim=64, max_batch=2, max_blocks_per_req=8,
+                          num_pages=16, kv_dtype="nvfp4")
+    for ws in (257, 260, 272, 384):
+        assert lib.msa_plan(ctypes.byref(cfg), 1, P(256), None, P(256), 8, P(ws), None) == INVALID
+        assert lib.msa_dense_decode(ctypes.byref(cfg), P(ws), *[P(256)] * 6, None) == INVALID
+        assert _call(cfg, _args(ws=ws)) == INVALID
+
+
 def test_rows_layouts_refused_by_the_binding():
     with pytest.raises(ValueError, match="CUDA"):
         ops._expect_rows(torch.zeros(2, 1, 128, dtype=torch.bfloat16), "q", (2, 1, 128), 0)
