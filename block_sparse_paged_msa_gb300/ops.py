@@ -491,8 +491,10 @@ def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, 
     idx_q, idx_k, idx_v [T, H_kv, d] bf16 with any token stride (slices of a
     fused projection), idx_* may be None.  cos_sin [positions, rotary_dim]
     fp32: cosines, then sines; idx_cos_sin the index heads' own table, None =
-    cos_sin, one of width 0 = their rows are not rotated.  q_out, idx_q_out: the rotated queries, contiguous; each may be its
-    input.  positions: [T] int64, None = the plan's."""
+    cos_sin, one of width 0 (of any length) = their rows are not rotated.  A
+    position has to lie in every table that the call reads.  q_out, idx_q_out:
+    the rotated queries, contiguous; each may be its input.  positions: [T]
+    int64, None = the plan's."""
     y = _layout(cfg)
     dev = _device_of(q, "q")
     p_q, s_q = _expect_rows(q, "q", y.q, dev)
@@ -502,7 +504,10 @@ def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, 
     p_ics, irot = None, rot
     if idx_cos_sin is not None:
         p_ics, n, irot = _expect_table(idx_cos_sin, "idx_cos_sin", dev)
-        rows = min(rows, n)
+        if irot == 0 or (idx_q is None and idx_k is None):
+            p_ics = None                    # not read: its rows limit nothing
+        else:
+            rows = min(rows, n)
     p_iq = p_ik = p_iv = p_iqo = p_ikp = p_ivp = None
     s_iq = s_ik = s_iv = 0
     if idx_q is not None:

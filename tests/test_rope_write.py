@@ -442,3 +442,54 @@ def test_inputs_of_exactly_the_steps_tokens(name):
     for x, y in ((w1.k_pages, w2.k_pages), (w1.v_pages, w2.v_pages),
                  (w1.idx_k_pages, w2.idx_k_pages)):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [0, 1, 7])
+def test_an_index_table_that_is_not_read_limits_no_position(length):
+    """Of width 0, whatever its length; and any table when the call has no index
+    rows (the full-attention layers of the same model)."""
+    spec = wl.small("nvfp4_decode", batch=3)
+    w = wl.make_workload(spec, device="cuda")
+    cfg = msa.config_for(spec)
+    T = w.num_tokens
+    q, k, v, iq, ik, _ = _fused(spec, T, 45)
+    tab = _table(int(w.seq_lens.max()), 64)
+    ws = torch.empty(msa.workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    msa.plan(cfg, w.seq_lens, w.block_table, ws)
+
+    def write(idx_cos_sin, with_index):
+        kp, ikp = w.k_pages.clone(), w.idx_k_pages.clone()
+        q_out = torch.zeros((T, spec.num_q_heads, 128), dtype=torch.bfloat16, device="cuda")
+        iq_out = torch.zeros((T, spec.num_kv_heads, spec.index_dim), dtype=torch.bfloat16,
+                             device="cuda")
+        msa.Rope(tab, idx_cos_sin=idx_cos_sin).write(
+            cfg, ws, q, k, v, iq if with_index else None, ik if with_index else None, q_out,
+            iq_out if with_index else None, kp, kp, ikp if with_index else None)
+        assert msa.check_device_error(ws) == 0
+        return q_out, iq_out, kp, ikp
+
+    full = torch.zeros((tab.shape[0], 0), device="cuda")
+    for a, b in zip(write(torch.zeros((length, 0), device="cuda"), True), write(full, True)):
+        assert torch.equal(a, b)
+    for a, b in zip(write(torch.zeros((length, 32), device="cuda"), False), write(None, False)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_a_position_outside_the_index_table_is_flagged():
+    """A table of the index heads that is read does limit the positions."""
+    spec = wl.small("medium_decode", batch=3)
+    w = wl.make_workload(spec, device="cuda")
+    cfg = msa.config_for(spec)
+    q, k, v, iq, ik, _ = _fused(spec, 3, 46)
+    sa = msa.SparseAttention(cfg)
+    iq_out = torch.empty((3, spec.num_kv_heads, spec.index_dim), dtype=torch.bfloat16,
+                         device="cuda")
+    msa.plan(cfg, w.seq_lens, w.block_table, sa.ws)
+    before = w.k_pages.clone()
+    msa.rope_cache_write(cfg, sa.ws, q, k, v, iq, ik, _table(int(w.seq_lens.max()), 64), sa.out,
+                         iq_out, w.k_pages, w.v_pages, w.idx_k_pages,
+                         idx_cos_sin=_table(1, 32))
+    assert msa.check_device_error(sa.ws) == 32
+    assert torch.equal(w.k_pages, before)
