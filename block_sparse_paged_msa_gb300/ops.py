@@ -140,6 +140,29 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current, on `stream` or its current
+    stream."""
+    if stream is None:
+        if _raw_stream is not None and dev == _device():
+            return fn(*args, _raw_stream(dev))
+    else:
+        at = getattr(stream, "device_index", dev)
+        if at != dev:
+            raise ValueError(f"the stream is on device {at}, the tensors on {dev}")
+        if dev == _device():
+            return fn(*args, stream.cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(stream))
+
+
+def _launch(name, t, stream, *args):
+    """The library's call `name` on the device of tensor `t`; raises what it says."""
+    st = _call(getattr(lib(), name), t.get_device(), stream, *args)
+    if st:
+        _check(name, st)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -338,9 +361,8 @@ def plan(cfg, seq_lens, block_table, ws, cu_seqlens_q=None, stream=None):
     B = _need_batch(cfg, seq_lens, cu_seqlens_q=cu_seqlens_q)
     _need_block_table(cfg, block_table, B)
     _need_ws(cfg, ws)
-    _check("msa_plan", lib().msa_plan(ctypes.byref(cfg), B, _ptr(seq_lens), _ptr(cu_seqlens_q),
-                                      _ptr(block_table), block_table.shape[1], _ptr(ws),
-                                      _stream(stream)))
+    _launch("msa_plan", ws, stream, ctypes.byref(cfg), B, _ptr(seq_lens),
+            _ptr(cu_seqlens_q), _ptr(block_table), block_table.shape[1], _ptr(ws))
 
 
 def plan_from_req_to_token(cfg, seq_lens, req_to_token, req_pool_indices, ws,
@@ -351,10 +373,9 @@ def plan_from_req_to_token(cfg, seq_lens, req_to_token, req_pool_indices, ws,
         raise ValueError("req_to_token rows are shorter than max_blocks_per_req * block_size")
     _need(req_pool_indices, "req_pool_indices", torch.int64, 1, B)
     _need_ws(cfg, ws)
-    _check("msa_plan_from_req_to_token", lib().msa_plan_from_req_to_token(
-        ctypes.byref(cfg), B, _ptr(seq_lens), _ptr(cu_seqlens_q),
-        _ptr(req_to_token), req_to_token.shape[1], _ptr(req_pool_indices), _ptr(ws),
-        _stream(stream)))
+    _launch("msa_plan_from_req_to_token", ws, stream, ctypes.byref(cfg), B, _ptr(seq_lens),
+            _ptr(cu_seqlens_q), _ptr(req_to_token), req_to_token.shape[1], _ptr(req_pool_indices),
+            _ptr(ws))
 
 
 def cache_write(cfg, ws, k, v, idx_k, k_pages, v_pages, idx_k_pages, out_cache_loc=None,
@@ -379,10 +400,9 @@ def cache_write(cfg, ws, k, v, idx_k, k_pages, v_pages, idx_k_pages, out_cache_l
         _need(idx_v, "idx_v", torch.bfloat16, 3, T, (cfg.num_kv_heads, cfg.index_dim))
         _need(idx_v_pages, "idx_v_pages", torch.bfloat16, 4, cfg.num_pages,
               (cfg.num_kv_heads, cfg.block_size, cfg.index_dim))
-    _check("msa_cache_write", lib().msa_cache_write(
-        ctypes.byref(cfg), _ptr(ws), _ptr(out_cache_loc), _ptr(k), _ptr(v), _ptr(idx_k),
-        _ptr(idx_v), _ptr(k_pages), _ptr(v_pages), _ptr(idx_k_pages), _ptr(idx_v_pages),
-        _stream(stream)))
+    _launch("msa_cache_write", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(out_cache_loc),
+            _ptr(k), _ptr(v), _ptr(idx_k), _ptr(idx_v), _ptr(k_pages), _ptr(v_pages),
+            _ptr(idx_k_pages), _ptr(idx_v_pages))
 
 
 class _Layout:
@@ -470,18 +490,6 @@ def _expect_rows(t, name, shape, dev):
     return ptr, (tok if T > 1 else heads * width)
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with device `dev` current, on `stream` or its current
-    stream."""
-    if stream is None:
-        if _raw_stream is not None and dev == _device():
-            return fn(*args, _raw_stream(dev))
-    elif stream.device.index != dev:
-        raise ValueError(f"the stream is on device {stream.device.index}, the tensors on {dev}")
-    with torch.cuda.device(dev):
-        return fn(*args, _stream(stream))
-
-
 def rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, cos_sin, q_out, idx_q_out, k_pages, v_pages,
                      idx_k_pages, *, interleaved=False, idx_cos_sin=None, positions=None,
                      out_cache_loc=None, idx_v=None, idx_v_pages=None, stream=None):
@@ -558,9 +566,8 @@ def index_attention(cfg, ws, idx_q, idx_k_pages, idx_v_pages, scratch, idx_out, 
     _need(idx_out, "idx_out", torch.bfloat16, 3, T, (cfg.num_kv_heads, cfg.index_dim))
     if idx_lse is not None:
         _need(idx_lse, "idx_lse", torch.float32, 2, T, (cfg.num_kv_heads,))
-    _check("msa_index_attention", lib().msa_index_attention(
-        ctypes.byref(cfg), _ptr(ws), _ptr(idx_q), _ptr(idx_k_pages), _ptr(idx_v_pages),
-        _ptr(scratch), _ptr(idx_out), _ptr(idx_lse), _stream(stream)))
+    _launch("msa_index_attention", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(idx_q),
+            _ptr(idx_k_pages), _ptr(idx_v_pages), _ptr(scratch), _ptr(idx_out), _ptr(idx_lse))
 
 
 def index_score(cfg, ws, idx_q, idx_k_pages, block_scores, stream=None):
@@ -568,9 +575,8 @@ def index_score(cfg, ws, idx_q, idx_k_pages, block_scores, stream=None):
     T = max_tokens(cfg)
     _need_tokens(cfg, T, idx_q=idx_q, block_scores=block_scores)
     _need_pools(cfg, idx_k_pages=idx_k_pages)
-    _check("msa_index_score", lib().msa_index_score(
-        ctypes.byref(cfg), _ptr(ws), _ptr(idx_q), _ptr(idx_k_pages), _ptr(block_scores),
-        _stream(stream)))
+    _launch("msa_index_score", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(idx_q),
+            _ptr(idx_k_pages), _ptr(block_scores))
 
 
 def decode_step(cfg, ws, seq_lens, block_table, idx_q, idx_k_pages, q, k_pages, v_pages,
@@ -584,11 +590,9 @@ def decode_step(cfg, ws, seq_lens, block_table, idx_q, idx_k_pages, q, k_pages, 
     _need_tokens(cfg, T, q=q, idx_q=idx_q, block_scores=block_scores, selected=selected,
                  out=out, lse=lse)
     _need_pools(cfg, k_pages, v_pages, idx_k_pages)
-    _check("msa_decode_step", lib().msa_decode_step(
-        ctypes.byref(cfg), _ptr(ws), B, _ptr(seq_lens), _ptr(block_table),
-        block_table.shape[1], _ptr(idx_q), _ptr(idx_k_pages), _ptr(q), _ptr(k_pages),
-        _ptr(v_pages), _ptr(block_scores), _ptr(selected), _ptr(out), _ptr(lse),
-        _stream(stream)))
+    _launch("msa_decode_step", ws, stream, ctypes.byref(cfg), _ptr(ws), B, _ptr(seq_lens),
+            _ptr(block_table), block_table.shape[1], _ptr(idx_q), _ptr(idx_k_pages), _ptr(q),
+            _ptr(k_pages), _ptr(v_pages), _ptr(block_scores), _ptr(selected), _ptr(out), _ptr(lse))
 
 
 def index_score_topk(cfg, ws, idx_q, idx_k_pages, block_scores, selected, stream=None):
@@ -597,25 +601,23 @@ def index_score_topk(cfg, ws, idx_q, idx_k_pages, block_scores, selected, stream
     T = max_tokens(cfg)
     _need_tokens(cfg, T, idx_q=idx_q, block_scores=block_scores, selected=selected)
     _need_pools(cfg, idx_k_pages=idx_k_pages)
-    _check("msa_index_score_topk", lib().msa_index_score_topk(
-        ctypes.byref(cfg), _ptr(ws), _ptr(idx_q), _ptr(idx_k_pages), _ptr(block_scores),
-        _ptr(selected), _stream(stream)))
+    _launch("msa_index_score_topk", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(idx_q),
+            _ptr(idx_k_pages), _ptr(block_scores), _ptr(selected))
 
 
 def topk_select(cfg, ws, block_scores, selected, stream=None):
     _need_ws(cfg, ws)
     _need_tokens(cfg, max_tokens(cfg), block_scores=block_scores, selected=selected)
-    _check("msa_topk_select", lib().msa_topk_select(
-        ctypes.byref(cfg), _ptr(ws), _ptr(block_scores), _ptr(selected), _stream(stream)))
+    _launch("msa_topk_select", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(block_scores),
+            _ptr(selected))
 
 
 def sparse_decode(cfg, ws, q, k_pages, v_pages, selected, stream=None):
     _need_ws(cfg, ws)
     _need_tokens(cfg, max_tokens(cfg), q=q, selected=selected)
     _need_pools(cfg, k_pages, v_pages)
-    _check("msa_sparse_decode", lib().msa_sparse_decode(
-        ctypes.byref(cfg), _ptr(ws), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(selected),
-        _stream(stream)))
+    _launch("msa_sparse_decode", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(q),
+            _ptr(k_pages), _ptr(v_pages), _ptr(selected))
 
 
 def compact_selected(cfg, ws, selected, page_table, dense_len, stream=None):
@@ -627,9 +629,8 @@ def compact_selected(cfg, ws, selected, page_table, dense_len, stream=None):
     _need_tokens(cfg, T, selected=selected)
     _need(page_table, "page_table", torch.int32, 3, T, (cfg.num_kv_heads, _sizes(cfg)[1]))
     _need(dense_len, "dense_len", torch.int32, 2, T, (cfg.num_kv_heads,))
-    _check("msa_compact_selected", lib().msa_compact_selected(
-        ctypes.byref(cfg), _ptr(ws), _ptr(selected), _ptr(page_table), _ptr(dense_len),
-        _stream(stream)))
+    _launch("msa_compact_selected", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(selected),
+            _ptr(page_table), _ptr(dense_len))
 
 
 def paged_decode(cfg, ws, q, k_pages, v_pages, page_table, dense_len, stream=None):
@@ -641,9 +642,8 @@ def paged_decode(cfg, ws, q, k_pages, v_pages, page_table, dense_len, stream=Non
     _need_pools(cfg, k_pages, v_pages)
     _need(page_table, "page_table", torch.int32, 3, T, (cfg.num_kv_heads, _sizes(cfg)[1]))
     _need(dense_len, "dense_len", torch.int32, 2, T, (cfg.num_kv_heads,))
-    _check("msa_paged_decode", lib().msa_paged_decode(
-        ctypes.byref(cfg), _ptr(ws), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-        _ptr(dense_len), _stream(stream)))
+    _launch("msa_paged_decode", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(q),
+            _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(dense_len))
 
 
 def dense_decode_scratch_bytes(cfg) -> int:
@@ -675,8 +675,7 @@ def dense_decode(cfg, ws, q, k_pages, v_pages, scratch, out, lse, stream=None):
 def combine(cfg, ws, out, lse, stream=None):
     _need_ws(cfg, ws)
     _need_tokens(cfg, max_tokens(cfg), out=out, lse=lse)
-    _check("msa_combine", lib().msa_combine(ctypes.byref(cfg), _ptr(ws), _ptr(out), _ptr(lse),
-                                            _stream(stream)))
+    _launch("msa_combine", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(out), _ptr(lse))
 
 
 def k2q_rows(cfg) -> int:
@@ -692,9 +691,8 @@ def build_k2q_csr(cfg, ws, selected, row_ptr, q_indices, stream=None):
     _need_tokens(cfg, max_tokens(cfg), selected=selected)
     _need(row_ptr, "row_ptr", torch.int32, 1, _sizes(cfg)[2] + 1)
     _need(q_indices, "q_indices", torch.int32, 1, _sizes(cfg)[3])
-    _check("msa_build_k2q_csr", lib().msa_build_k2q_csr(
-        ctypes.byref(cfg), _ptr(ws), _ptr(selected), _ptr(row_ptr), _ptr(q_indices),
-        _stream(stream)))
+    _launch("msa_build_k2q_csr", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(selected),
+            _ptr(row_ptr), _ptr(q_indices))
 
 
 def sparse_prefill(cfg, ws, q, k_pages, v_pages, selected, row_ptr, q_indices, stream=None):
@@ -703,15 +701,15 @@ def sparse_prefill(cfg, ws, q, k_pages, v_pages, selected, row_ptr, q_indices, s
     _need_pools(cfg, k_pages, v_pages)
     _need(row_ptr, "row_ptr", torch.int32, 1, _sizes(cfg)[2] + 1)
     _need(q_indices, "q_indices", torch.int32, 1, _sizes(cfg)[3])
-    _check("msa_sparse_prefill", lib().msa_sparse_prefill(
-        ctypes.byref(cfg), _ptr(ws), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(selected),
-        _ptr(row_ptr), _ptr(q_indices), _stream(stream)))
+    _launch("msa_sparse_prefill", ws, stream, ctypes.byref(cfg), _ptr(ws), _ptr(q),
+            _ptr(k_pages), _ptr(v_pages), _ptr(selected), _ptr(row_ptr), _ptr(q_indices))
 
 
 def check_device_error(ws, stream=None) -> int:
     """Synchronises the stream; returns the device error bits (0 = none)."""
     flags = ctypes.c_int32(0)
-    st = lib().msa_check_device_error(_ptr(ws), ctypes.byref(flags), _stream(stream))
+    st = _call(lib().msa_check_device_error, ws.get_device(), stream, _ptr(ws),
+               ctypes.byref(flags))
     if st not in (0, 4):
         _check("msa_check_device_error", st)
     return flags.value
@@ -721,8 +719,7 @@ def selftest_wait_timeout(cfg: MsaConfig, ws, stream=None):
     """Run the library's bounded wait on a barrier nothing completes (see
     msa_selftest_wait_timeout); the error word then holds MSA_DEVERR_TIMEOUT."""
     _need_ws(cfg, ws)
-    _check("msa_selftest_wait_timeout",
-           lib().msa_selftest_wait_timeout(ctypes.byref(cfg), _ptr(ws), _stream(stream)))
+    _launch("msa_selftest_wait_timeout", ws, stream, ctypes.byref(cfg), _ptr(ws))
 
 
 # ---------------------------------------------------------------- the step
@@ -874,10 +871,10 @@ def sparse_decode_noalloc(cfg, seq_lens, block_table, q, k_pages, v_pages, selec
     _need_block_table(cfg, block_table, B)
     _need_tokens(cfg, B * cfg.q_len, q=q, selected=selected, out=out, lse=lse)
     _need_pools(cfg, k_pages, v_pages)
-    _check("msa_sparse_decode_noalloc", lib().msa_sparse_decode_noalloc(
-        ctypes.byref(cfg), B, _ptr(seq_lens), _ptr(block_table),
-        block_table.shape[1], _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(selected), _ptr(out),
-        _ptr(lse), _stream(stream)),
+    _check("msa_sparse_decode_noalloc", _call(
+        lib().msa_sparse_decode_noalloc, q.get_device(), stream, ctypes.byref(cfg), B,
+        _ptr(seq_lens), _ptr(block_table), block_table.shape[1], _ptr(q), _ptr(k_pages),
+        _ptr(v_pages), _ptr(selected), _ptr(out), _ptr(lse)),
         "(the step may need more than the 16 MiB scratch: see msa_workspace_bytes)")
 
 
