@@ -46,7 +46,7 @@
 // tile's chain that four teams do not cover.  The same dequantisation in front
 // of mma.sync took 192 us: an mma.sync holds its scheduler for about 8 cycles,
 // 64 of them a page and warp.  16 requests of 32772 tokens with 4 new ones each
-// (32 rows): 152 us, 4.0 TB/s, against 295 us by mma.sync.  Two requests of
+// (32 rows): 149 us, 4.1 TB/s, against 295 us by mma.sync.  Two requests of
 // 1.5k tokens, one head: 8 us, the chain of one tile and two launches.
 #include <atomic>
 #include <cfloat>
@@ -64,6 +64,7 @@ constexpr float kSlack = 8.f;                  // 2^(kBias + kSlack) is below fp
 
 struct DenseArgs {
   int Hkv, Hq, G, q_len, max_blocks, max_batch, rows;   // rows = G * q_len
+  int teams;                                   // of the grid
   uint32_t g_magic;                            // row / G = row * g_magic >> 16
   float scale_log2, v_scale, slack;            // slack: kSlack in unscaled scores
   const __nv_bfloat16* q;
@@ -487,7 +488,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   if (extra >= 2 * S::kTeams) return;
   TeamShared<NG, TEAMS>& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
-  const int teams = S::kTeams * (int)gridDim.x;
+  // As an argument it stays in a register, which up to three teams have to spare
+  // (32 requests of 16384 tokens, 16 rows: 131.6 us, computed here 135.2; verify
+  // of 16 x 32772 149.0 and 151.8); four do not (32 of 8k-32k 142.6 and 139.0).
+  const int teams = TEAMS < 4 ? a.teams : TEAMS * (int)gridDim.x;
   uint8_t* qbuf = smem + team * S::kTeamSmem;  // Q x 2 and P: K-major, 128-byte swizzle
   uint8_t* pbuf = qbuf + 2 * S::kOperand;
   uint8_t* ring = pbuf + S::kOperand;
@@ -1005,7 +1009,7 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
 }
 
 template <int NG, int TEAMS>
-msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cudaStream_t s) {
+msa_status launch_dense(const WsView& v, DenseArgs& a, int64_t units, cudaStream_t s) {
   using S = Shape<NG, TEAMS>;
   static std::atomic<bool> ready[64];          // shared-memory limit raised, per device
   int dev = 0;
@@ -1022,7 +1026,7 @@ msa_status launch_dense(const WsView& v, const DenseArgs& a, int64_t units, cuda
   if (grid > kTeamsMax / S::kTeams) grid = kTeamsMax / S::kTeams;
   if (grid <= 0) return MSA_ERR_CUDA;
   if (grid > units) grid = units;
-  const int teams = (int)grid * S::kTeams;
+  const int teams = a.teams = (int)grid * S::kTeams;
   msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS>, dim3((unsigned)grid),
                              dim3(S::kThreads), S::kSmem, s, v, a);
   if (st != MSA_OK) return st;
@@ -1087,18 +1091,18 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
   const int64_t units = (int64_t)cfg->max_batch * cfg->max_blocks_per_req * a.Hkv;
   if (units > 0x7fffffff) return MSA_ERR_UNSUPPORTED;   // units are counted in 32 bits
   cudaStream_t s = (cudaStream_t)stream;
-  // Teams an SM: as many as TMEM holds, four up to 16 rows, three up to 32, two
-  // up to 64.  With 9 to 16 rows a fourth team pays off only on long steps
-  // (32 requests of 16384 tokens, 8 heads, 216 pages an SM: 130 us, with three
-  // 135 us) and costs time on short ones (8 requests, 54 pages an SM: 46 and
-  // 42 us; 61 requests of up to 6001 tokens, one head: 22 and 18 us); the limit
-  // lies between, in pages of the config's largest step.  Up to 8 rows four
-  // teams cost next to nothing on short ones (216 pages an SM: 114 and 122 us;
-  // 54: 37.9 and 38.3; 2 requests of 1.5k tokens, one head: 8.1 and 8.0).
+  // Teams an SM: four up to 8 rows, three up to 32, two up to 64, as many as TMEM
+  // holds -- except for 9 to 16 rows, where a fourth would fit.  It gains on long
+  // steps only (12 requests of 32768 tokens, 8 heads, 162 pages an SM: 99.4 us,
+  // with three 100.2; 32 of 16384, 216 pages: 128.7 and 131.7; 108 pages: 70.7
+  // and 70.1) and costs up to a fifth on short ones (54 pages: 45.4 and 41.8 us;
+  // 61 requests of up to 6001 tokens, one head: 21.6 and 17.9).  The host knows
+  // the config's largest step, not this one's size, and a fourth team that gets
+  // no range on short steps costs as much as one that does (21.9 us).  Up to 8
+  // rows four teams cost next to nothing on short steps (216 pages an SM: 114 and
+  // 122 us; 54: 37.9 and 38.3; 2 requests of 1.5k tokens, one head: 8.1 and 8.0).
   if (a.rows <= 8) return launch_dense<1, 4>(v, a, units, s);
-  if (a.rows <= 16)
-    return units >= (int64_t)128 * sm_count() ? launch_dense<2, 4>(v, a, units, s)
-                                              : launch_dense<2, 3>(v, a, units, s);
+  if (a.rows <= 16) return launch_dense<2, 3>(v, a, units, s);
   if (a.rows <= 32) return launch_dense<4, 3>(v, a, units, s);
   return launch_dense<8, 2>(v, a, units, s);
 }

@@ -86,7 +86,7 @@ def test_one_request_of_many_pages_a_range(group, q_len):
 @pytest.mark.gpu
 @pytest.mark.parametrize("group,q_len", [(16, 1), (3, 4)])
 def test_a_long_step_of_nine_to_sixteen_rows(group, q_len):
-    """More than 128 pages an SM: four teams."""
+    """More than 128 pages an SM."""
     c = Case(group * 8, 8, _mixed(62, 20, 7, 4200, 6000), q_len=q_len, q_std=3.0, seed=130)
     assert sum(-(-L // 128) for L in c.lens) * 8 >= 128 * 152
     d = c.run()
