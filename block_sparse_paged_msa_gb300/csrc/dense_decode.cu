@@ -14,14 +14,18 @@
 //     out = v_scale * sum_u 2^(s'_u - m) v_u / sum_u 2^(s'_u - m),   s' = s log2 e,
 // in one pass with a running maximum m and sum.  e2m1 x e4m3 has at most 6
 // significant bits and magnitudes 0 or 2^-10 .. 2688, so keys and values are
-// exact fp16 operands, and so are bf16 queries of fp16 magnitude (others are
-// flagged, MSA_DEVERR_FP16_RANGE); products accumulate in fp32.  The
-// probabilities are rounded to fp16 for P V (2^-11 relative, below the bf16
-// rounding of the output); they are carried as 2^(s' - m + 7) so that fp16's
-// normal range reaches 2^-21 below the running maximum.  Their sum is taken
-// before that rounding.  m is kept as an unscaled score and the scale applied to
-// the difference, which is exact near the maximum: scores past 2^24, where a
-// step of fp32 is more than 7, keep their weights too.
+// exact fp16 operands.  So are bf16 queries of 2^-14 .. 65504; larger ones are
+// flagged (MSA_DEVERR_FP16_RANGE), smaller ones keep the bits that fp16's
+// subnormals have, an error of up to 2^-25 absolute.  Products accumulate in
+// fp32.  The probabilities are rounded to fp16 for P V (2^-11 relative, below
+// the bf16 rounding of the output); they are carried as 2^(s' - m + 7) so that
+// fp16's normal range reaches 2^-21 below the running maximum (smaller ones are
+// off by up to 2^-25, 2^-32 of the sum).  Their sum is taken before that
+// rounding.  m is kept as an unscaled score and the scale applied to the
+// difference, which is exact near the maximum: scores past 2^24, where a step of
+// fp32 is more than 7, keep their weights too.  m follows the row's maximum only
+// when a score is 2^8 above it in the exponent, which the difference decides as
+// well: 2^15 is the largest probability.
 //
 // Work split.  One unit of work is a 128-key page of one (request, KV head).
 // The step's units, request by request and head by head, are cut into equal
