@@ -256,7 +256,8 @@ typedef struct msa_rope {
   int32_t idx_rotary_dim;     /* of the d dims of idx_q and idx_k; 0 = not rotated */
   int32_t interleaved;        /* 0: dims i and i + rotary_dim / 2 form pair i;
                                  1: dims 2i and 2i + 1                            */
-  int64_t num_positions;      /* rows of the tables                               */
+  int64_t num_positions;      /* rows of the tables that the call reads (the fewer
+                                 of two)                                          */
   int64_t q_stride, k_stride, v_stride;             /* elements from one token's row */
   int64_t idx_q_stride, idx_k_stride, idx_v_stride; /* to the next (multiples of 8)  */
 } msa_rope;
