@@ -760,8 +760,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         for (int k = 0; k < 2; ++k) {
           mx[i][k] = fmaxf(fmax3(xf(0, i, k), xf(0, i, k + 2), xf(1, i, k)), xf(1, i, k + 2));
           // the difference, exact near m (m + slack is rounded by up to half a step
-          // of fp32, which from 2^27 on is more than the probabilities have room
-          // for); -inf - -inf is NaN: no move
+          // of fp32: for |m| from 2^28 on, at a scale of 0.75 * 128^-0.5, that lets
+          // P pass fp16's largest value); -inf - -inf is NaN: no move
           move |= mx[i][k] - m[i][k] > a.slack;
         }
       if (named_bar_any(bar, 128, move)) {

@@ -253,9 +253,10 @@ extern "C" msa_status msa_rope_cache_write(const msa_config* cfg, void* ws, cons
       (idx_k && !rows_ok(idx_k, rope->idx_k_stride, Hkv * d)) ||
       (idx_v && !rows_ok(idx_v, rope->idx_v_stride, Hkv * d)))
     return MSA_ERR_INVALID_ARG;
-  if (((uintptr_t)ws & 255) != 0 || !aligned16(rope->cos_sin) || !aligned16(idx_cs) || !aligned16(q_out) ||
-      !aligned16(k_pages) || !aligned16(v_pages) || (idx_q && !aligned16(idx_q_out)) ||
-      (idx_k && !aligned16(idx_k_pages)) || (idx_v && !aligned16(idx_v_pages)))
+  if (((uintptr_t)ws & 255) != 0 || !aligned16(rope->cos_sin) || !aligned16(idx_cs) ||
+      !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      (idx_q && !aligned16(idx_q_out)) || (idx_k && !aligned16(idx_k_pages)) ||
+      (idx_v && !aligned16(idx_v_pages)))
     return MSA_ERR_INVALID_ARG;
   const int64_t T = max_tokens_of(*cfg);
   if (T <= 0) return MSA_OK;
