@@ -23,7 +23,8 @@ MSA_MODE_DECODE, MSA_MODE_PREFILL = 0, 1
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED",
           3: "MSA_ERR_CUDA", 4: "MSA_ERR_DEVICE_FLAG"}
 DEVERR_BITS = {1: "PAGE_RANGE", 2: "SEQ_LEN", 4: "SLOT_ALIGN", 8: "TIMEOUT", 16: "FP16_RANGE",
-               32: "POSITION"}
+               32: "POSITION", 64: "TREE", 128: "PROBS"}
+MAX_TREE_NODES = 64
 
 
 class MsaError(RuntimeError):
@@ -63,6 +64,15 @@ class MsaRope(ctypes.Structure):
     ]
 
 
+class MsaTreeProbs(ctypes.Structure):
+    """Mirror of ``msa_tree_probs`` in include/msa.h (field order matters)."""
+    _fields_ = [
+        ("target", ctypes.c_void_p), ("draft", ctypes.c_void_p), ("vocab", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("target_stride", ctypes.c_int64),
+        ("draft_stride", ctypes.c_int64),
+    ]
+
+
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MsaConfig)
 _SIGNATURES = {
@@ -82,6 +92,11 @@ _SIGNATURES = {
     "msa_rope_cache_write": (ctypes.c_int, [_CFG, _P, ctypes.POINTER(MsaRope)] + [_P] * 15),
     "msa_dense_decode_scratch_bytes": (ctypes.c_size_t, [_CFG]),
     "msa_dense_decode": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "msa_tree_plan": (ctypes.c_int, [_CFG] + [_P] * 5),
+    "msa_tree_attention_scratch_bytes": (ctypes.c_size_t, [_CFG]),
+    "msa_tree_attention": (ctypes.c_int, [_CFG] + [_P] * 9),
+    "msa_tree_verify": (ctypes.c_int, [_CFG, _P, _P, _P, ctypes.POINTER(MsaTreeProbs)] + [_P] * 6),
+    "msa_tree_commit": (ctypes.c_int, [_CFG, _P, _P, _P, ctypes.c_int32] + [_P] * 5),
     "msa_index_attention_scratch_bytes": (ctypes.c_size_t, [_CFG]),
     "msa_index_attention": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P]),
     "msa_topk_select": (ctypes.c_int, [_CFG, _P, _P, _P, _P]),
@@ -422,11 +437,14 @@ class _Layout:
         self.kv_dtypes = _kv_dtypes(cfg)
         self.ws = (workspace_bytes(cfg),)
         self.dense_scratch = (lib().msa_dense_decode_scratch_bytes(ctypes.byref(cfg)),)
+        self.tree_scratch = (lib().msa_tree_attention_scratch_bytes(ctypes.byref(cfg)),)
+        self.batch, self.paths = (cfg.max_batch,), (cfg.max_batch, MAX_TREE_NODES)
 
 
 _LAYOUTS = {}
 _Tensor = torch.Tensor
 _BF16, _F32, _I64, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int64,), (torch.uint8,)
+_I32 = (torch.int32,)
 
 
 def _layout(cfg) -> _Layout:
@@ -672,6 +690,136 @@ def dense_decode(cfg, ws, q, k_pages, v_pages, scratch, out, lse, stream=None):
         _check("msa_dense_decode", st)
 
 
+def tree_plan(cfg, ws, parents, tree_mask, positions=None, stream=None):
+    """What each node of the step's draft trees sees and where it stands, after
+    plan() (msa_tree_plan).  parents [T] int32: node indices within the request,
+    -1 = a root; tree_mask [T] int64 bits (out); positions [T] int64 (out), for
+    rope_cache_write, or None."""
+    y = _layout(cfg)
+    dev = _device_of(parents, "parents")
+    st = _call(lib().msa_tree_plan, dev, stream, ctypes.byref(cfg), _expect(ws, "ws", _U8, y.ws, dev),
+               _expect(parents, "parents", _I32, y.tokens, dev),
+               _expect(tree_mask, "tree_mask", _I64, y.tokens, dev),
+               None if positions is None else _expect(positions, "positions", _I64, y.tokens, dev))
+    if st:
+        _check("msa_tree_plan", st)
+
+
+def tree_attention_scratch_bytes(cfg) -> int:
+    n = lib().msa_tree_attention_scratch_bytes(ctypes.byref(cfg))
+    if n == 0:
+        _check("msa_tree_attention_scratch_bytes", validate_config(cfg) or 2)
+    return n
+
+
+def tree_attention(cfg, ws, q, k_pages, v_pages, tree_mask, scratch, out, lse, stream=None):
+    """Attention of every node of the step's draft trees over its request's
+    cached tokens and the nodes in its mask, any KV type (msa_tree_attention),
+    after plan() and the cache write of the step; no combine() follows.
+    tree_mask [T] int64 as tree_plan() writes it, or None: the new tokens are a
+    chain (a dense decode or verify).  scratch of
+    tree_attention_scratch_bytes(cfg) bytes."""
+    y = _layout(cfg)
+    dev = _device_of(q, "q")
+    if y.tree_scratch[0] == 0:
+        tree_attention_scratch_bytes(cfg)                # raises what the library says
+    st = _call(lib().msa_tree_attention, dev, stream, ctypes.byref(cfg),
+               _expect(ws, "ws", _U8, y.ws, dev), _expect(q, "q", _BF16, y.q, dev),
+               _expect(k_pages, "k_pages", y.kv_dtypes, y.pool, dev),
+               _expect(v_pages, "v_pages", y.kv_dtypes, y.pool, dev),
+               None if tree_mask is None else _expect(tree_mask, "tree_mask", _I64, y.tokens, dev),
+               _expect(scratch, "scratch", _U8, y.tree_scratch, dev),
+               _expect(out, "out", _BF16, y.q, dev), _expect(lse, "lse", _F32, y.lse, dev))
+    if st:
+        _check("msa_tree_attention", st)
+
+
+_PROB_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _expect_probs(t, name, T, vocab, dtype, dev):
+    """Pointer and row stride of [T, vocab] probabilities (rows contiguous)."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the step's other tensors")
+    if t.dtype is not dtype or dtype not in _PROB_DTYPES:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype} (float32 or bfloat16)")
+    s = t.shape
+    if len(s) != 2 or s[0] < T or s[1] != vocab or vocab < 1:
+        raise ValueError(f"{name} has shape {tuple(s)}, the step needs ({T}, {vocab})")
+    row, el = t.stride()
+    if (el != 1 and vocab > 1) or (T > 1 and row < vocab):
+        raise ValueError(f"{name}: a row's probabilities must be contiguous, rows apart")
+    return t.data_ptr(), (row if T > 1 else vocab)
+
+
+def tree_verify(cfg, ws, parents, tokens, target_probs, uniform, uniform_final, accepted,
+                num_accepted, out_tokens, draft_probs=None, stream=None):
+    """Accept the drafted tokens of the step's trees against the target's
+    probabilities, and draw the token after them (msa_tree_verify), after plan().
+    parents, tokens [T] int32; target_probs [T, vocab] float32 or bfloat16, any
+    row stride, row i the target's distribution after node i; draft_probs the
+    same of the draft model, whose row i node i's children were drawn from, or
+    None: the children were given.  uniform [T], uniform_final [max_batch]
+    float32 in [0, 1).  Out: accepted, out_tokens [max_batch, 64] int32 padded
+    with -1, num_accepted [max_batch] int32."""
+    y = _layout(cfg)
+    dev = _device_of(parents, "parents")
+    T = y.tokens[0]
+    if not isinstance(target_probs, _Tensor) or target_probs.dim() != 2:
+        raise ValueError("target_probs must be a CUDA tensor of 2 dims")
+    vocab, dt = target_probs.shape[1], target_probs.dtype
+    p_t, s_t = _expect_probs(target_probs, "target_probs", T, vocab, dt, dev)
+    p_d, s_d = None, 0
+    if draft_probs is not None:
+        p_d, s_d = _expect_probs(draft_probs, "draft_probs", T, vocab, dt, dev)
+    probs = MsaTreeProbs(p_t, p_d, vocab, _PROB_DTYPES[dt], s_t, s_d)
+    st = _call(lib().msa_tree_verify, dev, stream, ctypes.byref(cfg),
+               _expect(ws, "ws", _U8, y.ws, dev), _expect(parents, "parents", _I32, y.tokens, dev),
+               _expect(tokens, "tokens", _I32, y.tokens, dev), ctypes.byref(probs),
+               _expect(uniform, "uniform", _F32, y.tokens, dev),
+               _expect(uniform_final, "uniform_final", _F32, y.batch, dev),
+               _expect(accepted, "accepted", _I32, y.paths, dev),
+               _expect(num_accepted, "num_accepted", _I32, y.batch, dev),
+               _expect(out_tokens, "out_tokens", _I32, y.paths, dev))
+    if st:
+        _check("msa_tree_verify", st)
+
+
+def tree_commit(cfg, ws, accepted, num_accepted, k_pages, v_pages, idx_k_pages=None,
+                idx_v_pages=None, stream=None):
+    """Move the accepted nodes' rows of every layer's pools to consecutive cache
+    positions (msa_tree_commit), after tree_verify().  k_pages, v_pages (and
+    idx_k_pages, idx_v_pages): a pool, or a list of one pool per layer, each in
+    one list once (an NVFP4 pool as its layer's K and V)."""
+    y = _layout(cfg)
+    if len(k_pages) == 0:
+        raise ValueError("k_pages holds no pool")
+    dev = _device_of(accepted, "accepted")
+
+    def pointers(pools, name, dtypes, shape, n=None):
+        if pools is None:
+            return None
+        pools = [pools] if isinstance(pools, _Tensor) else pools
+        if n is not None and len(pools) != n:
+            raise ValueError(f"{name} has {len(pools)} layers, k_pages has {n}")
+        return (ctypes.c_void_p * len(pools))(*[_expect(p, name, dtypes, shape, dev)
+                                                for p in pools])
+
+    k = pointers(k_pages, "k_pages", y.kv_dtypes, y.pool)
+    n = len(k)
+    st = _call(lib().msa_tree_commit, dev, stream, ctypes.byref(cfg),
+               _expect(ws, "ws", _U8, y.ws, dev),
+               _expect(accepted, "accepted", _I32, y.paths, dev),
+               _expect(num_accepted, "num_accepted", _I32, y.batch, dev), n, k,
+               pointers(v_pages, "v_pages", y.kv_dtypes, y.pool, n),
+               pointers(idx_k_pages, "idx_k_pages", _BF16, y.idx_pool, n),
+               pointers(idx_v_pages, "idx_v_pages", _BF16, y.idx_pool, n))
+    if st:
+        _check("msa_tree_commit", st)
+
+
 def combine(cfg, ws, out, lse, stream=None):
     _need_ws(cfg, ws)
     _need_tokens(cfg, max_tokens(cfg), out=out, lse=lse)
@@ -731,11 +879,11 @@ class Rope:
         self.cos_sin, self.interleaved, self.idx_cos_sin = cos_sin, interleaved, idx_cos_sin
 
     def write(self, cfg, ws, q, k, v, idx_q, idx_k, q_out, idx_q_out, k_pages, v_pages,
-              idx_k_pages, out_cache_loc=None, stream=None):
+              idx_k_pages, out_cache_loc=None, stream=None, positions=None):
         rope_cache_write(cfg, ws, q, k, v, idx_q, idx_k, self.cos_sin, q_out, idx_q_out, k_pages,
                          v_pages, idx_k_pages, interleaved=self.interleaved,
-                         idx_cos_sin=self.idx_cos_sin, out_cache_loc=out_cache_loc,
-                         stream=stream)
+                         idx_cos_sin=self.idx_cos_sin, positions=positions,
+                         out_cache_loc=out_cache_loc, stream=stream)
 
 
 class SparseAttention:
@@ -855,6 +1003,76 @@ class DenseAttention:
                         stream)
         dense_decode(c, self.ws, q, k_pages, v_pages, self.scratch, self.out, self.lse, stream)
         return self.out, self.lse
+
+
+class TreeAttention:
+    """Owns the buffers of one full-attention layer shape for steps that verify
+    trees of drafted tokens (any KV type), and of their verification.  A step:
+    run() per layer (plan -> tree plan -> cache write -> tree attention), then
+    verify() with the target's probabilities, then commit() once with the pools
+    of all layers.  Further layers of a step: pass the first one's object as
+    `share` (its workspace, masks and positions) and run(planned=True)."""
+
+    def __init__(self, cfg: MsaConfig, device="cuda", rope: Optional[Rope] = None,
+                 share: Optional["TreeAttention"] = None):
+        self.cfg = cfg
+        self.rope = rope
+        _check("msa_validate_config", validate_config(cfg))
+        T, B = max_tokens(cfg), cfg.max_batch
+        self.max_tokens = T
+
+        def empty(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.scratch = empty(tree_attention_scratch_bytes(cfg), torch.uint8)
+        self.out = empty((T, cfg.num_q_heads, cfg.head_dim), torch.bfloat16)
+        self.lse = empty((T, cfg.num_q_heads), torch.float32)
+        if rope is not None:
+            self.q_rot = torch.empty_like(self.out)
+        if share is not None:
+            self.ws, self.tree_mask, self.positions = share.ws, share.tree_mask, share.positions
+            self.accepted, self.num_accepted = share.accepted, share.num_accepted
+            self.out_tokens = share.out_tokens
+            return
+        self.ws = empty(workspace_bytes(cfg), torch.uint8)
+        self.tree_mask, self.positions = empty(T, torch.int64), empty(T, torch.int64)
+        self.accepted = empty((B, MAX_TREE_NODES), torch.int32)
+        self.out_tokens = empty((B, MAX_TREE_NODES), torch.int32)
+        self.num_accepted = empty(B, torch.int32)
+
+    def run(self, seq_lens, block_table, parents, q, k_pages, v_pages, cu_seqlens_q=None,
+            stream=None, new_kv=None, out_cache_loc=None, planned=False):
+        """new_kv = (k, v) first stores the nodes' rows into the pools; with a
+        rope, q and k are rotated by the nodes' positions (their depth) on the
+        way."""
+        c = self.cfg
+        if self.rope is not None and new_kv is None:
+            raise ValueError("a rope rotates a step's new rows: new_kv is needed")
+        if not planned:
+            plan(c, seq_lens, block_table, self.ws, cu_seqlens_q, stream)
+            tree_plan(c, self.ws, parents, self.tree_mask, self.positions, stream)
+        if self.rope is not None:
+            self.rope.write(c, self.ws, q, *new_kv[:2], None, None, self.q_rot, None, k_pages,
+                            v_pages, None, out_cache_loc, stream, self.positions)
+            q = self.q_rot
+        elif new_kv is not None:
+            cache_write(c, self.ws, *new_kv[:2], None, k_pages, v_pages, None, out_cache_loc,
+                        stream)
+        tree_attention(c, self.ws, q, k_pages, v_pages, self.tree_mask, self.scratch, self.out,
+                       self.lse, stream)
+        return self.out, self.lse
+
+    def verify(self, parents, tokens, target_probs, uniform, uniform_final, draft_probs=None,
+               stream=None):
+        """(accepted, num_accepted, out_tokens) of the step (tree_verify)."""
+        tree_verify(self.cfg, self.ws, parents, tokens, target_probs, uniform, uniform_final,
+                    self.accepted, self.num_accepted, self.out_tokens, draft_probs, stream)
+        return self.accepted, self.num_accepted, self.out_tokens
+
+    def commit(self, k_pages, v_pages, idx_k_pages=None, idx_v_pages=None, stream=None):
+        """Keep the rows of the path that verify() accepted (tree_commit)."""
+        tree_commit(self.cfg, self.ws, self.accepted, self.num_accepted, k_pages, v_pages,
+                    idx_k_pages, idx_v_pages, stream)
 
 
 def sparse_decode_noalloc(cfg, seq_lens, block_table, q, k_pages, v_pages, selected, out, lse,

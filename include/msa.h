@@ -105,7 +105,13 @@ enum {
                                   prefill tiles (results involving it invalid).
                                   Magnitudes below 2^-14 are not flagged; they
                                   keep fp16's subnormal precision only.          */
-  MSA_DEVERR_POSITION = 32     /* a position outside the rotation table           */
+  MSA_DEVERR_POSITION = 32,    /* a position outside the rotation table           */
+  MSA_DEVERR_TREE = 64,        /* draft tree: more than MSA_MAX_TREE_NODES nodes, a
+                                  parent that is no earlier node of its request, a
+                                  drafted token outside the vocabulary, an accepted
+                                  list that is no path                            */
+  MSA_DEVERR_PROBS = 128       /* msa_tree_verify: a distribution without a positive
+                                  finite sum                                      */
 };
 
 /*
@@ -429,6 +435,127 @@ size_t msa_dense_decode_scratch_bytes(const msa_config* cfg);
 msa_status msa_dense_decode(const msa_config* cfg, void* ws, const void* q, const void* k_pages,
                             const void* v_pages, void* scratch, void* out, float* lse,
                             msa_stream_t stream);
+
+/*
+ * Draft trees.  A verify step may carry, instead of a chain, a tree of drafted
+ * tokens per request: its n new tokens are the tree's nodes, node 0 the root
+ * (the last token of the sequence, whose row is not cached yet), every node's
+ * parent an earlier node.  Node i is stored at cache position base + i, base =
+ * seq_len - n (msa_cache_write and msa_rope_cache_write with the plan's slots
+ * do that), and stands for the token at position base + depth.  A step:
+ *
+ *     msa_plan -> msa_tree_plan -> per full-attention layer: the cache write
+ *     (msa_rope_cache_write with msa_tree_plan's positions) and
+ *     msa_tree_attention -> (the model's logits) -> msa_tree_verify ->
+ *     msa_tree_commit (once for all layers)
+ *
+ * All four run after msa_plan of the step on its workspace, in either mode, any
+ * number of nodes per request up to MSA_MAX_TREE_NODES (cu_seqlens_q, or
+ * cfg->q_len of them each).  The pages have chains only (vLLM
+ * MiniMaxM3SparseMSAMetadataBuilder.build: decode_query_len).
+ */
+#define MSA_MAX_TREE_NODES 64
+
+/*
+ * msa_tree_plan -- what the nodes see and where they stand.
+ *   parents    [T] int32, node indices within the request, -1 = none (a root);
+ *              with several roots only node 0's tree is verified
+ *   tree_mask  [T] int64: bit j = the node sees node j of its request (itself
+ *              and its ancestors)
+ *   positions  [T] int64: base + depth, for msa_rope_cache_write; or NULL
+ * A parent that is not -1 and no earlier node sets MSA_DEVERR_TREE and counts as
+ * -1.  Requests of more than MSA_MAX_TREE_NODES nodes set it too; their tokens,
+ * and those of idle requests, get mask 0 and position -1.
+ */
+msa_status msa_tree_plan(const msa_config* cfg, void* ws, const int32_t* parents,
+                         int64_t* tree_mask, int64_t* positions, msa_stream_t stream);
+
+/*
+ * msa_tree_attention -- full-context attention of draft trees (and, with
+ * tree_mask NULL, of chains: the dense decode and verify over any KV type).
+ * Node i of a request, for each query head, over the keys at positions u < base
+ * and u = base + j with bit j of its mask set (j < n; NULL: j <= i):
+ *     out = sum_u softmax_u(softmax_scale q . k_u) v_u,  lse = natural-log sum
+ *   tree_mask [T] int64 as msa_tree_plan writes it, or any other
+ *   scratch   msa_tree_attention_scratch_bytes(cfg) bytes, 256-byte aligned, no
+ *             initialisation needed; calls that overlap on the GPU need one each
+ *   out [T, H_q, D] bf16 (16-byte aligned), lse [T, H_q] float
+ * A node that sees nothing gets out = 0, lse = -inf; so do idle requests' and
+ * those of requests with more than MSA_MAX_TREE_NODES nodes (MSA_DEVERR_TREE).
+ * What a node does not see does not reach it, infinities and NaN included.
+ * Values beyond the fp16 range (and queries, with e4m3 or NVFP4 pools) set
+ * MSA_DEVERR_FP16_RANGE.  Pages that the plan flagged are skipped.  Rows of out
+ * and lse from T on are left as they are.  softmax_scale * k_scale has to be a
+ * positive finite float; max_batch * max_blocks_per_req * H_kv < 2^27 and
+ * num_pages * H_kv < 2^24, else MSA_ERR_UNSUPPORTED.
+ */
+size_t msa_tree_attention_scratch_bytes(const msa_config* cfg);
+msa_status msa_tree_attention(const msa_config* cfg, void* ws, const void* q,
+                              const void* k_pages, const void* v_pages,
+                              const int64_t* tree_mask, void* scratch, void* out, float* lse,
+                              msa_stream_t stream);
+
+/* The distributions of msa_tree_verify: one row of vocab probabilities a node. */
+typedef struct msa_tree_probs {
+  const void* target;         /* [T, vocab]: row i = the target's distribution of the
+                                 token after node i                               */
+  const void* draft;          /* [T, vocab]: row i = the distribution that node i's
+                                 children were drawn from (independently), or
+                                 NULL: the children are given, not drawn          */
+  int32_t vocab;
+  int32_t dtype;              /* of both: 0 = float, 1 = bf16                     */
+  int64_t target_stride, draft_stride;   /* elements from row to row              */
+} msa_tree_probs;
+
+/*
+ * msa_tree_verify -- which drafted tokens stand, and the token after them, so
+ * that the emitted tokens are distributed as the target's own.  From node x = 0,
+ * with w = target row x, Z = 1, A = 0, over x's children c in ascending order, y
+ * = tokens[c]:
+ *     given drafts:  c stands if uniform[c] Z < w(y); else Z -= w(y), w(y) = 0
+ *     drawn drafts:  c stands if uniform[c] draft_x(y) Z < w(y); else A += Z,
+ *                    w = max(target_x - A draft_x, 0), Z = sum w
+ * The first child that stands becomes x.  Where none does, the last token is
+ * the lowest v with w(0) + ... + w(v) > uniform_final[r] * sum w.  If that sum is
+ * 0 it is drawn from the target's row instead.  Products, comparisons and sums
+ * carry 45 bits or more.  Target rows count as normalised (Z = 1).
+ *   parents, tokens  [T] int32 (a root's token is not read)
+ *   uniform          [T] float in [0, 1);  uniform_final [batch] float in [0, 1)
+ *   accepted         [max_batch, MSA_MAX_TREE_NODES] int32: the path's nodes,
+ *                    from the root, -1 after them
+ *   num_accepted     [max_batch] int32: nodes of the path (1 = the root alone):
+ *                    the rows of the step that stay in the cache
+ *   out_tokens       [max_batch, MSA_MAX_TREE_NODES] int32: the num_accepted new
+ *                    tokens (those of the path's nodes after the root, then the
+ *                    drawn one), -1 after them
+ * Only rows of the batch are written.  Idle requests, and those of more than
+ * MSA_MAX_TREE_NODES nodes (MSA_DEVERR_TREE), get num_accepted 0.  A drafted token
+ * outside the vocabulary is refused and sets MSA_DEVERR_TREE.  Where no positive
+ * finite sum is found the last token is -1 and MSA_DEVERR_PROBS is set.
+ */
+msa_status msa_tree_verify(const msa_config* cfg, void* ws, const int32_t* parents,
+                           const int32_t* tokens, const msa_tree_probs* probs,
+                           const float* uniform, const float* uniform_final, int32_t* accepted,
+                           int32_t* num_accepted, int32_t* out_tokens, msa_stream_t stream);
+
+/*
+ * msa_tree_commit -- the accepted nodes' rows move together: of every request,
+ * the row at position base + accepted[j] goes to base + j, for j below
+ * num_accepted, in the K and V (and index-K, index-V) pools of num_layers
+ * layers.  The sequence then has base + num_accepted cached tokens.
+ *   k_pages, v_pages, idx_k_pages, idx_v_pages   host arrays of num_layers device
+ *            pointers to pools (layouts above; NVFP4: k_pages and v_pages may hold
+ *            the same pools); the index arrays may be NULL.  A pool stands in a
+ *            list once; up to 1024 layers, else MSA_ERR_UNSUPPORTED
+ * accepted has to ascend within the request's nodes (as msa_tree_verify writes
+ * it); a list that does not moves nothing and sets MSA_DEVERR_TREE.  Positions on
+ * pages that the plan flagged are left.  Pointers 16-byte aligned.
+ */
+msa_status msa_tree_commit(const msa_config* cfg, void* ws, const int32_t* accepted,
+                           const int32_t* num_accepted, int32_t num_layers,
+                           void* const* k_pages, void* const* v_pages,
+                           void* const* idx_k_pages, void* const* idx_v_pages,
+                           msa_stream_t stream);
 
 /*
  * msa_combine -- log-sum-exp merge of the split-K partials in ws

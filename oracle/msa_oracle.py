@@ -45,7 +45,8 @@ __all__ = [
     "attention", "combine", "sparse_attention", "build_k2q_csr", "e4m3_encode",
     "cache_slots", "cache_write", "e2m1_to_float", "nvfp4_dequant", "nvfp4_row_bytes",
     "NVFP4_BLOCK", "e2m1_encode", "nvfp4_quantize", "cache_write_nvfp4", "compact_selection", "paged_attention", "index_attention",
-    "rotate_rows", "bf16_round", "dense_attention",
+    "rotate_rows", "bf16_round", "dense_attention", "tree_masks", "tree_attention", "tree_verify",
+    "tree_commit",
 ]
 
 
@@ -556,6 +557,103 @@ def dense_attention(*, seq_lens, q_lens, block_table, q, k, v, num_kv_heads: int
             out[t, rows], lse[t, rows] = attention(q[t, rows], kk, vv, softmax_scale)
             mag[t, rows], _ = attention(q[t, rows], kk, np.abs(vv), softmax_scale)
     return out, lse, mag
+
+
+# --------------------------------------------------------------------------
+# Draft trees: node i of a request's n nodes is stored at position base + i,
+# base = seq_len - n; a parent is an earlier node of the request or -1.
+# --------------------------------------------------------------------------
+def tree_masks(parents: Sequence[int]) -> List[int]:
+    """Bit j of entry i: node j is node i or an ancestor of it."""
+    masks: List[int] = []
+    for i, p in enumerate(parents):
+        masks.append((1 << i) | (masks[p] if p >= 0 else 0))
+    return masks
+
+
+def tree_attention(*, seq_lens, q_lens, masks, block_table, q, k, v, num_kv_heads: int,
+                   block_size: int, softmax_scale: float):
+    """Node i attends to the positions below base and to base + j for the bits j
+    of its mask.  ``masks``: one int per node, request after request.  Returns
+    out, lse and the attention of |v|, as dense_attention."""
+    T, H_q, D = q.shape
+    G = H_q // num_kv_heads
+    out, mag = np.zeros((T, H_q, D)), np.zeros((T, H_q, D))
+    lse = np.full((T, H_q), -np.inf)
+    t = 0
+    for r, (L, n) in enumerate(zip(seq_lens, q_lens)):
+        L, n = int(L), int(n)
+        if L == 0:
+            t += n
+            continue
+        ks = gather_sequence(k, block_table[r], L, block_size)
+        vs = gather_sequence(v, block_table[r], L, block_size)
+        for i in range(n):
+            see = list(range(L - n)) + [L - n + j for j in range(n) if int(masks[t]) >> j & 1]
+            for h in range(num_kv_heads):
+                rows = slice(h * G, (h + 1) * G)
+                if see:
+                    out[t, rows], lse[t, rows] = attention(q[t, rows], ks[see, h], vs[see, h],
+                                                           softmax_scale)
+                    mag[t, rows], _ = attention(q[t, rows], ks[see, h], np.abs(vs[see, h]),
+                                                softmax_scale)
+            t += 1
+    return out, lse, mag
+
+
+def tree_verify(parents: Sequence[int], tokens: Sequence[int], target: np.ndarray, draft,
+                uniform: Sequence[float], uniform_final: float):
+    """One request: (path of accepted nodes from the root, new tokens).  ``target``
+    [n, V]: the target's distribution after each node; ``draft`` the same of the
+    draft, or None where the children were given and not drawn."""
+    x, path = 0, [0]
+    while True:
+        p = np.asarray(target[x], dtype=np.float64)
+        w, z, spent, nxt = np.maximum(p, 0.0), 1.0, 0.0, None
+        for c in range(len(parents)):
+            if parents[c] != x:
+                continue
+            y = int(tokens[c])
+            known = 0 <= y < len(p)
+            have = w[y] if known else 0.0
+            q = None if draft is None else np.asarray(draft[x], dtype=np.float64)
+            drawn = 1.0 if q is None or not known else q[y]
+            if float(uniform[c]) * drawn * z < have:
+                nxt = c
+                break
+            if q is None:
+                z -= have
+                if known:
+                    w[y] = 0.0
+            else:
+                spent += z
+                w = np.maximum(p - spent * q, 0.0)
+                z = w.sum()
+        if nxt is None:
+            break
+        x = nxt
+        path.append(x)
+    if w.sum() == 0.0:
+        w = np.maximum(p, 0.0)
+    total = np.cumsum(w)
+    above = np.nonzero(total > float(uniform_final) * total[-1])[0]
+    last = int(above[0]) if len(above) else int(np.nonzero(w > 0)[0][-1])
+    return path, [int(tokens[c]) for c in path[1:]] + [last]
+
+
+def tree_commit(pool: np.ndarray, seq_len: int, nodes: int, block_table_row, path: Sequence[int],
+                block_size: int) -> None:
+    """Rows of ``pool`` [pages, H, P, row], in place: position base + path[j] ->
+    base + j."""
+    base = int(seq_len) - int(nodes)
+
+    def at(u):
+        return int(block_table_row[u // block_size]), u % block_size
+
+    rows = [pool[at(base + c)[0], :, at(base + c)[1]].copy() for c in path]
+    for j, row in enumerate(rows):
+        page, line = at(base + j)
+        pool[page, :, line] = row
 
 
 # --------------------------------------------------------------------------
