@@ -25,14 +25,14 @@
 // partial per CTA in the scratch, which a second kernel merges in CTA order.
 //
 // A CTA: a loader warp (pages by TMA into a ring), four converter warps (Q rows,
-// and the pages' rows as MMA operands), an MMA warp and eight softmax warps.  An
-// item is one (page, tile): S = Q K^T (128 rows x 128 keys) into one of two TMEM
-// buffers, the two softmax warpgroups take half a row a thread (TMEM lane = query
-// row), write P over their half of S, and O += P V with P as the A operand from
-// TMEM.  S of the next item is computed during the softmax of this one.  The two
-// threads of a row agree on m through one barrier with a vote.
+// and the pages' rows as MMA operands), an MMA warp and two softmax warpgroups.  An
+// item is one (page, tile): S = Q K^T (128 rows x 128 keys), softmax by a thread a
+// row (its TMEM lane), P over S, O += P V with P as the A operand from TMEM.  Items
+// alternate between the warpgroups, each of which has TMEM of its own for S and O:
+// of a pair of tiles each takes one, of a single tile every second page, whose two
+// results (m, sum, O) are joined at the end of the segment.  While one warpgroup
+// has its softmax, the tensor cores work for the other.
 #include <atomic>
-#include <cfloat>
 #include <cstring>
 
 #include "tcgen05.cuh"
@@ -46,18 +46,16 @@ constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kPairRows = 2 * kTile;
 constexpr int kMaxCtas = 320;
 constexpr float kBias = 7.f;                   // exponent offset of the probabilities
-constexpr float kSlack = 8.f;                  // 2^(kBias + kSlack) is below fp16's largest
+constexpr float kMaxSum = 60000.f;             // a row's sum over a page that fp16 holds
+constexpr float kNear = 64.f;                  // |m| of the fast path, in exponents
 
-constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kConvWarp = kSoftWarps, kLoadWarp = kConvWarp + kConvWarps, kMmaWarp = kLoadWarp + 1,
-              kIdleWarp = kMmaWarp + 1, kThreads = 512;
-// threads x launch registers = 512 x 128 = 256 x 176 + 128 x 104 + 128 x 56
-constexpr int kSoftRegs = 176, kConvRegs = 104, kMiscRegs = 56;
+constexpr int kSoftWarps = 8, kConvWarp = kSoftWarps;
+constexpr int kBads = 16;
 
 struct TreeArgs {
   int Hkv, Hq, G, max_blocks, rows;            // rows: of a partial
   uint32_t g_magic;                            // row / G = row * g_magic >> 20
-  float scale_log2, v_scale, slack;            // slack: kSlack in unscaled scores
+  float scale_log2, v_scale;
   const __nv_bfloat16* q;
   const uint8_t *k_pool, *v_pool;
   const int64_t* mask;
@@ -77,15 +75,26 @@ struct TreeArgs {
   }
 };
 
-// KV types: tiles of the operand ring, raw stages in front of the converters.
+// KV types: tiles of the operand ring, raw stages in front of the converters.  bf16
+// tiles arrive in the ring itself.  With raw stages, a segment of one tile uses the
+// second Q buffer as a fourth tile of the ring.
 template <int KV>
 struct Form {
   static constexpr bool kRaw = KV != MSA_KV_BF16;
   static constexpr int kTiles = kRaw ? 3 : 5;
+  static constexpr int kBufs = kRaw ? kTiles + 1 : kTiles;
   static constexpr int kStages = KV == MSA_KV_FP8_E4M3 ? 4 : (KV == MSA_KV_NVFP4 ? 7 : 1);
   static constexpr int kStageBytes =
       KV == MSA_KV_FP8_E4M3 ? kBlock * kHeadDim : (KV == MSA_KV_NVFP4 ? kBlock * kFp4Row : 0);
   static constexpr int kSmem = (2 + kTiles) * kTileBytes + (kRaw ? kStages * kStageBytes : 0);
+  // Warps: softmax, converters, loader, two for the MMAs, one for idle tokens.
+  static constexpr int kConvWarps = kRaw ? 8 : 4, kLoadWarp = kConvWarp + kConvWarps,
+                       kMmaWarp = kLoadWarp + 1, kIdleWarp = kMmaWarp + 2,
+                       kThreads = 32 * (kIdleWarp + 1), kConvThreads = 32 * kConvWarps;
+  // threads x launch registers: 512 x 128 = 256 x 176 + 128 x 96 + 128 x 64;
+  // 640 x 96 >= 256 x 152 + 256 x 56 + 128 x 56
+  static constexpr int kSoftRegs = kRaw ? 152 : 176, kConvRegs = kRaw ? 56 : 96,
+                       kMiscRegs = kRaw ? 56 : 64;
   // weight of a page for a pair of two tiles and of one
   static constexpr int kW2 = 1, kW1 = 1;
 };
@@ -95,18 +104,45 @@ template <int KV>
 struct Shared {
   using F = Form<KV>;
   uint64_t raw_full[F::kStages], raw_empty[F::kStages];
-  uint64_t full[F::kTiles], ready[F::kTiles], empty[F::kTiles];
+  uint64_t full[F::kBufs], ready[F::kBufs], empty[F::kBufs];
   uint64_t q_full[2], q_free[2];
-  uint64_t s_ready[2], p_ready[2], o_done[2];
-  uint64_t fin;
-  unsigned long long bad[8];                   // by segment: nodes with values that are not finite
-  float red[2][kTile];
+  uint64_t s_ready[2], p_ready[2], o_done[2], turn[2], fin[2];
+  unsigned long long bad[kBads];               // by segment: nodes with values that are not finite
+  float2 ml[2][kTile];                         // by warpgroup: (m, sum) of a row
   uint32_t tmem_base;
   // the CTA's range
   int r0;                                      // first request, and the weight before it
   uint32_t w0, from, to, total, ranges;
-  uint32_t part[kThreads / 32];
+  uint32_t part[F::kThreads / 32];
 };
+
+// The ring of operand tiles as a role goes through it: the next buffer, and for each
+// whether its uses so far are odd or even (bit b), its uses for values alike.
+template <int KV>
+struct Ring {
+  int pos = 0;
+  uint32_t uses = 0, v_uses = 0;
+  // the next tile's buffer; `tiles`: of the segment.  par: parity of this use
+  __device__ __forceinline__ int take(int tiles, bool values, uint32_t& par, uint32_t& v_par) {
+    const int n = Form<KV>::kRaw && tiles == 1 ? Form<KV>::kBufs : Form<KV>::kTiles;
+    const int b = pos < n ? pos : 0;
+    pos = b + 1;
+    par = uses >> b & 1u;
+    v_par = v_uses >> b & 1u;
+    uses ^= 1u << b;
+    if (values) v_uses ^= 1u << b;
+    return b;
+  }
+  __device__ __forceinline__ int take(int tiles, bool values, uint32_t& par) {
+    uint32_t v;
+    return take(tiles, values, par, v);
+  }
+};
+// Byte offset of buffer b from the first Q tile.
+template <int KV>
+__device__ __forceinline__ uint32_t tile_at(int b) {
+  return (uint32_t)(Form<KV>::kRaw && b == Form<KV>::kTiles ? 1 : 2 + b) * kTileBytes;
+}
 
 // Weights.  A request: heads x pairs of tiles x pages.
 struct Req {
@@ -203,17 +239,66 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(p));
   return p != 0;
 }
-// Barrier over `count` threads that also tells whether any of them said so.
-__device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
-  int any;
+
+// Lane i of the warp's quarter, 64 columns.
+__device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&r)[64]) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n"
-      " selp.b32 %0, 1, 0, q;\n}"
-      : "=r"(any)
-      : "r"(id), "r"(count), "r"((int)mine)
+      "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%"
+      "23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%"
+      "43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%"
+      "63,%64"
+      "};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+      "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]), "r"(r[36]), "r"(r[37]),
+      "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]), "r"(r[43]),
+      "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]),
+      "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]),
+      "r"(r[56]), "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]),
+      "r"(r[62]), "r"(r[63])
       : "memory");
-  return any != 0;
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for this thread's TMEM loads; the registers pass through it, so that no use
+// of them moves before it.
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+        "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+        "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+        "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+        "+r"(r[30]), "+r"(r[31])
+      :
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+        "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+        "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :
+      : "memory");
+}
+// Scores of consecutive columns, and the wait for them.
+__device__ __forceinline__ void ld_scores(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void ld_scores(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void wait_scores(uint32_t (&r)[32]) { tmem_wait32(r); }
+__device__ __forceinline__ void wait_scores(uint32_t (&r)[16]) { tmem_wait16(r); }
 
 // ---------------------------------------------------------------- conversion
 // Sixteen-bit pairs with an all-ones exponent -> 0; true if there was one.
@@ -237,13 +322,14 @@ __device__ __forceinline__ void to_f16(const uint4& x, uint32_t (&h)[4]) {
 }
 
 // One page's K or V slot -> the operand tile at `tile` (K-major rows, 128-byte
-// swizzle), by 128 threads.  kValues: rows from `ntok` on become 0; of rows from
+// swizzle), by all converter threads.  kValues: rows from `ntok` on become 0; of rows from
 // `all` on (which not every query row sees: 0 * NaN is not 0) elements that are
 // not finite become 0 and are noted in `bad` by node.  A bf16 tile is converted in
 // place.  Returns whether a value left the fp16 range.
 template <int KV, bool kValues>
 __device__ __forceinline__ bool convert_page(const uint8_t* raw, uint8_t* tile, int tid, int ntok,
                                              int all, unsigned long long* bad) {
+  constexpr int kN = Form<KV>::kConvThreads;
   bool ovf = false;
   auto special = [&](int key, uint32_t (&h)[4]) {
     if (key >= ntok) {
@@ -258,8 +344,8 @@ __device__ __forceinline__ bool convert_page(const uint8_t* raw, uint8_t* tile, 
     if (all >= kBlock) {
       uint32_t top = 0u;                       // largest magnitudes
 #pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int off = (tid + 128 * i) * 16;
+      for (int i = 0; i < kTileBytes / 16 / kN; ++i) {
+        const int off = (tid + kN * i) * 16;
         uint32_t h[4];
         to_f16(*reinterpret_cast<const uint4*>(tile + off), h);
 #pragma unroll
@@ -274,8 +360,8 @@ __device__ __forceinline__ bool convert_page(const uint8_t* raw, uint8_t* tile, 
       ovf = f16x2_has_inf(top);
     } else {
 #pragma unroll 1
-      for (int i = 0; i < 16; ++i) {
-        const int off = (tid + 128 * i) * 16;
+      for (int i = 0; i < kTileBytes / 16 / kN; ++i) {
+        const int off = (tid + kN * i) * 16;
         uint32_t h[4];
         to_f16(*reinterpret_cast<const uint4*>(tile + off), h);
         special((off & (kTileBytes / 2 - 1)) >> 7, h);
@@ -285,9 +371,9 @@ __device__ __forceinline__ bool convert_page(const uint8_t* raw, uint8_t* tile, 
   } else if constexpr (KV == MSA_KV_FP8_E4M3) {
     // eight lanes take one 16-byte chunk of eight rows: the swizzles of the raw
     // tile and of the operand spread them over all banks
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int x = tid + 128 * i, key = (x & 7) | ((x >> 6) << 3), c = (x >> 3) & 7;
+#pragma unroll
+    for (int i = 0; i < 1024 / kN; ++i) {
+      const int x = tid + kN * i, key = (x & 7) | ((x >> 6) << 3), c = (x >> 3) & 7;
       const uint4 w = *reinterpret_cast<const uint4*>(raw + key * 128 + ((c ^ (key & 7)) << 4));
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -306,9 +392,9 @@ __device__ __forceinline__ bool convert_page(const uint8_t* raw, uint8_t* tile, 
   } else {
     // sixteen lanes take one block of sixteen rows: 72-byte rows spread over all
     // banks, and so does the operand's swizzle
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int x = tid + 128 * i, key = (x & 15) | ((x >> 7) << 4), b = (x >> 4) & 7;
+#pragma unroll
+    for (int i = 0; i < 1024 / kN; ++i) {
+      const int x = tid + kN * i, key = (x & 15) | ((x >> 7) << 4), b = (x >> 4) & 7;
       const uint8_t* row = raw + key * kFp4Row;
       const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * b);
       const uint32_t s = e4m3_scale_f16x2(row[kHeadDim / 2 + b]);
@@ -352,36 +438,38 @@ __device__ __forceinline__ float value_of(const uint8_t* v_pool, int64_t page, i
 
 // ---------------------------------------------------------------- the kernel
 template <int KV>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<KV>::kThreads, 1)
 tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v) {
   using F = Form<KV>;
+  constexpr int kThreads = F::kThreads, kLoadWarp = F::kLoadWarp, kMmaWarp = F::kMmaWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(16) Shared<KV> sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
-  uint8_t* qbuf = smem;                        // two tiles
-  uint8_t* tiles = smem + 2 * kTileBytes;
-  uint8_t* raw = tiles + F::kTiles * kTileBytes;
+  uint8_t* qbuf = smem;                        // two tiles, then the ring's
+  uint8_t* raw = smem + (2 + F::kTiles) * kTileBytes;
   if (tid == 0) {
     for (int i = 0; i < F::kStages; ++i) {
       mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], kConvWarps);
+      mbar_init(&sh.raw_empty[i], F::kConvWarps);
     }
-    for (int i = 0; i < F::kTiles; ++i) {
+    for (int i = 0; i < F::kBufs; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.ready[i], kConvWarps);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.ready[i], F::kConvWarps);
+      // both MMA warps, or one twice; of tiles that arrive in the ring the converters too
+      mbar_init(&sh.empty[i], F::kRaw ? 2 : 2 + F::kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], kConvWarps);
-      mbar_init(&sh.q_free[i], 1);
+      mbar_init(&sh.q_full[i], F::kConvWarps);
+      mbar_init(&sh.q_free[i], 2);             // both MMA warps
       mbar_init(&sh.s_ready[i], 1);
-      mbar_init(&sh.p_ready[i], kSoftWarps);
+      mbar_init(&sh.p_ready[i], 4);
       mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.turn[i], 1);
+      mbar_init(&sh.fin[i], 1);
     }
-    mbar_init(&sh.fin, 1);
-    for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
+    for (int i = 0; i < kBads; ++i) sh.bad[i] = 0;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -456,220 +544,270 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
   const uint32_t tmem = sh.tmem_base;
 
   if (warp >= kLoadWarp) {
-    regs_down<kMiscRegs>();
-  if (warp == kLoadWarp) {
-    // ---------------------------------------------------------------- loader
-    // The pages of a segment 32 at a time (a lane each).
-    Walk<KV> wk;
-    wk.open(ws, a, sh);
-    int arms = 0, at = 0;
-    uint32_t phase = 0;
-    constexpr int kSlots = F::kRaw ? F::kStages : F::kTiles;
-    while (wk.next(ws, a)) {
-      int mine = -1;
-      for (int j = wk.j0; j < wk.j1; ++j) {
-        const int k = (j - wk.j0) & 31;
-        if (k == 0)
-          mine = j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + j + lane] : -1;
-        const int page = __shfl_sync(0xffffffffu, mine, k);
-        for (int kind = 0; kind < 2; ++kind) {
-          uint64_t* full = F::kRaw ? &sh.raw_full[at] : &sh.full[at];
-          mbar_wait(F::kRaw ? &sh.raw_empty[at] : &sh.empty[at], phase ^ 1u, ws.hdr);
-          __syncwarp();
-          if (elect_one()) {
-            if (page < 0) {
-              mbar_arrive(full);
-            } else if constexpr (KV == MSA_KV_NVFP4) {
-              const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2 + kind;
-              const int rows = min(kBlock, wk.q.L - j * kBlock);
-              const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;   // a multiple of 16
-              mbar_arrive_expect_tx(full, bytes);
-              bulk_load(raw + at * F::kStageBytes,
-                        (kind ? a.v_pool : a.k_pool) + slot * (kBlock * kFp4Row), bytes, full);
+    regs_down<F::kMiscRegs>();
+    if (warp == kLoadWarp) {
+      // -------------------------------------------------------------- loader
+      // The pages of a segment 32 at a time (a lane each).
+      Walk<KV> wk;
+      wk.open(ws, a, sh);
+      Ring<KV> ring;                           // bf16: the operand ring itself
+      int arms = 0, at = 0;
+      uint32_t phase = 0;
+      bool going = true;                       // after a wait gave up nothing more is copied
+      while (going && wk.next(ws, a)) {
+        int mine = -1;
+        for (int j = wk.j0; going && j < wk.j1; ++j) {
+          const int k = (j - wk.j0) & 31;
+          if (k == 0)
+            mine = j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + j + lane] : -1;
+          const int page = __shfl_sync(0xffffffffu, mine, k);
+          for (int kind = 0; going && kind < 2; ++kind) {
+            uint64_t* full;
+            uint8_t* dst;
+            if constexpr (F::kRaw) {
+              full = &sh.raw_full[at];
+              dst = raw + at * F::kStageBytes;
+              going = mbar_wait(&sh.raw_empty[at], phase ^ 1u, ws.hdr);
+              if (++at == F::kStages) { at = 0; phase ^= 1u; }
             } else {
-              const int y = (page * a.Hkv + wk.h) * kBlock;
-              const void* map = kind ? (const void*)&tmap_v : (const void*)&tmap_k;
-              if constexpr (KV == MSA_KV_FP8_E4M3) {
-                mbar_arrive_expect_tx(full, F::kStageBytes);
-                tma_load_2d(raw + at * F::kStageBytes, map, 0, y, full);
+              uint32_t par;
+              const int b = ring.take(wk.tiles, kind, par);
+              full = &sh.full[b];
+              dst = smem + tile_at<KV>(b);
+              going = mbar_wait(&sh.empty[b], par ^ 1u, ws.hdr);
+            }
+            going = __all_sync(0xffffffffu, going);
+            if (going && elect_one()) {
+              if (page < 0) {
+                mbar_arrive(full);
+              } else if constexpr (KV == MSA_KV_NVFP4) {
+                const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2 + kind;
+                const int rows = min(kBlock, wk.q.L - j * kBlock);
+                const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;   // 16 divides it
+                mbar_arrive_expect_tx(full, bytes);
+                bulk_load(dst, (kind ? a.v_pool : a.k_pool) + slot * (kBlock * kFp4Row), bytes,
+                          full);
               } else {
-                mbar_arrive_expect_tx(full, kTileBytes);
-                tma_load_2d(tiles + at * kTileBytes, map, 0, y, full);
-                tma_load_2d(tiles + at * kTileBytes + kTileBytes / 2, map, 64, y, full);
+                const int y = (page * a.Hkv + wk.h) * kBlock;
+                const void* map = kind ? (const void*)&tmap_v : (const void*)&tmap_k;
+                if constexpr (KV == MSA_KV_FP8_E4M3) {
+                  mbar_arrive_expect_tx(full, F::kStageBytes);
+                  tma_load_2d(dst, map, 0, y, full);
+                } else {
+                  mbar_arrive_expect_tx(full, kTileBytes);
+                  tma_load_2d(dst, map, 0, y, full);
+                  tma_load_2d(dst + kTileBytes / 2, map, 64, y, full);
+                }
               }
             }
+            __syncwarp();
+            if (going) ++arms;
+          }
+        }
+      }
+      // Normally the converters and the MMAs wait for every copy issued here.
+      // After a wait gave up they may not have: let the copies in flight land.
+      if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
+        constexpr int kSlots = F::kRaw ? F::kStages : F::kTiles;
+        for (int i = 0; i < kSlots && i < arms; ++i)
+          mbar_drain(F::kRaw ? &sh.raw_full[i] : &sh.full[i],
+                     (uint32_t)(((arms - 1 - i) / kSlots) & 1));
+      }
+    } else if (warp < F::kIdleWarp) {
+      // ---------------------------------------------------------------- MMAs
+      // A warp per softmax warpgroup w, on the items of w: O += P V, then the next S
+      // once that has read the P which it overwrites.  The same wait orders O for
+      // the softmax: where an S is there, O holds the items before it.  The two
+      // warps take turns, an item's P V and the next S together: left to themselves
+      // they fall into step, both in the tensor cores, then both in the softmax.
+      const int w = warp - kMmaWarp;
+      const uint32_t idesc_s = idesc_f16(F::kRaw ? 0 : 1, kTile, kBlock),
+                     idesc_o = idesc_f16_bmn(0, kTile, kHeadDim);
+      const uint64_t d0 = kstep_desc(smem_u32(smem), 0, kTile),
+                     v0 = sdesc_sw128_mn(smem_u32(smem), kTileBytes / 2);
+      const uint32_t lo = (uint32_t)d0, hi = (uint32_t)(d0 >> 32), v_lo = (uint32_t)v0,
+                     v_hi = (uint32_t)(v0 >> 32);
+      const uint32_t ts = tmem + w * 128, to = tmem + 256 + w * 128;
+      Walk<KV> wk;
+      Ring<KV> ring;
+      wk.open(ws, a, sh);
+      int k0 = 0, mine = 0, qsel = 0;          // first item of the segment; items of w so far
+      uint32_t q_phase = 0;                    // bit b: uses of Q buffer b, odd or even
+      while (wk.next(ws, a)) {
+        const bool two = wk.tiles == 2;
+        const int pages = wk.j1 - wk.j0, odd = (w ^ k0) & 1;
+        const int qb = two ? odd : (F::kRaw ? 0 : qsel);         // this warp's Q
+        const int step = two ? 1 : 2;
+        if (!two) qsel ^= 1;
+        int kb, vb, kb2 = 0, vb2 = 0;          // tiles of the page, and of this warp's next
+        uint32_t kpar, vpar, kpar2 = 0, vpar2 = 0;
+        auto take = [&](int& k_, uint32_t& kp_, int& v_, uint32_t& vp_) {
+          uint32_t x;
+          k_ = ring.take(wk.tiles, false, kp_, x);
+          v_ = ring.take(wk.tiles, true, vp_, x);
+          if (!F::kRaw) vp_ = x;               // bf16: `ready` counts values alone
+        };
+        auto issue_s = [&](int k_, int p, bool pass) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t qd = lo + qb * (kTileBytes >> 4), kd = lo + (tile_at<KV>(k_) >> 4);
+            umma_ss<false>(ts, qd, hi, kd, hi, idesc_s);
+#pragma unroll
+            for (int ks = 1; ks < 8; ++ks) {
+              const uint32_t o = (ks >> 2) * (kTileBytes >> 5) + (ks & 3) * 2;
+              umma_ss<true>(ts, qd + o, hi, kd + o, hi, idesc_s);
+              // the other warp's MMAs queue up behind the last of these
+              if (ks == 4 && pass) mbar_arrive(&sh.turn[w ^ 1]);
+            }
+            umma_commit(&sh.s_ready[w]);
+            umma_commit(&sh.empty[k_]);
+            if (!two) umma_commit(&sh.empty[k_]);                // (counts both warps)
+            if (p + step >= pages) umma_commit(&sh.q_free[qb]);  // its last S
           }
           __syncwarp();
-          ++arms;
-          if (++at == kSlots) { at = 0; phase ^= 1u; }
+        };
+        auto wait = [&](uint64_t* bar, uint32_t par) {
+          mbar_wait(bar, par, ws.hdr);
+          __syncwarp();
+        };
+        auto k_bar = [&](int b) { return F::kRaw ? &sh.ready[b] : &sh.full[b]; };
+        int p = two ? 0 : odd;
+        const bool any = p < pages;
+        if (any) {                             // the first S of the segment, without a turn
+          if (p == 1) take(kb, kpar, vb, vpar);
+          take(kb, kpar, vb, vpar);
+          wait(k_bar(kb), kpar);
+          wait(&sh.q_full[qb], q_phase >> qb & 1u);
+          if (mine > 0) wait(&sh.o_done[w], (uint32_t)(mine - 1) & 1u);
+          issue_s(kb, p, false);
         }
-      }
-    }
-    // Normally the converters and the MMAs wait for every copy issued here.
-    // After a wait gave up they may not have: let the copies in flight land.
-    if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
-      for (int i = 0; i < kSlots && i < arms; ++i)
-        mbar_drain(F::kRaw ? &sh.raw_full[i] : &sh.full[i],
-                   (uint32_t)(((arms - 1 - i) / kSlots) & 1));
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMAs
-    // Item by item, S one ahead: S_{k+1} once P_{k-1} V has read the buffer it
-    // overwrites, then O += P_k V.
-    struct Cursor {                            // over (page, tile) items
-      Walk<KV> wk;
-      int j, t, k, kv;                         // k: item number; kv: pages before this one
-      int qsel, qb;                            // buffer of the segment's first Q tile
-      bool more, first;                        // first: page of the segment
-    };
-    uint32_t q_phase = 0;                      // bit b: uses of Q buffer b so far, odd or even
-    const uint32_t idesc_s = idesc_f16(F::kRaw ? 0 : 1, kTile, kBlock),
-                   idesc_o = idesc_f16_bmn(0, kTile, kHeadDim);
-    Cursor cs, cp;
-    auto enter = [&](Cursor& c) {              // a segment's first item
-      c.j = c.wk.j0;
-      c.t = 0;
-      c.first = true;
-      c.qb = c.wk.tiles == 2 ? 0 : c.qsel;
-      if (c.wk.tiles == 1) c.qsel ^= 1;
-    };
-    auto advance = [&](Cursor& c) {
-      ++c.k;
-      if (++c.t < c.wk.tiles) return;
-      c.t = 0;
-      ++c.kv;
-      c.first = false;
-      if (++c.j < c.wk.j1) return;
-      c.more = c.wk.next(ws, a);
-      if (c.more) enter(c);
-    };
-    cs.wk.open(ws, a, sh);
-    cs.k = cs.kv = cs.qsel = 0;
-    cs.more = cs.wk.next(ws, a);
-    if (cs.more) enter(cs);
-    cp = cs;
-    const uint64_t dq = kstep_desc(smem_u32(qbuf), 0, kTile), dk = kstep_desc(smem_u32(tiles), 0, 128),
-                   dv = sdesc_sw128_mn(smem_u32(tiles), kTileBytes / 2);
-    const uint32_t hi = (uint32_t)(dk >> 32), vhi = (uint32_t)(dv >> 32);
-    auto issue_s = [&]() {
-      Cursor& c = cs;
-      const int tile = 2 * c.kv, b = tile % F::kTiles, buf = c.k & 1, qb = (c.qb + c.t) & 1;
-      if (c.t == 0)
-        mbar_wait(F::kRaw ? &sh.ready[b] : &sh.full[b], (uint32_t)(tile / F::kTiles) & 1u, ws.hdr);
-      if (c.first) {
-        mbar_wait(&sh.q_full[qb], q_phase >> qb & 1u, ws.hdr);
-        q_phase ^= 1u << qb;
-      }
-      if (c.k >= 2) mbar_wait(&sh.o_done[buf], (uint32_t)((c.k - 2) >> 1) & 1u, ws.hdr);
-      __syncwarp();
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t qlo = (uint32_t)dq + qb * (kTileBytes >> 4),
-                       klo = (uint32_t)dk + b * (kTileBytes >> 4), d = tmem + buf * 128;
-        umma_ss<false>(d, qlo, hi, klo, hi, idesc_s);
+        int taken = any ? p + 1 : 0;           // pages whose tiles were taken from the ring
+        for (; p < pages; p += step) {
+          const bool next = p + step < pages;
+          if (next) {
+            if (!two) take(kb2, kpar2, vb2, vpar2);
+            take(kb2, kpar2, vb2, vpar2);
+            taken = p + step + 1;
+          }
+          wait(&sh.ready[vb], vpar);
+          wait(&sh.p_ready[w], (uint32_t)mine & 1u);
+          // keys that are not there yet are not waited for in one's turn
+          const bool here =
+              next && __shfl_sync(0xffffffffu, (int)mbar_test_wait(k_bar(kb2), kpar2), 0);
+          if (mine > 0 || w == 1)              // phase n of a turn: the other's n-th pass
+            wait(&sh.turn[w], (uint32_t)(w ? mine : mine - 1) & 1u);
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vd = v_lo + (tile_at<KV>(vb) >> 4);
+            if (p < step) umma_ts<false>(to, ts, vd, v_hi, idesc_o);   // O of the segment begins
+            else umma_ts<true>(to, ts, vd, v_hi, idesc_o);
 #pragma unroll
-        for (int ks = 1; ks < 8; ++ks) {
-          const uint32_t o = (ks >> 2) * (kTileBytes >> 5) + (ks & 3) * 2;
-          umma_ss<true>(d, qlo + o, hi, klo + o, hi, idesc_s);
+            for (int ks = 1; ks < 8; ++ks)
+              umma_ts<true>(to, ts + 8 * ks, vd + 128 * ks, v_hi, idesc_o);
+            umma_commit(&sh.o_done[w]);
+            umma_commit(&sh.empty[vb]);
+            if (!two) umma_commit(&sh.empty[vb]);
+          }
+          __syncwarp();
+          if (!here && elect_one()) mbar_arrive(&sh.turn[w ^ 1]);
+          __syncwarp();
+          if (next) {
+            if (!here) wait(k_bar(kb2), kpar2);
+            wait(&sh.o_done[w], (uint32_t)mine & 1u);
+            issue_s(kb2, p + step, here);
+            kb = kb2;
+            vb = vb2;
+            vpar = vpar2;
+          }
+          ++mine;
         }
-        umma_commit(&sh.s_ready[buf]);
-        if (c.t + 1 == c.wk.tiles) umma_commit(&sh.empty[b]);
-        if (c.j + 1 == c.wk.j1) umma_commit(&sh.q_free[qb]);
+        for (; taken < pages; ++taken) take(kb2, kpar2, vb2, vpar2);
+        // a Q buffer that this warp did not read: seen all the same, so that none of
+        // its phases passes this warp by
+        for (int b = 0; b < 2; ++b) {
+          if (!two && b != qb) continue;
+          if (!any || b != qb) {
+            wait(&sh.q_full[b], q_phase >> b & 1u);
+            if (elect_one()) mbar_arrive(&sh.q_free[b]);
+            __syncwarp();
+          }
+          q_phase ^= 1u << b;
+        }
+        k0 += pages * wk.tiles;
       }
+      // every MMA issued here has completed before TMEM goes and the smem is left
+      if (elect_one()) umma_commit(&sh.fin[w]);
       __syncwarp();
-      advance(c);
-    };
-    if (cs.more) issue_s();
-    while (cp.more) {
-      if (cs.more) issue_s();
-      const int tile = 2 * cp.kv + 1, b = tile % F::kTiles, buf = cp.k & 1;
-      if (cp.t == 0) {
-        // bf16: of an odd ring's uses every second one holds values
-        const int use = F::kRaw ? tile / F::kTiles : tile / (2 * F::kTiles);
-        mbar_wait(&sh.ready[b], (uint32_t)use & 1u, ws.hdr);
+      mbar_drain(&sh.fin[w], 0);
+    } else if (warp == F::kIdleWarp) {
+      // tokens of no request that has a tree
+      const int T = ws.hdr->num_tokens;
+      for (int t = blockIdx.x; t < T; t += gridDim.x) {
+        const int r = ws.tok_req[t];
+        if (r >= 0) {
+          const Tree tr = tree_of(ws, r);
+          if (tr.n > 0) continue;
+          if (tr.too_large && lane == 0) set_error(ws.hdr, MSA_DEVERR_TREE);
+        }
+        uint4* row = reinterpret_cast<uint4*>(a.out + (int64_t)t * a.Hq * kHeadDim);
+        for (int x = lane; x < a.Hq * (kHeadDim / 8); x += 32) row[x] = make_uint4(0, 0, 0, 0);
+        for (int x = lane; x < a.Hq; x += 32) a.lse[(int64_t)t * a.Hq + x] = -INFINITY;
       }
-      mbar_wait(&sh.p_ready[buf], (uint32_t)(cp.k >> 1) & 1u, ws.hdr);
-      __syncwarp();
-      tc_fence_after();
-      if (elect_one()) {
-        // P: keys 0..63 in columns 0..31 of the buffer, 64..127 in 64..95
-        const uint32_t p = tmem + buf * 128, d = tmem + 256 + cp.t * 128,
-                       vlo = (uint32_t)dv + b * (kTileBytes >> 4);
-        if (cp.first) umma_ts<false>(d, p, vlo, vhi, idesc_o);
-        else umma_ts<true>(d, p, vlo, vhi, idesc_o);
-#pragma unroll
-        for (int ks = 1; ks < 8; ++ks)
-          umma_ts<true>(d, p + (ks >> 2) * 64 + (ks & 3) * 8, vlo + 128 * ks, vhi, idesc_o);
-        umma_commit(&sh.o_done[buf]);
-        if (cp.t + 1 == cp.wk.tiles) umma_commit(&sh.empty[b]);
-      }
-      __syncwarp();
-      advance(cp);
     }
-    // every MMA issued here has completed before TMEM goes and the smem is left
-    if (elect_one()) umma_commit(&sh.fin);
-    __syncwarp();
-    mbar_drain(&sh.fin, 0);
-  } else if (warp == kIdleWarp) {
-    // tokens of no request that has a tree
-    const int T = ws.hdr->num_tokens;
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
-      const int r = ws.tok_req[t];
-      if (r >= 0) {
-        const Tree tr = tree_of(ws, r);
-        if (tr.n > 0) continue;
-        if (tr.too_large && lane == 0) set_error(ws.hdr, MSA_DEVERR_TREE);
-      }
-      for (int x = lane; x < a.Hq * (kHeadDim / 8); x += 32)
-        reinterpret_cast<uint4*>(a.out + (int64_t)t * a.Hq * kHeadDim)[x] = make_uint4(0, 0, 0, 0);
-      for (int x = lane; x < a.Hq; x += 32) a.lse[(int64_t)t * a.Hq + x] = -INFINITY;
-    }
-  }
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------------------ converters
-    regs_down<kConvRegs>();
+    regs_down<F::kConvRegs>();
     const int ct = tid - kConvWarp * 32;
     Walk<KV> wk;
     wk.open(ws, a, sh);
-    int n = 0, seg = 0, qsel = 0;
+    Ring<KV> ring;
+    int seg = 0, qsel = 0, st = 0;
+    uint32_t st_phase = 0;
     uint32_t q_used = 0, q_phase = 0;          // bit b: Q buffer b was used; its uses, odd or even
+    bool extra_used = false;                   // the second Q buffer held a tile of the ring
     auto done = [&](uint64_t* bar) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    while (wk.next(ws, a)) {
-      // ---- Q rows of the segment's tiles, zero past the last
-      for (int t = 0; t < wk.tiles; ++t) {
-        const int b = wk.tiles == 2 ? t : qsel;
-        if (q_used >> b & 1u) mbar_wait(&sh.q_free[b], (q_phase >> b & 1u) ^ 1u, ws.hdr);
-        q_used |= 1u << b;
-        q_phase ^= 1u << b;
-        bool ovf = false;
-        const int first = wk.pair * kPairRows + t * kTile, rows = wk.rows - t * kTile;
-#pragma unroll 8
-        for (int i = 0; i < 16; ++i) {
-          const int x = ct + 128 * i, row = x >> 4, ch = x & 15;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (row < rows)
-            v = *reinterpret_cast<const uint4*>(
-                a.q + a.q_row(wk.q.t0, wk.h, first + row) * kHeadDim + 8 * ch);
-          if (F::kRaw) {
-            uint32_t h[4];
-            to_f16(v, h);
-            ovf |= any_inf(h);
-            v = make_uint4(h[0], h[1], h[2], h[3]);
-          }
-          *reinterpret_cast<uint4*>(qbuf + b * kTileBytes + kmaj_off(row, ch, kTile)) = v;
+    // Q rows of tile t of the segment into buffer b, zero past the last
+    auto load_q = [&](int t, int b) {
+      if (q_used >> b & 1u) mbar_wait(&sh.q_free[b], (q_phase >> b & 1u) ^ 1u, ws.hdr);
+      if (F::kRaw && b == 1 && extra_used)
+        mbar_wait(&sh.empty[F::kTiles], (ring.uses >> F::kTiles & 1u) ^ 1u, ws.hdr);
+      q_used |= 1u << b;
+      q_phase ^= 1u << b;
+      bool ovf = false;
+      const int first = wk.pair * kPairRows + t * kTile, rows = wk.rows - t * kTile;
+#pragma unroll (F::kRaw ? 4 : 8)
+      for (int i = 0; i < kTile * 16 / F::kConvThreads; ++i) {
+        const int x = ct + F::kConvThreads * i, row = x >> 4, ch = x & 15;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows)
+          v = *reinterpret_cast<const uint4*>(
+              a.q + a.q_row(wk.q.t0, wk.h, first + row) * kHeadDim + 8 * ch);
+        if (F::kRaw) {
+          uint32_t h[4];
+          to_f16(v, h);
+          ovf |= any_inf(h);
+          v = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        if (F::kRaw && __any_sync(0xffffffffu, ovf) && lane == 0)
-          set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
-        done(&sh.q_full[b]);
+        *reinterpret_cast<uint4*>(qbuf + b * kTileBytes + kmaj_off(row, ch, kTile)) = v;
       }
+      if (F::kRaw && __any_sync(0xffffffffu, ovf) && lane == 0)
+        set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
+      done(&sh.q_full[b]);
+    };
+    while (wk.next(ws, a)) {
+      if (ct == 0) sh.bad[(seg + kBads / 2) & (kBads - 1)] = 0;
+      load_q(0, F::kRaw || wk.tiles == 2 ? 0 : qsel);
+      if (!F::kRaw && wk.tiles == 2) load_q(1, 1);
       if (wk.tiles == 1) qsel ^= 1;
       // ---- pages
+      unsigned long long* bad = &sh.bad[seg & (kBads - 1)];
       int mine = -1;
       bool ovf = false;
-      for (int j = wk.j0; j < wk.j1; ++j, n += 2) {
+      for (int j = wk.j0; j < wk.j1; ++j) {
         const int k = (j - wk.j0) & 31;
         if (k == 0)
           mine = j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + j + lane] : -1;
@@ -678,24 +816,37 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
         const int all = usable ? wk.q.base - j * kBlock : 0;     // and that every row sees
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
-          const int i = n + kind, b = i % F::kTiles;
-          uint8_t* tile = tiles + b * kTileBytes;
-          if (F::kRaw) {
-            const int st = i % F::kStages;
-            mbar_wait(&sh.raw_full[st], (uint32_t)(i / F::kStages) & 1u, ws.hdr);
-            mbar_wait(&sh.empty[b], ((uint32_t)(i / F::kTiles) & 1u) ^ 1u, ws.hdr);
-            if (kind == 0)
-              convert_page<KV, false>(raw + st * F::kStageBytes, tile, ct, ntok, all, nullptr);
-            else
-              convert_page<KV, true>(raw + st * F::kStageBytes, tile, ct, ntok, all,
-                                     &sh.bad[seg & 7]);
+          uint32_t par;
+          if constexpr (F::kRaw) {
+            const int b = ring.take(wk.tiles, kind, par);
+            uint8_t* tile = smem + tile_at<KV>(b);
+            const uint8_t* src = raw + st * F::kStageBytes;
+            mbar_wait(&sh.empty[b], par ^ 1u, ws.hdr);
+            if (b == F::kTiles) {              // the second Q buffer: its last S is done
+              extra_used = true;
+              if (q_used & 2u) mbar_wait(&sh.q_free[1], (q_phase >> 1 & 1u) ^ 1u, ws.hdr);
+            }
+            mbar_wait(&sh.raw_full[st], st_phase, ws.hdr);
+            if (kind == 0) convert_page<KV, false>(src, tile, ct, ntok, all, nullptr);
+            else convert_page<KV, true>(src, tile, ct, ntok, all, bad);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.raw_empty[st]);
+            if (++st == F::kStages) { st = 0; st_phase ^= 1u; }
             done(&sh.ready[b]);
-          } else if (kind == 1) {
-            mbar_wait(&sh.full[b], (uint32_t)(i / F::kTiles) & 1u, ws.hdr);
-            ovf |= convert_page<KV, true>(nullptr, tile, ct, ntok, all, &sh.bad[seg & 7]);
-            done(&sh.ready[b]);
+            // the second tile's Q comes after the first K: the last V of a segment of
+            // one tile may still be where it goes
+            if (kind == 0 && j == wk.j0 && wk.tiles == 2) load_q(1, 1);
+          } else {
+            const int b = ring.take(wk.tiles, kind, par);
+            // keys are waited for as well: a copy may land after a later one, and a
+            // wait is only for the phase after one that was seen
+            mbar_wait(&sh.full[b], par, ws.hdr);
+            if (kind == 1) {
+              ovf |= convert_page<KV, true>(nullptr, smem + tile_at<KV>(b), ct, ntok, all, bad);
+              done(&sh.ready[b]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty[b]);
           }
         }
       }
@@ -704,104 +855,51 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    regs_up<kSoftRegs>();
-    // Control flow depends on the plan's data and on votes of all eight warps
-    // alone (never on what a wait saw): the named barriers match even after a
-    // wait gave up.
+    // Control flow depends on the plan's data alone (never on what a wait saw),
+    // so that the named barriers match even after a wait gave up.
+    regs_up<F::kSoftRegs>();
     constexpr int kBar = 1, kCount = kSoftWarps * 32;
+    constexpr int kC = F::kRaw ? 16 : 32;      // columns at a time, by the registers there are
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t ts = lanes + wg * 128, to = lanes + 256 + wg * 128;
     Walk<KV> wk;
     wk.open(ws, a, sh);
-    int k = 0, seg = 0;
+    int k0 = 0, seg = 0;                       // first item of the segment
     int4 split = make_int4(0, 0, 0, 0);
     while (wk.next(ws, a)) {
-      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-      uint64_t mk[2];                          // the two rows' masks
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int n = wk.pair * kPairRows + t * kTile + row;
-        mk[t] = 0;
-        if (n < wk.q.rows) {
-          const int i = a.node_of(n);
-          mk[t] = a.mask ? (uint64_t)a.mask[wk.q.t0 + i] : ~0ull >> (63 - i);
-          if (wk.q.n < 64) mk[t] &= (1ull << wk.q.n) - 1;
-        }
+      const bool two = wk.tiles == 2;
+      const int pages = wk.j1 - wk.j0, odd = (wg ^ k0) & 1;
+      const int t = two ? odd : 0;             // this warpgroup's tile
+      float m = -INFINITY, l = 0.f;
+      uint64_t mask = 0;                       // what the row sees of the nodes
+      const int n = t * kTile + row;           // row of the pair
+      const bool on = n < wk.rows;
+      if (on) {
+        const int i = a.node_of(wk.pair * kPairRows + n);
+        mask = a.mask ? (uint64_t)a.mask[wk.q.t0 + i] : ~0ull >> (63 - i);
+        if (wk.q.n < 64) mask &= (1ull << wk.q.n) - 1;
       }
-      int mine = -1;
-      for (int j = wk.j0; j < wk.j1; ++j) {
-        const int at = (j - wk.j0) & 31;
-        if (at == 0)
-          mine = j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + j + lane] : -1;
-        const bool usable = __shfl_sync(0xffffffffu, mine, at) >= 0;
-        // keys before the nodes, from this thread's first column on
-        const int d = wk.q.base - j * kBlock - 64 * wg;
-        const bool plain = usable && wk.q.base >= (j + 1) * kBlock;
-#pragma unroll 1
-        for (int t = 0; t < wk.tiles; ++t, ++k) {
-          const int buf = k & 1;
-          const uint32_t ts = lanes + buf * 128 + 64 * wg;
-          mbar_wait(&sh.s_ready[buf], (uint32_t)(k >> 1) & 1u, ws.hdr);
-          tc_fence_after();
-          uint32_t x[64];
-          tmem_ld64(ts, x);
-          tmem_ld_wait();
-          if (!plain) {
-            const uint64_t mask = t ? mk[1] : mk[0];
-            uint64_t vis;
-            if (!usable) vis = 0;
-            else if (d >= 64) vis = ~0ull;
-            else if (d > 0) vis = ((1ull << d) - 1) | (mask << d);
-            else vis = d > -64 ? mask >> -d : 0;
+      int mine = -1, have = -1;
+      bool first = true, fast = false;         // first: page of this warpgroup's
+      for (int p = two ? 0 : odd; p < pages; p += two ? 1 : 2) {
+        const int k = two ? k0 + 2 * p + t : k0 + p, j = wk.j0 + p;
+        if (p >> 5 != have) {
+          have = p >> 5;
+          const int jj = wk.j0 + 32 * have + lane;
+          mine = jj < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + jj] : -1;
+        }
+        const bool usable = __shfl_sync(0xffffffffu, mine, p & 31) >= 0;
+        const int d = wk.q.base - j * kBlock;  // keys before the nodes
+        mbar_wait(&sh.s_ready[wg], (uint32_t)(k >> 1) & 1u, ws.hdr);
+        tc_fence_after();
+        const bool plain = usable && d >= kBlock;
+        const uint64_t sl = f2(a.scale_log2, a.scale_log2), bias = f2(kBias, kBias);
+        uint64_t sum0 = 0, sum1 = 0;
+        // P = 2^((s - m) scale + bias) of kC columns, as fp16 pairs from pk[0] on
+        auto prob = [&](const uint32_t (&x)[kC], uint64_t rf, uint32_t* pk) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (!(vis >> i & 1)) x[i] = 0xff800000u;
-          }
-          float m = t ? m1 : m0, l = t ? l1 : l0;
-          float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-          float my = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
-#pragma unroll
-          for (int i = 4; i < 64; i += 4) {
-            mx = fmax3(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            my = fmax3(my, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-          }
-          mx = fmaxf(mx, my);
-          // the difference, exact near m; -inf - -inf is NaN: no move
-          if (named_bar_any(kBar, kCount, mx - m > a.slack)) {
-            sh.red[wg][row] = mx;
-            named_bar_sync(kBar, kCount);
-            const float mn = fmax3(m, sh.red[0][row], sh.red[1][row]);
-            const float alpha = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * a.scale_log2);
-            m = mn;
-            l *= alpha;
-            if (j > wk.j0) {
-              // O of this tile: its last P V has to be done
-              const int kp = k - wk.tiles;
-              mbar_wait(&sh.o_done[kp & 1], (uint32_t)(kp >> 1) & 1u, ws.hdr);
-              tc_fence_after();
-              if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                for (int c = 0; c < 64; c += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(lanes + 256 + t * 128 + 64 * wg + c, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                  tmem_st32(lanes + 256 + t * 128 + 64 * wg + c, o);
-                }
-                tmem_st_wait();
-              }
-            }
-          }
-          // P = 2^((s - m) scale + bias), over this half of S
-          const float ref = m == -INFINITY ? 0.f : -m;
-          const uint64_t sl = f2(a.scale_log2, a.scale_log2), bias = f2(kBias, kBias),
-                         rf = f2(ref, ref);
-          uint64_t sum0 = 0, sum1 = 0;
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < kC / 2; i += 2) {
             float p0, p1, p2, p3;
             f2_split(fma_f2(add_f2(f2u(x[2 * i], x[2 * i + 1]), rf), sl, bias), p0, p1);
             f2_split(fma_f2(add_f2(f2u(x[2 * i + 2], x[2 * i + 3]), rf), sl, bias), p2, p3);
@@ -814,99 +912,229 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
             pk[i] = pack_f16(p0, p1);
             pk[i + 1] = pack_f16(p2, p3);
           }
-          tmem_st32(ts, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_ready[buf]);
+        };
+        float mx[2];
+        auto most = [&](const uint32_t (&x)[kC]) {
+#pragma unroll
+          for (int i = 0; i < kC; i += 4) {
+            mx[0] = fmax3(mx[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            mx[1] = fmax3(mx[1], __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          }
+        };
+        uint32_t pk[64];
+        bool good = false;
+        if (plain && fast) {
+          // One pass, with m as it is and -m scale + bias rounded to fp32 (fast: off
+          // by less than 2^-18): P stays in registers until its sum says that no
+          // probability is beyond fp16.
+          const float c0 = fmaf(-m, a.scale_log2, kBias);
+          const uint64_t cc = f2(c0, c0);
+          auto prob1 = [&](const uint32_t (&x)[kC], uint32_t* y) {
+#pragma unroll
+            for (int i = 0; i < kC / 2; i += 2) {
+              float p0, p1, p2, p3;
+              f2_split(fma_f2(f2u(x[2 * i], x[2 * i + 1]), sl, cc), p0, p1);
+              f2_split(fma_f2(f2u(x[2 * i + 2], x[2 * i + 3]), sl, cc), p2, p3);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              p2 = ex2_approx(p2);
+              p3 = ex2_approx(p3);
+              sum0 = add_f2(sum0, f2(p0, p1));
+              sum1 = add_f2(sum1, f2(p2, p3));
+              y[i] = pack_f16(p0, p1);
+              y[i + 1] = pack_f16(p2, p3);
+            }
+          };
+          uint32_t xa[kC], xb[kC];
+          ld_scores(ts, xa);
+#pragma unroll
+          for (int c = 0; c < kBlock; c += 2 * kC) {
+            wait_scores(xa);
+            ld_scores(ts + c + kC, xb);
+            prob1(xa, pk + c / 2);
+            wait_scores(xb);
+            if (c + 2 * kC < kBlock) ld_scores(ts + c + 2 * kC, xa);
+            prob1(xb, pk + (c + kC) / 2);
+          }
           float s0, s1;
           f2_split(add_f2(sum0, sum1), s0, s1);
-          l += s0 + s1;
-          if (t) {
-            m1 = m;
-            l1 = l;
-          } else {
-            m0 = m;
-            l0 = l;
+          good = __all_sync(0xffffffffu, s0 + s1 < kMaxSum);
+        }
+        if (!good) {
+          // Two passes: the row's maximum over what it sees, then P.
+          auto see = [&](uint32_t (&x)[kC], int c) {             // columns c ..
+            if (plain) return;
+            const int e = d - c;
+            uint32_t vis;
+            if (!usable) vis = 0;
+            else if (e >= 32) vis = ~0u;
+            else if (e > 0) vis = ((1u << e) - 1) | (uint32_t)(mask << e);
+            else vis = e > -64 ? (uint32_t)(mask >> -e) : 0;
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+              if (!(vis >> i & 1)) x[i] = 0xff800000u;
+          };
+          uint32_t x[kC];
+          mx[0] = mx[1] = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kBlock; c += kC) {
+            ld_scores(ts + c, x);
+            wait_scores(x);
+            see(x, c);
+            most(x);
+          }
+          const float top = fmaxf(mx[0], mx[1]);
+          if (__any_sync(0xffffffffu, top > m)) {
+            const float mn = fmaxf(m, top);
+            const float alpha = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * a.scale_log2);
+            m = mn;
+            l *= alpha;
+            if (!first) {                      // (S was issued after the last P V of this O)
+#pragma unroll 1
+              for (int c = 0; c < kHeadDim; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(to + c, o);
+                tmem_wait32(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st32(to + c, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : -m;
+          const uint64_t rf = f2(ref, ref);
+          sum0 = sum1 = 0;
+#pragma unroll
+          for (int c = 0; c < kBlock; c += kC) {
+            ld_scores(ts + c, x);
+            wait_scores(x);
+            see(x, c);
+            prob(x, rf, pk + c / 2);
           }
         }
+        tmem_st64(ts, pk);                     // over S
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[wg]);
+        float s0, s1;
+        f2_split(add_f2(sum0, sum1), s0, s1);
+        l += s0 + s1;
+        first = false;
+        fast = __all_sync(0xffffffffu, fabsf(m) * a.scale_log2 < kNear);
       }
 
       // ---- the segment's result: whole rows, or a partial
       const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.starts ? 1 : 0);
-#pragma unroll 1
-      for (int t = 0; t < wk.tiles; ++t) {
-        const int kp = k - wk.tiles + t;
-        mbar_wait(&sh.o_done[kp & 1], (uint32_t)(kp >> 1) & 1u, ws.hdr);
+      const int items = pages * wk.tiles, kl = k0 + items - 1;   // the last item, and the one
+                                                                 // before it in the other slot
+      float* part = a.o_part + (slot * a.rows + n) * kHeadDim;
+      const int64_t out_row = on ? a.q_row(wk.q.t0, wk.h, wk.pair * kPairRows + n) : 0;
+      // 32 dims of the row from dim on
+      auto put = [&](const uint32_t (&o)[32], int dim, float inv) {
+        if (!on) return;
+        if (wk.whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * kHeadDim + dim);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              h[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                               __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            reinterpret_cast<uint4*>(part + dim)[i] =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      };
+      int dim0 = 0, dims = kHeadDim;           // this thread's part of the row
+      if (two) {
+        const int mine_l = kl & 1 ? (wg ? kl : kl - 1) : (wg ? kl - 1 : kl);
+        mbar_wait(&sh.o_done[wg], (uint32_t)(mine_l >> 1) & 1u, ws.hdr);
         tc_fence_after();
-        const float m = t ? m1 : m0;
-        named_bar_sync(kBar, kCount);
-        sh.red[wg][row] = t ? l1 : l0;
-        named_bar_sync(kBar, kCount);
-        const float sum = sh.red[0][row] + sh.red[1][row];
-        const unsigned long long bad = sh.bad[seg & 7] & (t ? mk[1] : mk[0]);
-        const int n = t * kTile + row;         // row of the pair
-        const bool on = n < wk.rows;
-        const int64_t out_row = on ? a.q_row(wk.q.t0, wk.h, wk.pair * kPairRows + n) : 0;
-        const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+        const float inv = l == 0.f ? 0.f : a.v_scale / l;
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          const int dim = 64 * wg + c;
+        for (int c = 0; c < kHeadDim; c += 32) {
           uint32_t o[32];
-          tmem_ld32(lanes + 256 + t * 128 + dim, o);
-          tmem_ld_wait();
-          if (!on) continue;
-          float* part = a.o_part + (slot * a.rows + n) * kHeadDim + dim;
+          tmem_ld32(to + c, o);
+          tmem_wait32(o);
+          put(o, c, inv);
+        }
+      } else {
+        // one tile: both warpgroups' results of a row, half its dims each
+        sh.ml[wg][row] = make_float2(m, l);
+        named_bar_sync(kBar, kCount);
+        const bool both = pages > 1;
+        const int wl = kl & 1;                 // the warpgroup of the last item
+        mbar_wait(&sh.o_done[wl], (uint32_t)(kl >> 1) & 1u, ws.hdr);
+        if (both) mbar_wait(&sh.o_done[wl ^ 1], (uint32_t)((kl - 1) >> 1) & 1u, ws.hdr);
+        tc_fence_after();
+        const float2 ml = sh.ml[wl][row], mo = sh.ml[wl ^ 1][row];
+        m = ml.x;
+        l = ml.y;
+        float fl = 1.f, fo = 0.f;
+        if (both) {
+          m = fmaxf(ml.x, mo.x);
+          if (m != -INFINITY) {
+            fl = ex2_approx((ml.x - m) * a.scale_log2);
+            fo = ex2_approx((mo.x - m) * a.scale_log2);
+          }
+          l = ml.y * fl + mo.y * fo;
+        }
+        const float inv = l == 0.f ? 0.f : a.v_scale / l;
+        dim0 = 64 * wg;
+        dims = 64;
+#pragma unroll 1
+        for (int c = dim0; c < dim0 + 64; c += 32) {
+          uint32_t o[32], q[32];
+          tmem_ld32(lanes + 256 + wl * 128 + c, o);
+          if (both) tmem_ld32(lanes + 256 + (wl ^ 1) * 128 + c, q);
+          tmem_wait32(o);
+          if (both) {
+            tmem_wait32(q);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * fl + __uint_as_float(q[i]) * fo);
+          }
+          if (c == dim0 + 32) {                // O and ml may be overwritten from here on
+            tc_fence_before();
+            named_bar_sync(kBar, kCount);
+          }
+          put(o, c, inv);
+        }
+      }
+      if (on && (two || wg == 0)) {
+        if (wk.whole)
+          a.lse[out_row] = l == 0.f ? -INFINITY : (m * a.scale_log2 + log2f(l) - kBias) * kLn2;
+        else
+          a.ml_part[slot * a.rows + n] = make_float2(m, l);
+      }
+      // rare: values that are not finite, of nodes that the row sees
+      for (unsigned long long b = on ? sh.bad[seg & (kBads - 1)] & mask : 0; b; b &= b - 1) {
+        const int u = wk.q.base + __ffsll((long long)b) - 1;
+        const int page = ws.block_table[(int64_t)wk.r * a.max_blocks + u / kBlock];
+        for (int dim = dim0; dim < dim0 + dims; ++dim) {
+          const float v = value_of<KV>(a.v_pool, page, a.Hkv, wk.h, u % kBlock, dim);
+          if (fabsf(v) < INFINITY) continue;
           if (wk.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * kHeadDim + dim);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                h[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                 __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-              dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
-            }
+            __nv_bfloat16* y = a.out + out_row * kHeadDim + dim;
+            *y = __float2bfloat16_rn(__bfloat162float(*y) + v);
           } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(part)[i] =
-                  make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            part[dim] += v;
           }
-        }
-        // rare: values that are not finite, of nodes that the row sees
-        for (unsigned long long b = on ? bad : 0; b; b &= b - 1) {
-          const int u = wk.q.base + __ffsll((long long)b) - 1;
-          const int page = ws.block_table[(int64_t)wk.r * a.max_blocks + u / kBlock];
-          for (int dim = 64 * wg; dim < 64 * wg + 64; ++dim) {
-            const float v = value_of<KV>(a.v_pool, page, a.Hkv, wk.h, u % kBlock, dim);
-            if (fabsf(v) < INFINITY) continue;
-            if (wk.whole) {
-              __nv_bfloat16* y = a.out + out_row * kHeadDim + dim;
-              *y = __float2bfloat16_rn(__bfloat162float(*y) + v);
-            } else {
-              a.o_part[(slot * a.rows + n) * kHeadDim + dim] += v;
-            }
-          }
-        }
-        if (on && wg == 0) {
-          if (wk.whole)
-            a.lse[out_row] =
-                sum == 0.f ? -INFINITY : (m * a.scale_log2 + log2f(sum) - kBias) * kLn2;
-          else
-            a.ml_part[slot * a.rows + n] = make_float2(m, sum);
         }
       }
       tc_fence_before();
-      named_bar_sync(kBar, kCount);            // bad is read, red is free
-      if (tid == 0) {
-        sh.bad[seg & 7] = 0;
-        if (wk.starts && !wk.whole) {          // the range ends inside this group
-          const int c1 = (int)range_of(sh.total, sh.ranges, wk.last);
-          split = make_int4(c1 - (int)blockIdx.x + 1, wk.q.t0, wk.h, wk.pair << 16 | wk.rows);
-        }
+      if (wk.starts && !wk.whole) {            // the range ends inside this group
+        const int c1 = (int)range_of(sh.total, sh.ranges, wk.last);
+        split = make_int4(c1 - (int)blockIdx.x + 1, wk.q.t0, wk.h, wk.pair << 16 | wk.rows);
       }
+      k0 += items;
       ++seg;
     }
     if (tid == 0) a.split[blockIdx.x] = split;
@@ -1016,7 +1244,7 @@ msa_status launch_tree(const WsView& v, const TreeArgs& a, int64_t pool_rows, in
   if (grid <= 0) return MSA_ERR_CUDA;
   if (grid > kMaxCtas) grid = kMaxCtas;
   if (grid > units) grid = units;
-  msa_status st = launch_pdl(tree_attention_kernel<KV>, dim3((unsigned)grid), dim3(kThreads),
+  msa_status st = launch_pdl(tree_attention_kernel<KV>, dim3((unsigned)grid), dim3(F::kThreads),
                              F::kSmem, s, v, a, tk, tv);
   if (st != MSA_OK) return st;
   int64_t blocks = grid * ((a.rows + kMergeWarps - 1) / kMergeWarps);
@@ -1067,7 +1295,6 @@ extern "C" msa_status msa_tree_attention(const msa_config* cfg, void* ws, const 
   if (!(a.scale_log2 > 0.f && a.scale_log2 < INFINITY)) return MSA_ERR_INVALID_ARG;
   const int64_t T = max_tokens_of(*cfg);
   if (T <= 0 || cfg->max_batch == 0) return MSA_OK;
-  a.slack = fminf(kSlack / a.scale_log2, FLT_MAX);
   a.v_scale = bf16 ? 1.f : cfg->v_scale;
   a.Hkv = cfg->num_kv_heads;
   a.Hq = cfg->num_q_heads;
