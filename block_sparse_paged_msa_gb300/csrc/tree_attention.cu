@@ -35,6 +35,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "kv_quant.cuh"
 #include "tcgen05.cuh"
 #include "tree.cuh"
 
@@ -49,11 +50,12 @@ constexpr float kBias = 7.f;                   // exponent offset of the probabi
 constexpr float kMaxSum = 60000.f;             // a row's sum over a page that fp16 holds
 constexpr float kNear = 64.f;                  // |m| of the fast path, in exponents
 
-constexpr int kSoftWarps = 8, kConvWarp = kSoftWarps;
+constexpr int kSoftWarps = 8, kConvWarp = kSoftWarps, kConvThreads = 128;   // of a group
 constexpr int kBads = 16;
 
 struct TreeArgs {
   int Hkv, Hq, G, max_blocks, rows;            // rows: of a partial
+  bool out32;                                  // out is 32-byte aligned
   uint32_t g_magic;                            // row / G = row * g_magic >> 20
   float scale_log2, v_scale;
   const __nv_bfloat16* q;
@@ -61,7 +63,8 @@ struct TreeArgs {
   const int64_t* mask;
   __nv_bfloat16* out;
   float* lse;
-  float* o_part;                               // [2 * CTAs][rows][128]
+  float* o_part;                               // [2 * CTAs][32][rows][4]: 4 dims of all rows side
+                                               // by side, as the threads of a tile have them
   float2* ml_part;                             // [2 * CTAs][rows] (m, sum)
   int4* split;                                 // [CTAs] the split group that starts in the CTA's
                                                // range: (partials, first token, head, pair << 16
@@ -75,38 +78,50 @@ struct TreeArgs {
   }
 };
 
-// KV types: tiles of the operand ring, raw stages in front of the converters.  bf16
-// tiles arrive in the ring itself.  With raw stages, a segment of one tile uses the
-// second Q buffer as a fourth tile of the ring.
+// KV types.  Keys and values have rings of operand tiles of their own, a page's
+// tile after the other's:
+//   bf16   both arrive in their rings; values are converted to fp16 in place;
+//   e4m3   keys arrive in their ring (the scores are e4m3 products); values arrive
+//          in raw stages and are converted into theirs;
+//   NVFP4  both go through raw stages.
 template <int KV>
 struct Form {
-  static constexpr bool kRaw = KV != MSA_KV_BF16;
-  static constexpr int kTiles = kRaw ? 3 : 5;
-  static constexpr int kBufs = kRaw ? kTiles + 1 : kTiles;
-  static constexpr int kStages = KV == MSA_KV_FP8_E4M3 ? 4 : (KV == MSA_KV_NVFP4 ? 7 : 1);
-  static constexpr int kStageBytes =
-      KV == MSA_KV_FP8_E4M3 ? kBlock * kHeadDim : (KV == MSA_KV_NVFP4 ? kBlock * kFp4Row : 0);
-  static constexpr int kSmem = (2 + kTiles) * kTileBytes + (kRaw ? kStages * kStageBytes : 0);
-  // Warps: softmax, converters, loader, two for the MMAs, one for idle tokens.
-  static constexpr int kConvWarps = kRaw ? 8 : 4, kLoadWarp = kConvWarp + kConvWarps,
+  static constexpr bool kBf16 = KV == MSA_KV_BF16, kE4m3 = KV == MSA_KV_FP8_E4M3,
+                        kFp4 = KV == MSA_KV_NVFP4;
+  static constexpr int kKeys = kE4m3 ? 3 : 2, kVals = kBf16 ? 3 : 2;           // tiles
+  static constexpr int kKeyBytes = kE4m3 ? kTileBytes / 2 : kTileBytes;
+  static constexpr int kRawKeys = kFp4 ? 1 : 0, kRawVals = kBf16 ? 0 : (kE4m3 ? 3 : 2);
+  static constexpr int kRawBytes = kE4m3 ? kBlock * kHeadDim : kBlock * kFp4Row;
+  // shared memory: two Q tiles, keys, values, raw stages
+  static constexpr int kKeyAt = 2 * kTileBytes, kValAt = kKeyAt + kKeys * kKeyBytes,
+                       kRawAt = kValAt + kVals * kTileBytes,
+                       kSmem = kRawAt + (kRawKeys + kRawVals) * kRawBytes;
+  // Warps: softmax, converters (four for the values; four for the keys where those
+  // are converted too), loader, two for the MMAs, one for idle tokens.
+  static constexpr int kConvWarps = kFp4 ? 8 : 4, kLoadWarp = kConvWarp + kConvWarps,
                        kMmaWarp = kLoadWarp + 1, kIdleWarp = kMmaWarp + 2,
-                       kThreads = 32 * (kIdleWarp + 1), kConvThreads = 32 * kConvWarps;
+                       kThreads = 32 * (kIdleWarp + 1);
   // threads x launch registers: 512 x 128 = 256 x 176 + 128 x 96 + 128 x 64;
   // 640 x 96 >= 256 x 152 + 256 x 56 + 128 x 56
-  static constexpr int kSoftRegs = kRaw ? 152 : 176, kConvRegs = kRaw ? 56 : 96,
-                       kMiscRegs = kRaw ? 56 : 64;
+  static constexpr int kSoftRegs = kFp4 ? 152 : 176, kConvRegs = kFp4 ? 56 : 96,
+                       kMiscRegs = kFp4 ? 56 : 64;
   // weight of a page for a pair of two tiles and of one
   static constexpr int kW2 = 1, kW1 = 1;
 };
+
+constexpr int at_least(int n) { return n < 1 ? 1 : n; }
 
 // What the roles share.
 template <int KV>
 struct Shared {
   using F = Form<KV>;
-  uint64_t raw_full[F::kStages], raw_empty[F::kStages];
-  uint64_t full[F::kBufs], ready[F::kBufs], empty[F::kBufs];
+  // full: arrived; ready: converted; empty: read by the MMAs
+  uint64_t k_full[F::kKeys], k_ready[F::kKeys], k_empty[F::kKeys];
+  uint64_t v_full[F::kVals], v_ready[F::kVals], v_empty[F::kVals];
+  uint64_t kr_full[at_least(F::kRawKeys)], kr_empty[at_least(F::kRawKeys)];
+  uint64_t vr_full[at_least(F::kRawVals)], vr_empty[at_least(F::kRawVals)];
   uint64_t q_full[2], q_free[2];
-  uint64_t s_ready[2], p_ready[2], o_done[2], turn[2], fin[2];
+  uint64_t s_ready[2], p_ready[2], o_done[2], turn[2], mid[2], fin[2];
   unsigned long long bad[kBads];               // by segment: nodes with values that are not finite
   float2 ml[2][kTile];                         // by warpgroup: (m, sum) of a row
   uint32_t tmem_base;
@@ -116,33 +131,18 @@ struct Shared {
   uint32_t part[F::kThreads / 32];
 };
 
-// The ring of operand tiles as a role goes through it: the next buffer, and for each
-// whether its uses so far are odd or even (bit b), its uses for values alike.
-template <int KV>
-struct Ring {
-  int pos = 0;
-  uint32_t uses = 0, v_uses = 0;
-  // the next tile's buffer; `tiles`: of the segment.  par: parity of this use
-  __device__ __forceinline__ int take(int tiles, bool values, uint32_t& par, uint32_t& v_par) {
-    const int n = Form<KV>::kRaw && tiles == 1 ? Form<KV>::kBufs : Form<KV>::kTiles;
-    const int b = pos < n ? pos : 0;
-    pos = b + 1;
-    par = uses >> b & 1u;
-    v_par = v_uses >> b & 1u;
-    uses ^= 1u << b;
-    if (values) v_uses ^= 1u << b;
-    return b;
-  }
-  __device__ __forceinline__ int take(int tiles, bool values, uint32_t& par) {
-    uint32_t v;
-    return take(tiles, values, par, v);
+// A place in a ring of N: the buffer, and the parity of its use.
+template <int N>
+struct Place {
+  int b = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void next() {
+    if (++b == N) {
+      b = 0;
+      par ^= 1u;
+    }
   }
 };
-// Byte offset of buffer b from the first Q tile.
-template <int KV>
-__device__ __forceinline__ uint32_t tile_at(int b) {
-  return (uint32_t)(Form<KV>::kRaw && b == Form<KV>::kTiles ? 1 : 2 + b) * kTileBytes;
-}
 
 // Weights.  A request: heads x pairs of tiles x pages.
 struct Req {
@@ -240,7 +240,15 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Lane i of the warp's quarter, 64 columns.
+// Lane i of the warp's quarter, 16 and 64 columns.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&r)[64]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {"
@@ -262,16 +270,6 @@ __device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&r)[64
       "r"(r[62]), "r"(r[63])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
 // Waits for this thread's TMEM loads; the registers pass through it, so that no use
 // of them moves before it.
 __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
@@ -286,19 +284,80 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-        "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-        "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-      :
+// 32 bytes of a row: a whole sector in one store where the address allows it (a
+// thread has a row of its own, and half sectors cost as much as whole ones).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&h)[8], bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(h[0]), "r"(h[1]),
+                 "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
+
+// ---------------------------------------------------------------- e4m3 scores
+// D[tmem] (+)= A[smem] * B[smem]^T of e4m3 operands, one K step of 32.
+template <bool kAcc>
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint32_t alo, uint32_t ahi,
+                                          uint32_t blo, uint32_t bhi, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .b64 a, b;\n .reg .pred p;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n}" ::"r"(d_tmem),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "n"(kAcc ? 1 : 0)
       : "memory");
 }
-// Scores of consecutive columns, and the wait for them.
-__device__ __forceinline__ void ld_scores(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
-__device__ __forceinline__ void ld_scores(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
-__device__ __forceinline__ void wait_scores(uint32_t (&r)[32]) { tmem_wait32(r); }
-__device__ __forceinline__ void wait_scores(uint32_t (&r)[16]) { tmem_wait16(r); }
+__device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
+
+// Largest magnitudes of the even and of the odd ones of eight bf16 (as their bits),
+// those that are not finite left out.
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = w[i] & 0x7fff7fffu;
+    top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+  }
+  return top;
+}
+// The exponent e of a query row's scale from its largest magnitudes: they lie in
+// [2^7, 2^8) of 2^e.  (Not below -107: scales stay normal numbers.)
+__device__ __forceinline__ int row_exponent(uint32_t top) {
+  const int x = (int)max(top & 0xffffu, top >> 16);
+  return max((x >> 7) - 127, -100) - 7;
+}
+
+// Eight elements of a bf16 query row (sixteen lanes hold the row) as hi + lo of two
+// e4m3 values times 2^e, the row's largest magnitude scaled into [128, 256).  bf16
+// has 8 significant bits and e4m3 4: hi takes the first four, what is left is a
+// multiple of 2^-7 of at most 2^-4 (of the element's power of two), which lo holds
+// exactly down to e4m3's smallest step, 2^-9: an element is off by at most 2^-10,
+// 2^-17 of the row's largest.  Elements that are not finite become NaN.
+__device__ __forceinline__ void split_e4m3(const uint4& v, uint2& q_hi, uint2& q_lo) {
+  float f[8];
+  bf16x8_to_f32(v, f);
+  uint32_t top = largest(v);
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float scale = exp2_of(-row_exponent(top));
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = make_float2(f[2 * i] * scale, f[2 * i + 1] * scale);
+    h[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    if (!(fabsf(x.x) < INFINITY)) h[i] = (h[i] & 0xff00u) | 0x7fu;
+    if (!(fabsf(x.y) < INFINITY)) h[i] = (h[i] & 0xffu) | 0x7f00u;
+    const uint32_t back = e4m3x2_to_f16x2((uint16_t)h[i]);
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&back));
+    l[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE,
+                                              __NV_E4M3);
+  }
+  q_hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  q_lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
 
 // ---------------------------------------------------------------- conversion
 // Sixteen-bit pairs with an all-ones exponent -> 0; true if there was one.
@@ -321,97 +380,107 @@ __device__ __forceinline__ void to_f16(const uint4& x, uint32_t (&h)[4]) {
   h[3] = bf16x2_to_f16x2(x.w);
 }
 
+// A chunk of a page's slot: 16 bytes of the tile it becomes (bf16, whose tile it is
+// already), or 16 dims that become two such chunks (e4m3, NVFP4).  Eight (sixteen)
+// lanes take the same chunk of eight (sixteen) rows, which the swizzles of the raw
+// tile (72-byte rows) and of the operand spread over all banks.
+template <int KV>
+struct Chunk {
+  static constexpr bool kBf16 = KV == MSA_KV_BF16, kE4m3 = KV == MSA_KV_FP8_E4M3;
+  static constexpr int kOut = kBf16 ? 1 : 2, kChunks = kTileBytes / 16 / kOut / kConvThreads;
+  uint4 w;                     // as read (NVFP4: 8 bytes, and the scale)
+  int key, c;                  // row, and chunk of the row (of kOut operand chunks)
+
+  __device__ __forceinline__ void load(const uint8_t* raw, int x) {
+    if constexpr (kBf16) {
+      key = (x >> 3) & (kBlock - 1);
+      c = (x & 7) ^ (key & 7) | (x >> 10) << 3;
+      w = *reinterpret_cast<const uint4*>(raw + x * 16);
+    } else if constexpr (kE4m3) {
+      key = (x & 7) | ((x >> 6) << 3);
+      c = (x >> 3) & 7;
+      w = *reinterpret_cast<const uint4*>(raw + key * 128 + ((c ^ (key & 7)) << 4));
+    } else {
+      key = (x & 15) | ((x >> 7) << 4);
+      c = (x >> 4) & 7;
+      const uint8_t* row = raw + key * kFp4Row;
+      const uint2 y = *reinterpret_cast<const uint2*>(row + 8 * c);
+      w.x = y.x;
+      w.y = y.y;
+      w.z = row[kHeadDim / 2 + c];
+    }
+  }
+  // eight fp16 values of operand chunk k
+  __device__ __forceinline__ void convert(int k, uint32_t (&h)[4]) const {
+    if constexpr (kBf16) {
+      to_f16(w, h);
+    } else if constexpr (kE4m3) {
+      const uint32_t u[2] = {k ? w.z : w.x, k ? w.w : w.y};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        h[2 * e] = e4m3x2_to_f16x2((uint16_t)u[e]);
+        h[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(u[e] >> 16));
+      }
+    } else {
+      const uint32_t s = e4m3_scale_f16x2(w.z);
+      e2m1x8_to_f16x2(k ? w.y : w.x, h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = hmul2_u32(h[e], s);
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* tile, int k, const uint32_t (&h)[4]) const {
+    *reinterpret_cast<uint4*>(tile + swz_tma(key, kOut * c + k)) =
+        make_uint4(h[0], h[1], h[2], h[3]);
+  }
+};
+
 // One page's K or V slot -> the operand tile at `tile` (K-major rows, 128-byte
-// swizzle), by all converter threads.  kValues: rows from `ntok` on become 0; of rows from
-// `all` on (which not every query row sees: 0 * NaN is not 0) elements that are
-// not finite become 0 and are noted in `bad` by node.  A bf16 tile is converted in
-// place.  Returns whether a value left the fp16 range.
-template <int KV, bool kValues>
+// swizzle), by a group of converter threads; a bf16 tile in place.  kEdge: a page of
+// values with an end or nodes in it: rows from `ntok` on become 0; of rows from `all`
+// on (which not every query row sees: 0 * NaN is not 0) elements that are not finite
+// become 0 and are noted in `bad` by node.  Returns whether a value left the fp16
+// range.  (The pages without edges are most, and their loop has to stay small: the
+// roles' loops together have to fit the instruction cache.)
+template <int KV, bool kEdge>
 __device__ __forceinline__ bool convert_page(const uint8_t* raw, uint8_t* tile, int tid, int ntok,
                                              int all, unsigned long long* bad) {
-  constexpr int kN = Form<KV>::kConvThreads;
+  using C = Chunk<KV>;
+  constexpr int kAhead = kEdge ? 1 : 4;
   bool ovf = false;
-  auto special = [&](int key, uint32_t (&h)[4]) {
-    if (key >= ntok) {
-      h[0] = h[1] = h[2] = h[3] = 0u;
-    } else {
-      if (KV == MSA_KV_BF16) ovf |= any_inf(h);
-      if (key >= all && clear_non_finite(h)) atomicOr(bad, 1ull << (key - all));
-    }
-  };
-  if constexpr (KV == MSA_KV_BF16) {
-    // a 16-byte chunk lies in one key row, 128 bytes per row and 64-dim half
-    if (all >= kBlock) {
-      uint32_t top = 0u;                       // largest magnitudes
-#pragma unroll 4
-      for (int i = 0; i < kTileBytes / 16 / kN; ++i) {
-        const int off = (tid + kN * i) * 16;
-        uint32_t h[4];
-        to_f16(*reinterpret_cast<const uint4*>(tile + off), h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t m = h[e] & 0x7fff7fffu;
-          const __half2 x = __hmax2(*reinterpret_cast<const __half2*>(&top),
-                                    *reinterpret_cast<const __half2*>(&m));
-          top = *reinterpret_cast<const uint32_t*>(&x);
-        }
-        *reinterpret_cast<uint4*>(tile + off) = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      ovf = f16x2_has_inf(top);
-    } else {
+  uint32_t top = 0;                            // bf16: largest magnitudes
 #pragma unroll 1
-      for (int i = 0; i < kTileBytes / 16 / kN; ++i) {
-        const int off = (tid + kN * i) * 16;
+  for (int i = 0; i < C::kChunks; i += kAhead) {
+    C chunk[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) chunk[e].load(raw, tid + kConvThreads * (i + e));
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+#pragma unroll
+      for (int k = 0; k < C::kOut; ++k) {
         uint32_t h[4];
-        to_f16(*reinterpret_cast<const uint4*>(tile + off), h);
-        special((off & (kTileBytes / 2 - 1)) >> 7, h);
-        *reinterpret_cast<uint4*>(tile + off) = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-    }
-  } else if constexpr (KV == MSA_KV_FP8_E4M3) {
-    // eight lanes take one 16-byte chunk of eight rows: the swizzles of the raw
-    // tile and of the operand spread them over all banks
+        chunk[e].convert(k, h);
+        if (kEdge) {
+          const int key = chunk[e].key;
+          if (key >= ntok) {
+            h[0] = h[1] = h[2] = h[3] = 0u;
+          } else {
+            if (KV == MSA_KV_BF16) ovf |= any_inf(h);
+            if (key >= all && clear_non_finite(h)) atomicOr(bad, 1ull << (key - all));
+          }
+        } else if (KV == MSA_KV_BF16) {
 #pragma unroll
-    for (int i = 0; i < 1024 / kN; ++i) {
-      const int x = tid + kN * i, key = (x & 7) | ((x >> 6) << 3), c = (x >> 3) & 7;
-      const uint4 w = *reinterpret_cast<const uint4*>(raw + key * 128 + ((c ^ (key & 7)) << 4));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          h[2 * e] = e4m3x2_to_f16x2((uint16_t)u[2 * k + e]);
-          h[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(u[2 * k + e] >> 16));
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t m = h[q] & 0x7fff7fffu;
+            const __half2 y = __hmax2(*reinterpret_cast<const __half2*>(&top),
+                                      *reinterpret_cast<const __half2*>(&m));
+            top = *reinterpret_cast<const uint32_t*>(&y);
+          }
         }
-        if (kValues && all < kBlock) special(key, h);
-        *reinterpret_cast<uint4*>(tile + swz_tma(key, 2 * c + k)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
-      }
-    }
-  } else {
-    // sixteen lanes take one block of sixteen rows: 72-byte rows spread over all
-    // banks, and so does the operand's swizzle
-#pragma unroll
-    for (int i = 0; i < 1024 / kN; ++i) {
-      const int x = tid + kN * i, key = (x & 15) | ((x >> 7) << 4), b = (x >> 4) & 7;
-      const uint8_t* row = raw + key * kFp4Row;
-      const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * b);
-      const uint32_t s = e4m3_scale_f16x2(row[kHeadDim / 2 + b]);
-      uint32_t h[2][4];
-      e2m1x8_to_f16x2(w.x, h[0]);
-      e2m1x8_to_f16x2(w.y, h[1]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[k][e] = hmul2_u32(h[k][e], s);
-        if (kValues && all < kBlock) special(key, h[k]);
-        *reinterpret_cast<uint4*>(tile + swz_tma(key, 2 * b + k)) =
-            make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+        chunk[e].store(tile, k, h);
       }
     }
   }
-  return ovf;
+  return ovf | f16x2_has_inf(top);
 }
 
 // Dim d of value row `row` of a page as the converters see it (fp16 range), for
@@ -442,31 +511,39 @@ __global__ void __launch_bounds__(Form<KV>::kThreads, 1)
 tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v) {
   using F = Form<KV>;
-  constexpr int kThreads = F::kThreads, kLoadWarp = F::kLoadWarp, kMmaWarp = F::kMmaWarp;
+  constexpr int kThreads = F::kThreads, kLoadWarp = F::kLoadWarp, kMmaWarp = F::kMmaWarp,
+                kIdleWarp = F::kIdleWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(16) Shared<KV> sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
-  uint8_t* qbuf = smem;                        // two tiles, then the ring's
-  uint8_t* raw = smem + (2 + F::kTiles) * kTileBytes;
   if (tid == 0) {
-    for (int i = 0; i < F::kStages; ++i) {
-      mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], F::kConvWarps);
+    for (int i = 0; i < F::kKeys; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_ready[i], 4);
+      mbar_init(&sh.k_empty[i], 2);            // both MMA warps, or one twice
     }
-    for (int i = 0; i < F::kBufs; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.ready[i], F::kConvWarps);
-      // both MMA warps, or one twice; of tiles that arrive in the ring the converters too
-      mbar_init(&sh.empty[i], F::kRaw ? 2 : 2 + F::kConvWarps);
+    for (int i = 0; i < F::kVals; ++i) {
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_ready[i], 4);
+      mbar_init(&sh.v_empty[i], 2);
+    }
+    for (int i = 0; i < F::kRawKeys; ++i) {
+      mbar_init(&sh.kr_full[i], 1);
+      mbar_init(&sh.kr_empty[i], 4);
+    }
+    for (int i = 0; i < F::kRawVals; ++i) {
+      mbar_init(&sh.vr_full[i], 1);
+      mbar_init(&sh.vr_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], F::kConvWarps);
+      mbar_init(&sh.q_full[i], 4);
       mbar_init(&sh.q_free[i], 2);             // both MMA warps
       mbar_init(&sh.s_ready[i], 1);
       mbar_init(&sh.p_ready[i], 4);
       mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.turn[i], 1);
+      mbar_init(&sh.mid[i], 1);
       mbar_init(&sh.fin[i], 1);
     }
     for (int i = 0; i < kBads; ++i) sh.bad[i] = 0;
@@ -550,10 +627,39 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
       // The pages of a segment 32 at a time (a lane each).
       Walk<KV> wk;
       wk.open(ws, a, sh);
-      Ring<KV> ring;                           // bf16: the operand ring itself
-      int arms = 0, at = 0;
-      uint32_t phase = 0;
+      Place<F::kFp4 ? at_least(F::kRawKeys) : F::kKeys> kp;
+      Place<F::kBf16 ? F::kVals : at_least(F::kRawVals)> vp;
+      int keys = 0, vals = 0;                  // copied
       bool going = true;                       // after a wait gave up nothing more is copied
+      // one page's slot (kind 0 keys, 1 values) into `dst`, once `empty` says so
+      auto copy = [&](const Walk<KV>& wk, int j, int page, int kind, uint64_t* empty, uint64_t* full,
+                      uint32_t par, uint8_t* dst) {
+        going = __all_sync(0xffffffffu, mbar_wait(empty, par ^ 1u, ws.hdr));
+        if (!going) return;
+        if (elect_one()) {
+          if (page < 0) {
+            mbar_arrive(full);
+          } else if constexpr (F::kFp4) {
+            const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2 + kind;
+            const int rows = min(kBlock, wk.q.L - j * kBlock);
+            const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;       // 16 divides it
+            mbar_arrive_expect_tx(full, bytes);
+            bulk_load(dst, (kind ? a.v_pool : a.k_pool) + slot * (kBlock * kFp4Row), bytes, full);
+          } else {
+            const int y = (page * a.Hkv + wk.h) * kBlock;
+            const void* map = kind ? (const void*)&tmap_v : (const void*)&tmap_k;
+            if constexpr (F::kE4m3) {
+              mbar_arrive_expect_tx(full, F::kRawBytes);
+              tma_load_2d(dst, map, 0, y, full);
+            } else {
+              mbar_arrive_expect_tx(full, kTileBytes);
+              tma_load_2d(dst, map, 0, y, full);
+              tma_load_2d(dst + kTileBytes / 2, map, 64, y, full);
+            }
+          }
+        }
+        __syncwarp();
+      };
       while (going && wk.next(ws, a)) {
         int mine = -1;
         for (int j = wk.j0; going && j < wk.j1; ++j) {
@@ -561,59 +667,39 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
           if (k == 0)
             mine = j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + j + lane] : -1;
           const int page = __shfl_sync(0xffffffffu, mine, k);
-          for (int kind = 0; going && kind < 2; ++kind) {
-            uint64_t* full;
-            uint8_t* dst;
-            if constexpr (F::kRaw) {
-              full = &sh.raw_full[at];
-              dst = raw + at * F::kStageBytes;
-              going = mbar_wait(&sh.raw_empty[at], phase ^ 1u, ws.hdr);
-              if (++at == F::kStages) { at = 0; phase ^= 1u; }
-            } else {
-              uint32_t par;
-              const int b = ring.take(wk.tiles, kind, par);
-              full = &sh.full[b];
-              dst = smem + tile_at<KV>(b);
-              going = mbar_wait(&sh.empty[b], par ^ 1u, ws.hdr);
-            }
-            going = __all_sync(0xffffffffu, going);
-            if (going && elect_one()) {
-              if (page < 0) {
-                mbar_arrive(full);
-              } else if constexpr (KV == MSA_KV_NVFP4) {
-                const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2 + kind;
-                const int rows = min(kBlock, wk.q.L - j * kBlock);
-                const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;   // 16 divides it
-                mbar_arrive_expect_tx(full, bytes);
-                bulk_load(dst, (kind ? a.v_pool : a.k_pool) + slot * (kBlock * kFp4Row), bytes,
-                          full);
-              } else {
-                const int y = (page * a.Hkv + wk.h) * kBlock;
-                const void* map = kind ? (const void*)&tmap_v : (const void*)&tmap_k;
-                if constexpr (KV == MSA_KV_FP8_E4M3) {
-                  mbar_arrive_expect_tx(full, F::kStageBytes);
-                  tma_load_2d(dst, map, 0, y, full);
-                } else {
-                  mbar_arrive_expect_tx(full, kTileBytes);
-                  tma_load_2d(dst, map, 0, y, full);
-                  tma_load_2d(dst + kTileBytes / 2, map, 64, y, full);
-                }
-              }
-            }
-            __syncwarp();
-            if (going) ++arms;
-          }
+          if constexpr (F::kFp4)
+            copy(wk, j, page, 0, &sh.kr_empty[kp.b], &sh.kr_full[kp.b], kp.par,
+                 smem + F::kRawAt + kp.b * F::kRawBytes);
+          else
+            copy(wk, j, page, 0, &sh.k_empty[kp.b], &sh.k_full[kp.b], kp.par,
+                 smem + F::kKeyAt + kp.b * F::kKeyBytes);
+          if (!going) break;
+          kp.next();
+          ++keys;
+          if constexpr (F::kBf16)
+            copy(wk, j, page, 1, &sh.v_empty[vp.b], &sh.v_full[vp.b], vp.par,
+                 smem + F::kValAt + vp.b * kTileBytes);
+          else
+            copy(wk, j, page, 1, &sh.vr_empty[vp.b], &sh.vr_full[vp.b], vp.par,
+                 smem + F::kRawAt + (F::kRawKeys + vp.b) * F::kRawBytes);
+          if (!going) break;
+          vp.next();
+          ++vals;
         }
       }
       // Normally the converters and the MMAs wait for every copy issued here.
       // After a wait gave up they may not have: let the copies in flight land.
       if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
-        constexpr int kSlots = F::kRaw ? F::kStages : F::kTiles;
-        for (int i = 0; i < kSlots && i < arms; ++i)
-          mbar_drain(F::kRaw ? &sh.raw_full[i] : &sh.full[i],
-                     (uint32_t)(((arms - 1 - i) / kSlots) & 1));
+        auto drain = [&](uint64_t* bars, int n, int b, uint32_t par, int arms) {
+          for (int i = 0; i < n; ++i)          // its last use: of this round before b, else the last
+            if (i < arms) mbar_drain(&bars[i], i < b ? par : par ^ 1u);
+        };
+        drain(F::kFp4 ? sh.kr_full : sh.k_full, F::kFp4 ? F::kRawKeys : F::kKeys, kp.b, kp.par,
+              keys);
+        drain(F::kBf16 ? sh.v_full : sh.vr_full, F::kBf16 ? F::kVals : F::kRawVals, vp.b, vp.par,
+              vals);
       }
-    } else if (warp < F::kIdleWarp) {
+    } else if (warp < kIdleWarp) {
       // ---------------------------------------------------------------- MMAs
       // A warp per softmax warpgroup w, on the items of w: O += P V, then the next S
       // once that has read the P which it overwrites.  The same wait orders O for
@@ -621,7 +707,8 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
       // warps take turns, an item's P V and the next S together: left to themselves
       // they fall into step, both in the tensor cores, then both in the softmax.
       const int w = warp - kMmaWarp;
-      const uint32_t idesc_s = idesc_f16(F::kRaw ? 0 : 1, kTile, kBlock),
+      // (the fields of e4m3 x e4m3 read as those of fp16 x fp16)
+      const uint32_t idesc_s = idesc_f16(F::kBf16 ? 1 : 0, kTile, kBlock),
                      idesc_o = idesc_f16_bmn(0, kTile, kHeadDim);
       const uint64_t d0 = kstep_desc(smem_u32(smem), 0, kTile),
                      v0 = sdesc_sw128_mn(smem_u32(smem), kTileBytes / 2);
@@ -629,99 +716,114 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
                      v_hi = (uint32_t)(v0 >> 32);
       const uint32_t ts = tmem + w * 128, to = tmem + 256 + w * 128;
       Walk<KV> wk;
-      Ring<KV> ring;
       wk.open(ws, a, sh);
+      Place<F::kKeys> kp;                      // of the next page
+      Place<F::kVals> vp;
       int k0 = 0, mine = 0, qsel = 0;          // first item of the segment; items of w so far
       uint32_t q_phase = 0;                    // bit b: uses of Q buffer b, odd or even
+      uint32_t mids = 0;
+      constexpr int kMid = 2;
       while (wk.next(ws, a)) {
         const bool two = wk.tiles == 2;
         const int pages = wk.j1 - wk.j0, odd = (w ^ k0) & 1;
-        const int qb = two ? odd : (F::kRaw ? 0 : qsel);         // this warp's Q
+        const int qb = two ? odd : qsel;       // this warp's Q
         const int step = two ? 1 : 2;
         if (!two) qsel ^= 1;
-        int kb, vb, kb2 = 0, vb2 = 0;          // tiles of the page, and of this warp's next
-        uint32_t kpar, vpar, kpar2 = 0, vpar2 = 0;
-        auto take = [&](int& k_, uint32_t& kp_, int& v_, uint32_t& vp_) {
-          uint32_t x;
-          k_ = ring.take(wk.tiles, false, kp_, x);
-          v_ = ring.take(wk.tiles, true, vp_, x);
-          if (!F::kRaw) vp_ = x;               // bf16: `ready` counts values alone
-        };
-        auto issue_s = [&](int k_, int p, bool pass) {
+        auto issue_s = [&](int kb, int p, bool pass) {
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t qd = lo + qb * (kTileBytes >> 4), kd = lo + (tile_at<KV>(k_) >> 4);
-            umma_ss<false>(ts, qd, hi, kd, hi, idesc_s);
+            const uint32_t qd = lo + qb * (kTileBytes >> 4),
+                           kd = lo + ((F::kKeyAt + kb * F::kKeyBytes) >> 4);
+            if constexpr (F::kE4m3) {          // Q as two e4m3 tiles, 32 dims a step
 #pragma unroll
-            for (int ks = 1; ks < 8; ++ks) {
-              const uint32_t o = (ks >> 2) * (kTileBytes >> 5) + (ks & 3) * 2;
-              umma_ss<true>(ts, qd + o, hi, kd + o, hi, idesc_s);
-              // the other warp's MMAs queue up behind the last of these
-              if (ks == 4 && pass) mbar_arrive(&sh.turn[w ^ 1]);
+              for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t qs = qd + (ks >> 2) * (kTileBytes >> 5) + (ks & 3) * 2,
+                               kk = kd + (ks & 3) * 2;
+                if (ks == 0) umma_e4m3<false>(ts, qs, hi, kk, hi, idesc_s);
+                else umma_e4m3<true>(ts, qs, hi, kk, hi, idesc_s);
+                if (ks == kMid && pass) umma_commit(&sh.mid[w]);
+              }
+            } else {
+              umma_ss<false>(ts, qd, hi, kd, hi, idesc_s);
+#pragma unroll
+              for (int ks = 1; ks < 8; ++ks) {
+                const uint32_t o = (ks >> 2) * (kTileBytes >> 5) + (ks & 3) * 2;
+                umma_ss<true>(ts, qd + o, hi, kd + o, hi, idesc_s);
+                if (ks == kMid && pass) umma_commit(&sh.mid[w]);
+              }
             }
             umma_commit(&sh.s_ready[w]);
-            umma_commit(&sh.empty[k_]);
-            if (!two) umma_commit(&sh.empty[k_]);                // (counts both warps)
+            umma_commit(&sh.k_empty[kb]);
+            if (!two) umma_commit(&sh.k_empty[kb]);              // (counts both warps)
             if (p + step >= pages) umma_commit(&sh.q_free[qb]);  // its last S
           }
           __syncwarp();
+          if (pass) {
+            // MMAs of two warps would take turns one by one: the turn goes on when
+            // these are so far that the other's first follows their last
+            mbar_wait(&sh.mid[w], mids & 1u, ws.hdr);
+            ++mids;
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&sh.turn[w ^ 1]);
+            __syncwarp();
+          }
         };
         auto wait = [&](uint64_t* bar, uint32_t par) {
           mbar_wait(bar, par, ws.hdr);
           __syncwarp();
         };
-        auto k_bar = [&](int b) { return F::kRaw ? &sh.ready[b] : &sh.full[b]; };
-        int p = two ? 0 : odd;
+        auto k_bar = [&](int b) { return F::kFp4 ? &sh.k_ready[b] : &sh.k_full[b]; };
+        int p = two ? 0 : odd, taken = 0;      // pages that kp and vp have passed
         const bool any = p < pages;
+        auto go = [&](int page) {              // to a page of the segment
+          for (; taken < page; ++taken) {
+            kp.next();
+            vp.next();
+          }
+        };
         if (any) {                             // the first S of the segment, without a turn
-          if (p == 1) take(kb, kpar, vb, vpar);
-          take(kb, kpar, vb, vpar);
-          wait(k_bar(kb), kpar);
+          go(p);
+          wait(k_bar(kp.b), kp.par);
           wait(&sh.q_full[qb], q_phase >> qb & 1u);
           if (mine > 0) wait(&sh.o_done[w], (uint32_t)(mine - 1) & 1u);
-          issue_s(kb, p, false);
+          issue_s(kp.b, p, false);
         }
-        int taken = any ? p + 1 : 0;           // pages whose tiles were taken from the ring
         for (; p < pages; p += step) {
           const bool next = p + step < pages;
-          if (next) {
-            if (!two) take(kb2, kpar2, vb2, vpar2);
-            take(kb2, kpar2, vb2, vpar2);
-            taken = p + step + 1;
-          }
-          wait(&sh.ready[vb], vpar);
+          const int vb = vp.b;
+          wait(&sh.v_ready[vb], vp.par);
+          go(next ? p + step : p);
           wait(&sh.p_ready[w], (uint32_t)mine & 1u);
-          // keys that are not there yet are not waited for in one's turn
-          const bool here =
-              next && __shfl_sync(0xffffffffu, (int)mbar_test_wait(k_bar(kb2), kpar2), 0);
           if (mine > 0 || w == 1)              // phase n of a turn: the other's n-th pass
             wait(&sh.turn[w], (uint32_t)(w ? mine : mine - 1) & 1u);
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t vd = v_lo + (tile_at<KV>(vb) >> 4);
+            const uint32_t vd = v_lo + ((F::kValAt + vb * kTileBytes) >> 4);
             if (p < step) umma_ts<false>(to, ts, vd, v_hi, idesc_o);   // O of the segment begins
             else umma_ts<true>(to, ts, vd, v_hi, idesc_o);
 #pragma unroll
             for (int ks = 1; ks < 8; ++ks)
               umma_ts<true>(to, ts + 8 * ks, vd + 128 * ks, v_hi, idesc_o);
             umma_commit(&sh.o_done[w]);
-            umma_commit(&sh.empty[vb]);
-            if (!two) umma_commit(&sh.empty[vb]);
+            umma_commit(&sh.v_empty[vb]);
+            if (!two) umma_commit(&sh.v_empty[vb]);
           }
           __syncwarp();
+          // Keys that are not there yet are not waited for in one's turn.  (Asked
+          // after the turn came: the other warp's S of the page before is done, and
+          // with it the phase before the one that is asked for.)
+          const bool here =
+              next && __shfl_sync(0xffffffffu, (int)mbar_test_wait(k_bar(kp.b), kp.par), 0);
           if (!here && elect_one()) mbar_arrive(&sh.turn[w ^ 1]);
           __syncwarp();
           if (next) {
-            if (!here) wait(k_bar(kb2), kpar2);
+            if (!here) wait(k_bar(kp.b), kp.par);
             wait(&sh.o_done[w], (uint32_t)mine & 1u);
-            issue_s(kb2, p + step, here);
-            kb = kb2;
-            vb = vb2;
-            vpar = vpar2;
+            issue_s(kp.b, p + step, here);
           }
           ++mine;
         }
-        for (; taken < pages; ++taken) take(kb2, kpar2, vb2, vpar2);
+        go(pages);
         // a Q buffer that this warp did not read: seen all the same, so that none of
         // its phases passes this warp by
         for (int b = 0; b < 2; ++b) {
@@ -739,7 +841,7 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
       if (elect_one()) umma_commit(&sh.fin[w]);
       __syncwarp();
       mbar_drain(&sh.fin[w], 0);
-    } else if (warp == F::kIdleWarp) {
+    } else if (warp == kIdleWarp) {
       // tokens of no request that has a tree
       const int T = ws.hdr->num_tokens;
       for (int t = blockIdx.x; t < T; t += gridDim.x) {
@@ -757,14 +859,18 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------------------ converters
     regs_down<F::kConvRegs>();
-    const int ct = tid - kConvWarp * 32;
+    // Four warps convert the values (and load Q), four more the keys of NVFP4 pages
+    // (and load Q there).
+    const int ct = (tid - kConvWarp * 32) & (kConvThreads - 1);
+    const bool keys = F::kFp4 && warp < kConvWarp + 4;
     Walk<KV> wk;
     wk.open(ws, a, sh);
-    Ring<KV> ring;
-    int seg = 0, qsel = 0, st = 0;
-    uint32_t st_phase = 0;
+    Place<F::kKeys> kp;
+    Place<F::kVals> vp;
+    Place<at_least(F::kRawKeys)> krp;
+    Place<at_least(F::kRawVals)> vrp;
+    int seg = 0, qsel = 0;
     uint32_t q_used = 0, q_phase = 0;          // bit b: Q buffer b was used; its uses, odd or even
-    bool extra_used = false;                   // the second Q buffer held a tile of the ring
     auto done = [&](uint64_t* bar) {
       fence_proxy_async_smem();
       __syncwarp();
@@ -773,36 +879,53 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
     // Q rows of tile t of the segment into buffer b, zero past the last
     auto load_q = [&](int t, int b) {
       if (q_used >> b & 1u) mbar_wait(&sh.q_free[b], (q_phase >> b & 1u) ^ 1u, ws.hdr);
-      if (F::kRaw && b == 1 && extra_used)
-        mbar_wait(&sh.empty[F::kTiles], (ring.uses >> F::kTiles & 1u) ^ 1u, ws.hdr);
       q_used |= 1u << b;
       q_phase ^= 1u << b;
       bool ovf = false;
       const int first = wk.pair * kPairRows + t * kTile, rows = wk.rows - t * kTile;
-#pragma unroll (F::kRaw ? 4 : 8)
-      for (int i = 0; i < kTile * 16 / F::kConvThreads; ++i) {
-        const int x = ct + F::kConvThreads * i, row = x >> 4, ch = x & 15;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows)
-          v = *reinterpret_cast<const uint4*>(
-              a.q + a.q_row(wk.q.t0, wk.h, first + row) * kHeadDim + 8 * ch);
-        if (F::kRaw) {
-          uint32_t h[4];
-          to_f16(v, h);
-          ovf |= any_inf(h);
-          v = make_uint4(h[0], h[1], h[2], h[3]);
+      uint8_t* dst = smem + b * kTileBytes;
+      constexpr int kN = kTile * 16 / kConvThreads, kBatch = F::kFp4 ? 4 : 8;
+      for (int i0 = 0; i0 < kN; i0 += kBatch) {                  // a batch's loads in flight
+        uint4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int x = ct + kConvThreads * (i0 + i), row = x >> 4, ch = x & 15;
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (row < rows)
+            v[i] = *reinterpret_cast<const uint4*>(
+                a.q + a.q_row(wk.q.t0, wk.h, first + row) * kHeadDim + 8 * ch);
         }
-        *reinterpret_cast<uint4*>(qbuf + b * kTileBytes + kmaj_off(row, ch, kTile)) = v;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int x = ct + kConvThreads * (i0 + i), row = x >> 4, ch = x & 15;
+          if constexpr (F::kE4m3) {
+            uint2 q_hi, q_lo;
+            split_e4m3(v[i], q_hi, q_lo);
+            uint8_t* at = dst + row * 128 + (((ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = q_hi;
+            *reinterpret_cast<uint2*>(at + kTileBytes / 2) = q_lo;
+          } else {
+            if constexpr (F::kFp4) {
+              uint32_t h[4];
+              to_f16(v[i], h);
+              ovf |= any_inf(h);
+              v[i] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            *reinterpret_cast<uint4*>(dst + kmaj_off(row, ch, kTile)) = v[i];
+          }
+        }
       }
-      if (F::kRaw && __any_sync(0xffffffffu, ovf) && lane == 0)
+      if (F::kFp4 && __any_sync(0xffffffffu, ovf) && lane == 0)
         set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
       done(&sh.q_full[b]);
     };
     while (wk.next(ws, a)) {
-      if (ct == 0) sh.bad[(seg + kBads / 2) & (kBads - 1)] = 0;
-      load_q(0, F::kRaw || wk.tiles == 2 ? 0 : qsel);
-      if (!F::kRaw && wk.tiles == 2) load_q(1, 1);
+      if (!F::kFp4 || keys) {
+        load_q(0, wk.tiles == 2 ? 0 : qsel);
+        if (wk.tiles == 2) load_q(1, 1);
+      }
       if (wk.tiles == 1) qsel ^= 1;
+      if (!keys && ct == 0) sh.bad[(seg + kBads / 2) & (kBads - 1)] = 0;
       // ---- pages
       unsigned long long* bad = &sh.bad[seg & (kBads - 1)];
       int mine = -1;
@@ -814,43 +937,40 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
         const bool usable = __shfl_sync(0xffffffffu, mine, k) >= 0;
         const int ntok = usable ? wk.q.L - j * kBlock : 0;       // keys that exist
         const int all = usable ? wk.q.base - j * kBlock : 0;     // and that every row sees
-#pragma unroll
-        for (int kind = 0; kind < 2; ++kind) {
-          uint32_t par;
-          if constexpr (F::kRaw) {
-            const int b = ring.take(wk.tiles, kind, par);
-            uint8_t* tile = smem + tile_at<KV>(b);
-            const uint8_t* src = raw + st * F::kStageBytes;
-            mbar_wait(&sh.empty[b], par ^ 1u, ws.hdr);
-            if (b == F::kTiles) {              // the second Q buffer: its last S is done
-              extra_used = true;
-              if (q_used & 2u) mbar_wait(&sh.q_free[1], (q_phase >> 1 & 1u) ^ 1u, ws.hdr);
-            }
-            mbar_wait(&sh.raw_full[st], st_phase, ws.hdr);
-            if (kind == 0) convert_page<KV, false>(src, tile, ct, ntok, all, nullptr);
-            else convert_page<KV, true>(src, tile, ct, ntok, all, bad);
+        if (keys) {
+          if constexpr (F::kFp4) {
+            mbar_wait(&sh.kr_full[krp.b], krp.par, ws.hdr);
+            mbar_wait(&sh.k_empty[kp.b], kp.par ^ 1u, ws.hdr);
+            convert_page<KV, false>(smem + F::kRawAt + krp.b * F::kRawBytes,
+                                    smem + F::kKeyAt + kp.b * kTileBytes, ct, 0, 0, nullptr);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.raw_empty[st]);
-            if (++st == F::kStages) { st = 0; st_phase ^= 1u; }
-            done(&sh.ready[b]);
-            // the second tile's Q comes after the first K: the last V of a segment of
-            // one tile may still be where it goes
-            if (kind == 0 && j == wk.j0 && wk.tiles == 2) load_q(1, 1);
-          } else {
-            const int b = ring.take(wk.tiles, kind, par);
-            // keys are waited for as well: a copy may land after a later one, and a
-            // wait is only for the phase after one that was seen
-            mbar_wait(&sh.full[b], par, ws.hdr);
-            if (kind == 1) {
-              ovf |= convert_page<KV, true>(nullptr, smem + tile_at<KV>(b), ct, ntok, all, bad);
-              done(&sh.ready[b]);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.empty[b]);
+            if (lane == 0) mbar_arrive(&sh.kr_empty[krp.b]);
+            done(&sh.k_ready[kp.b]);
+            krp.next();
+            kp.next();
           }
+          continue;
         }
+        uint8_t* tile = smem + F::kValAt + vp.b * kTileBytes;
+        if constexpr (F::kBf16) {
+          mbar_wait(&sh.v_full[vp.b], vp.par, ws.hdr);
+          ovf |= all >= kBlock ? convert_page<KV, false>(tile, tile, ct, 0, 0, nullptr)
+                               : convert_page<KV, true>(tile, tile, ct, ntok, all, bad);
+        } else {
+          mbar_wait(&sh.vr_full[vrp.b], vrp.par, ws.hdr);
+          mbar_wait(&sh.v_empty[vp.b], vp.par ^ 1u, ws.hdr);
+          const uint8_t* src = smem + F::kRawAt + (F::kRawKeys + vrp.b) * F::kRawBytes;
+          if (all >= kBlock) convert_page<KV, false>(src, tile, ct, 0, 0, nullptr);
+          else convert_page<KV, true>(src, tile, ct, ntok, all, bad);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.vr_empty[vrp.b]);
+          vrp.next();
+        }
+        done(&sh.v_ready[vp.b]);
+        vp.next();
       }
-      if (__any_sync(0xffffffffu, ovf) && lane == 0) set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
+      if (F::kBf16 && __any_sync(0xffffffffu, ovf) && lane == 0)
+        set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
       ++seg;
     }
   } else {
@@ -859,18 +979,19 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
     // so that the named barriers match even after a wait gave up.
     regs_up<F::kSoftRegs>();
     constexpr int kBar = 1, kCount = kSoftWarps * 32;
-    constexpr int kC = F::kRaw ? 16 : 32;      // columns at a time, by the registers there are
+    constexpr int kC = 32;                     // columns at a time
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lanes + wg * 128, to = lanes + 256 + wg * 128;
     Walk<KV> wk;
     wk.open(ws, a, sh);
-    int k0 = 0, seg = 0;                       // first item of the segment
+    int k0 = 0, seg = 0;                       // k0: first item of the segment
     int4 split = make_int4(0, 0, 0, 0);
     while (wk.next(ws, a)) {
       const bool two = wk.tiles == 2;
       const int pages = wk.j1 - wk.j0, odd = (wg ^ k0) & 1;
       const int t = two ? odd : 0;             // this warpgroup's tile
+      float sc = a.scale_log2;                 // exponent of a score
       float m = -INFINITY, l = 0.f;
       uint64_t mask = 0;                       // what the row sees of the nodes
       const int n = t * kTile + row;           // row of the pair
@@ -879,6 +1000,14 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
         const int i = a.node_of(wk.pair * kPairRows + n);
         mask = a.mask ? (uint64_t)a.mask[wk.q.t0 + i] : ~0ull >> (63 - i);
         if (wk.q.n < 64) mask &= (1ull << wk.q.n) - 1;
+        if constexpr (F::kE4m3) {              // the scale of the row's Q, from the row itself
+          const uint4* q = reinterpret_cast<const uint4*>(
+              a.q + a.q_row(wk.q.t0, wk.h, wk.pair * kPairRows + n) * kHeadDim);
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) top = __vmaxu2(top, largest(q[c]));
+          sc = a.scale_log2 * exp2_of(row_exponent(top));
+        }
       }
       int mine = -1, have = -1;
       bool first = true, fast = false;         // first: page of this warpgroup's
@@ -894,25 +1023,8 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
         mbar_wait(&sh.s_ready[wg], (uint32_t)(k >> 1) & 1u, ws.hdr);
         tc_fence_after();
         const bool plain = usable && d >= kBlock;
-        const uint64_t sl = f2(a.scale_log2, a.scale_log2), bias = f2(kBias, kBias);
+        const uint64_t sl = f2(sc, sc), bias = f2(kBias, kBias);
         uint64_t sum0 = 0, sum1 = 0;
-        // P = 2^((s - m) scale + bias) of kC columns, as fp16 pairs from pk[0] on
-        auto prob = [&](const uint32_t (&x)[kC], uint64_t rf, uint32_t* pk) {
-#pragma unroll
-          for (int i = 0; i < kC / 2; i += 2) {
-            float p0, p1, p2, p3;
-            f2_split(fma_f2(add_f2(f2u(x[2 * i], x[2 * i + 1]), rf), sl, bias), p0, p1);
-            f2_split(fma_f2(add_f2(f2u(x[2 * i + 2], x[2 * i + 3]), rf), sl, bias), p2, p3);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            p2 = ex2_approx(p2);
-            p3 = ex2_approx(p3);
-            sum0 = add_f2(sum0, f2(p0, p1));
-            sum1 = add_f2(sum1, f2(p2, p3));
-            pk[i] = pack_f16(p0, p1);
-            pk[i + 1] = pack_f16(p2, p3);
-          }
-        };
         float mx[2];
         auto most = [&](const uint32_t (&x)[kC]) {
 #pragma unroll
@@ -927,7 +1039,7 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
           // One pass, with m as it is and -m scale + bias rounded to fp32 (fast: off
           // by less than 2^-18): P stays in registers until its sum says that no
           // probability is beyond fp16.
-          const float c0 = fmaf(-m, a.scale_log2, kBias);
+          const float c0 = fmaf(-m, sc, kBias);
           const uint64_t cc = f2(c0, c0);
           auto prob1 = [&](const uint32_t (&x)[kC], uint32_t* y) {
 #pragma unroll
@@ -946,22 +1058,34 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
             }
           };
           uint32_t xa[kC], xb[kC];
-          ld_scores(ts, xa);
+          if constexpr (F::kFp4) {             // fewer registers: no loads ahead
 #pragma unroll
-          for (int c = 0; c < kBlock; c += 2 * kC) {
-            wait_scores(xa);
-            ld_scores(ts + c + kC, xb);
-            prob1(xa, pk + c / 2);
-            wait_scores(xb);
-            if (c + 2 * kC < kBlock) ld_scores(ts + c + 2 * kC, xa);
-            prob1(xb, pk + (c + kC) / 2);
+            for (int c = 0; c < kBlock; c += kC) {
+              tmem_ld32(ts + c, xa);
+              tmem_wait32(xa);
+              prob1(xa, pk + c / 2);
+            }
+          } else {
+            tmem_ld32(ts, xa);
+#pragma unroll
+            for (int c = 0; c < kBlock; c += 2 * kC) {
+              tmem_wait32(xa);
+              tmem_ld32(ts + c + kC, xb);
+              prob1(xa, pk + c / 2);
+              tmem_wait32(xb);
+              if (c + 2 * kC < kBlock) tmem_ld32(ts + c + 2 * kC, xa);
+              prob1(xb, pk + (c + kC) / 2);
+            }
           }
           float s0, s1;
           f2_split(add_f2(sum0, sum1), s0, s1);
           good = __all_sync(0xffffffffu, s0 + s1 < kMaxSum);
         }
-        if (!good) {
-          // Two passes: the row's maximum over what it sees, then P.
+        if (good) {
+          tmem_st64(ts, pk);                   // over S
+        } else {
+          // Two passes: the row's maximum over what it sees, then P.  (Loops: this is
+          // for pages with an end or nodes in them, and where m moves.)
           auto see = [&](uint32_t (&x)[kC], int c) {             // columns c ..
             if (plain) return;
             const int e = d - c;
@@ -978,77 +1102,89 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
           mx[0] = mx[1] = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < kBlock; c += kC) {
-            ld_scores(ts + c, x);
-            wait_scores(x);
+            tmem_ld32(ts + c, x);
+            tmem_wait32(x);
             see(x, c);
             most(x);
           }
           const float top = fmaxf(mx[0], mx[1]);
           if (__any_sync(0xffffffffu, top > m)) {
             const float mn = fmaxf(m, top);
-            const float alpha = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * a.scale_log2);
+            const float alpha = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sc);
             m = mn;
             l *= alpha;
             if (!first) {                      // (S was issued after the last P V of this O)
 #pragma unroll 1
               for (int c = 0; c < kHeadDim; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(to + c, o);
-                tmem_wait32(o);
+                tmem_ld32(to + c, x);
+                tmem_wait32(x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st32(to + c, o);
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+                tmem_st32(to + c, x);
               }
             }
           }
+          // P = 2^((s - m) scale + bias)
           const float ref = m == -INFINITY ? 0.f : -m;
           const uint64_t rf = f2(ref, ref);
           sum0 = sum1 = 0;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kBlock; c += kC) {
-            ld_scores(ts + c, x);
-            wait_scores(x);
+            tmem_ld32(ts + c, x);
+            tmem_wait32(x);
             see(x, c);
-            prob(x, rf, pk + c / 2);
+            uint32_t y[kC / 2];
+#pragma unroll
+            for (int i = 0; i < kC / 2; ++i) {
+              float p0, p1;
+              f2_split(fma_f2(add_f2(f2u(x[2 * i], x[2 * i + 1]), rf), sl, bias), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              sum0 = add_f2(sum0, f2(p0, p1));
+              y[i] = pack_f16(p0, p1);
+            }
+            tmem_st16(ts + c / 2, y);          // over columns that were read
           }
         }
-        tmem_st64(ts, pk);                     // over S
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_ready[wg]);
-        float s0, s1;
-        f2_split(add_f2(sum0, sum1), s0, s1);
-        l += s0 + s1;
+        {
+          float s0, s1;
+          f2_split(add_f2(sum0, sum1), s0, s1);
+          l += s0 + s1;
+        }
         first = false;
-        fast = __all_sync(0xffffffffu, fabsf(m) * a.scale_log2 < kNear);
+        fast = __all_sync(0xffffffffu, fabsf(m) * sc < kNear);
       }
 
       // ---- the segment's result: whole rows, or a partial
       const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.starts ? 1 : 0);
       const int items = pages * wk.tiles, kl = k0 + items - 1;   // the last item, and the one
                                                                  // before it in the other slot
-      float* part = a.o_part + (slot * a.rows + n) * kHeadDim;
+      auto part = [&](int dim) {               // this row's 4 dims from dim on
+        return a.o_part + ((slot * (kHeadDim / 4) + dim / 4) * a.rows + n) * 4;
+      };
       const int64_t out_row = on ? a.q_row(wk.q.t0, wk.h, wk.pair * kPairRows + n) : 0;
       // 32 dims of the row from dim on
       auto put = [&](const uint32_t (&o)[32], int dim, float inv) {
         if (!on) return;
         if (wk.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * kHeadDim + dim);
+          __nv_bfloat16* dst = a.out + out_row * kHeadDim + dim;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t h[4];
+          for (int i = 0; i < 2; ++i) {
+            uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              h[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                               __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int e = 0; e < 8; ++e)
+              h[e] = pack_bf16(__uint_as_float(o[16 * i + 2 * e]) * inv,
+                               __uint_as_float(o[16 * i + 2 * e + 1]) * inv);
+            store32(dst + 16 * i, h, a.out32);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            reinterpret_cast<uint4*>(part + dim)[i] =
+            *reinterpret_cast<uint4*>(part(dim + 4 * i)) =
                 make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       };
@@ -1081,8 +1217,8 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
         if (both) {
           m = fmaxf(ml.x, mo.x);
           if (m != -INFINITY) {
-            fl = ex2_approx((ml.x - m) * a.scale_log2);
-            fo = ex2_approx((mo.x - m) * a.scale_log2);
+            fl = ex2_approx((ml.x - m) * sc);
+            fo = ex2_approx((mo.x - m) * sc);
           }
           l = ml.y * fl + mo.y * fo;
         }
@@ -1110,9 +1246,9 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
       }
       if (on && (two || wg == 0)) {
         if (wk.whole)
-          a.lse[out_row] = l == 0.f ? -INFINITY : (m * a.scale_log2 + log2f(l) - kBias) * kLn2;
+          a.lse[out_row] = l == 0.f ? -INFINITY : (m * sc + log2f(l) - kBias) * kLn2;
         else
-          a.ml_part[slot * a.rows + n] = make_float2(m, l);
+          a.ml_part[slot * a.rows + n] = make_float2(F::kE4m3 ? m * (sc / a.scale_log2) : m, l);
       }
       // rare: values that are not finite, of nodes that the row sees
       for (unsigned long long b = on ? sh.bad[seg & (kBads - 1)] & mask : 0; b; b &= b - 1) {
@@ -1125,7 +1261,7 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
             __nv_bfloat16* y = a.out + out_row * kHeadDim + dim;
             *y = __float2bfloat16_rn(__bfloat162float(*y) + v);
           } else {
-            part[dim] += v;
+            part(dim)[dim & 3] += v;
           }
         }
       }
@@ -1149,13 +1285,22 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
 
 // ---------------------------------------------------------------- the merge
 // The groups that lie in several CTAs' ranges: every block lists them in order,
-// then takes its share of (group, row), a warp a row (a lane four dims).
-constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+// then takes its share of (group, 32 rows).  A lane has a row, as the partials are
+// laid out.  Up to kFew partials: a warp takes 16 of the 128 dims, all loads in
+// flight at once.  More: a block takes 32 dims, its warps every eighth partial,
+// and joins their sums in shared memory.
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32, kFew = 4;
 constexpr int kMergeChunks = (kMaxCtas + kMergeThreads - 1) / kMergeThreads;
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, int ctas) {
   __shared__ int4 list[kMaxCtas];
   __shared__ int owner[kMaxCtas];
   __shared__ int counts[kMergeChunks * kMergeWarps];
+  __shared__ union {
+    float sums[kMergeWarps][32][33];           // [warp][row][dim], and l
+    uint4 stage[32][17];                       // rows of 256 bytes
+  } u;
+  auto& sums = u.sums;
+  auto& stage = u.stage;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
   griddep_wait();
@@ -1185,38 +1330,129 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
     }
   }
   __syncthreads();
-  const int64_t items = (int64_t)n * a.rows;
-  for (int64_t item = (int64_t)blockIdx.x * kMergeWarps + warp; item < items;
-       item += (int64_t)gridDim.x * kMergeWarps) {
-    const int gi = (int)(item / a.rows), row = (int)(item - (int64_t)gi * a.rows);
+  const int tiles = (a.rows + 31) / 32, items = n * tiles * 4;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int quarter = item & 3, gi = (item >> 2) / tiles, row0 = ((item >> 2) - gi * tiles) * 32;
     const int4 g = list[gi];
-    if (row >= (g.w & 0xffff)) continue;
+    const int rows = g.w & 0xffff, np = g.x, row = row0 + lane;
+    if (row0 >= rows || (np <= kFew && quarter != 0)) continue;  // (the whole block)
     const int64_t c0 = owner[gi];
+    const bool on = row < rows;
     // partial i: the second slot of c0, the first of c0 + i
-    auto at = [&](int i) { return (2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
-    float M = -INFINITY;
-    for (int i = lane; i < g.x; i += 32) M = fmaxf(M, a.ml_part[at(i)].x);
+    auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+    auto ml_of = [&](int i) {
+      return on ? a.ml_part[slot(i) * a.rows + row] : make_float2(-INFINITY, 0.f);
+    };
+    auto o_of = [&](int i, int chunk) {
+      return on ? *reinterpret_cast<const float4*>(
+                      a.o_part + ((slot(i) * (kHeadDim / 4) + chunk) * a.rows + row) * 4)
+                : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    auto weight = [&](float m, float M) {
+      return M == -INFINITY ? 1.f : ex2_approx((m - M) * a.scale_log2);
+    };
+    auto lse_of = [&](float M, float l) {
+      return l == 0.f ? -INFINITY : (M * a.scale_log2 + log2f(l) - kBias) * kLn2;
+    };
+    const int64_t hq = on ? a.q_row(g.y, g.z, (g.w >> 16) * kPairRows + row) : 0;
+    if (np <= kFew) {
+      float2 ml[kFew];
+      float4 v[kFew][4];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < g.x; ++i) {
-      const float2 ml = a.ml_part[at(i)];
-      const float4 v = *reinterpret_cast<const float4*>(a.o_part + at(i) * kHeadDim + 4 * lane);
-      const float f = M == -INFINITY ? 1.f : ex2_approx((ml.x - M) * a.scale_log2);
-      l = fmaf(f, ml.y, l);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
+      for (int i = 0; i < kFew; ++i) {
+        ml[i] = i < np ? ml_of(i) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[i][c] = i < np ? o_of(i, 4 * warp + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float M = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) M = fmaxf(M, ml[i].x);
+      float4 o[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        if (i >= np) continue;
+        const float f = weight(ml[i].x, M);
+        l = fmaf(f, ml[i].y, l);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          o[c].x = fmaf(f, v[i][c].x, o[c].x);
+          o[c].y = fmaf(f, v[i][c].y, o[c].y);
+          o[c].z = fmaf(f, v[i][c].z, o[c].z);
+          o[c].w = fmaf(f, v[i][c].w, o[c].w);
+        }
+      }
+      const float inv = l == 0.f ? 0.f : a.v_scale / l;
+#pragma unroll
+      for (int c = 0; c < 4; c += 2)           // 16 dims of 32 rows, out through shared memory
+        stage[lane][2 * warp + c / 2] =
+            make_uint4(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv),
+                       pack_bf16(o[c + 1].x * inv, o[c + 1].y * inv),
+                       pack_bf16(o[c + 1].z * inv, o[c + 1].w * inv));
+      if (warp == 0 && on) a.lse[hq] = lse_of(M, l);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {            // a warp's four rows, 16 lanes a row
+        const int r = 4 * warp + k;
+        const int64_t to = __shfl_sync(0xffffffffu, hq, r);
+        if (row0 + r < rows && lane < 16)
+          reinterpret_cast<uint4*>(a.out + to * kHeadDim)[lane] = stage[r][lane];
+      }
+      __syncthreads();
+    } else {
+      float M = -INFINITY;
+#pragma unroll 8
+      for (int i = 0; i < np; ++i) M = fmaxf(M, ml_of(i).x);
+      float4 o[8];
+      float l = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int i = warp; i < np; i += kMergeWarps) {
+        const float2 ml = ml_of(i);
+        float4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = o_of(i, 8 * quarter + c);
+        const float f = weight(ml.x, M);
+        l = fmaf(f, ml.y, l);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          o[c].x = fmaf(f, v[c].x, o[c].x);
+          o[c].y = fmaf(f, v[c].y, o[c].y);
+          o[c].z = fmaf(f, v[c].z, o[c].z);
+          o[c].w = fmaf(f, v[c].w, o[c].w);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        sums[warp][lane][4 * c] = o[c].x;
+        sums[warp][lane][4 * c + 1] = o[c].y;
+        sums[warp][lane][4 * c + 2] = o[c].z;
+        sums[warp][lane][4 * c + 3] = o[c].w;
+      }
+      sums[warp][lane][32] = l;
+      __syncthreads();
+      // thread: row tid / 8, 4 dims; the warps' sums in order
+      const int r = tid >> 3, d = (tid & 7) * 4;
+      float y[4] = {0.f, 0.f, 0.f, 0.f}, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += sums[w][r][d + e];
+        ll += sums[w][r][32];
+      }
+      const int64_t to = __shfl_sync(0xffffffffu, hq, r);
+      const float Mr = __shfl_sync(0xffffffffu, M, r);
+      if (row0 + r < rows) {
+        const float inv = ll == 0.f ? 0.f : a.v_scale / ll;
+        *reinterpret_cast<uint2*>(a.out + to * kHeadDim + 32 * quarter + d) =
+            make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+        if (quarter == 0 && (tid & 7) == 0) a.lse[to] = lse_of(Mr, ll);
+      }
+      __syncthreads();
     }
-    const int64_t hq = a.q_row(g.y, g.z, (g.w >> 16) * kPairRows + row);
-    const float inv = l == 0.f ? 0.f : a.v_scale / l;
-    reinterpret_cast<uint2*>(a.out + hq * kHeadDim)[lane] =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (lane == 0)
-      a.lse[hq] = l == 0.f ? -INFINITY : (M * a.scale_log2 + log2f(l) - kBias) * kLn2;
   }
 }
 
@@ -1247,8 +1483,8 @@ msa_status launch_tree(const WsView& v, const TreeArgs& a, int64_t pool_rows, in
   msa_status st = launch_pdl(tree_attention_kernel<KV>, dim3((unsigned)grid), dim3(F::kThreads),
                              F::kSmem, s, v, a, tk, tv);
   if (st != MSA_OK) return st;
-  int64_t blocks = grid * ((a.rows + kMergeWarps - 1) / kMergeWarps);
-  if (blocks > 8 * sm_count()) blocks = 8 * sm_count();
+  int64_t blocks = grid * ((a.rows + 31) / 32) * 4;
+  if (blocks > 4 * sm_count()) blocks = 4 * sm_count();
   return launch_pdl(tree_merge_kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a,
                     (int)grid);
 }
@@ -1302,6 +1538,7 @@ extern "C" msa_status msa_tree_attention(const msa_config* cfg, void* ws, const 
   a.g_magic = ((1u << 20) + a.G - 1) / a.G;    // exact for rows up to 1024 and G <= 16
   a.max_blocks = cfg->max_blocks_per_req;
   a.rows = part_rows(*cfg);
+  a.out32 = ((uintptr_t)out & 31) == 0;
   a.q = (const __nv_bfloat16*)q;
   a.k_pool = (const uint8_t*)k_pages;
   a.v_pool = (const uint8_t*)v_pages;

@@ -10,6 +10,8 @@ bounds derived from the roundings the kernel makes:
 * a score is 128 exact products summed by the tensor cores, 8 accumulations of
   16 products each, every one within 2^-22 of the largest magnitude reached,
   which softmax_scale |q| |k| bounds: e = 8 * 2 * 2^-22 * max |q| |k| scale;
+* with e4m3 pools an element of q is off by up to 2^-17 of its row's largest
+  (two e4m3 values stand for it): 2^-17 max |q_d| sum |k_d| scale more;
 * P V accumulates n / 16 times, 2^-22 each: n / 4 * 2^-24; the sum of n
   probabilities in fp32 is n / 4 per accumulator, 2^-24 each, and merges add less
   than 64 such steps;
@@ -256,11 +258,47 @@ def test_an_infinite_value_that_no_other_node_sees():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kv", ["fp8_e4m3", "nvfp4"])
-def test_queries_beyond_fp16_are_flagged(kv):
-    s = Step(8, 1, [300], [3], kv)
+def test_queries_beyond_fp16():
+    """Flagged with NVFP4 pools; with the others they are within the range."""
+    s = Step(8, 1, [300], [3], "nvfp4")
     s.q[0, 3, 5] = 1.0e5
     assert msa.check_device_error(s.attend().ws) == 16
+    for kv in ("bf16", "fp8_e4m3"):
+        s = Step(8, 1, [300], [3], kv)
+        s.q[0, 3] *= 2.0 ** 18
+        s.q[1, 2] *= 2.0 ** -40
+        s.q[2, 1] = 0.0
+        d = s.attend()
+        assert msa.check_device_error(d.ws) == 0
+        s.check(d)
+
+
+@pytest.mark.gpu
+def test_queries_of_very_different_elements():
+    """e4m3 pools: rows whose elements span many powers of two, so that the small
+    ones lose bits beside the largest."""
+    s = Step(16, 2, [700, 130], [9, 30], "fp8_e4m3", seed=23)
+    g = torch.Generator(device="cuda").manual_seed(24)
+    e = torch.randint(-14, 4, s.q.shape, generator=g, device="cuda")
+    s.q.copy_(s.q.float() * torch.exp2(e.float()))
+    d = s.attend()
+    assert msa.check_device_error(d.ws) == 0
+    s.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", KV)
+def test_an_infinite_query_stays_in_its_row(kv):
+    s = Step(8, 2, [900, 30], [5, 20], kv, seed=25)
+    want = s.attend()
+    s.q[3, 2, 9] = float("inf")
+    d = s.attend()
+    assert msa.check_device_error(d.ws) == (16 if kv == "nvfp4" else 0)
+    clean = torch.ones_like(d.lse, dtype=torch.bool)
+    clean[3, 2] = False
+    assert not bool(torch.isfinite(d.out[3, 2]).any())
+    assert torch.equal(d.out[clean], want.out[clean])
+    assert torch.equal(d.lse[clean], want.lse[clean])
 
 
 @pytest.mark.gpu

@@ -115,6 +115,9 @@ class Step:
                 block_size=128, softmax_scale=c.softmax_scale)
             top = np.sqrt((k ** 2).sum(-1)).max() * np.sqrt((q ** 2).sum(-1)) * c.softmax_scale
             e = 16 * 2.0 ** -22 * top + 2.0 ** -21
+            if self.kv == "fp8_e4m3":            # Q as two e4m3 values
+                e = e + (2.0 ** -17 * np.abs(q).max(-1) * np.abs(k).sum(-1).max()
+                         * c.softmax_scale)
             n = max(max(self.lens), 1)
             tol = (2.0 ** -8 * np.abs(out) + (2.0 ** -11 + 2 * e + (n / 4 + 64) * 2.0 ** -24
                                               )[..., None] * mag + 2.0 ** -24)
