@@ -49,6 +49,7 @@ constexpr int kMaxCtas = 320;
 constexpr float kBias = 7.f;                   // exponent offset of the probabilities
 constexpr float kMaxSum = 60000.f;             // a row's sum over a page that fp16 holds
 constexpr float kNear = 64.f;                  // |m| of the fast path, in exponents
+constexpr float kSlack = 8.f;                  // m lags by up to that
 
 constexpr int kSoftWarps = 8, kConvWarp = kSoftWarps, kConvThreads = 128;   // of a group
 constexpr int kBads = 16;
@@ -336,24 +337,29 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
 // multiple of 2^-7 of at most 2^-4 (of the element's power of two), which lo holds
 // exactly down to e4m3's smallest step, 2^-9: an element is off by at most 2^-10,
 // 2^-17 of the row's largest.  Elements that are not finite become NaN.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
 __device__ __forceinline__ void split_e4m3(const uint4& v, uint2& q_hi, uint2& q_lo) {
-  float f[8];
-  bf16x8_to_f32(v, f);
   uint32_t top = largest(v);
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float scale = exp2_of(-row_exponent(top));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = make_float2(f[2 * i] * scale, f[2 * i + 1] * scale);
-    h[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-    if (!(fabsf(x.x) < INFINITY)) h[i] = (h[i] & 0xff00u) | 0x7fu;
-    if (!(fabsf(x.y) < INFINITY)) h[i] = (h[i] & 0xffu) | 0x7f00u;
-    const uint32_t back = e4m3x2_to_f16x2((uint16_t)h[i]);
-    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&back));
-    l[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE,
-                                              __NV_E4M3);
+    // times 0 is NaN where it is not finite, and adds nothing elsewhere; the eight
+    // bits fit fp16's eleven, below 2^-16 apart, and so does what hi leaves
+    const float a = bf16lo(w[i]), b = bf16hi(w[i]);
+    const uint32_t x = pack_f16(fmaf(a, 0.f, a * scale), fmaf(b, 0.f, b * scale));
+    h[i] = e4m3x2_of_f16x2(x);
+    const uint32_t y = e4m3x2_to_f16x2((uint16_t)h[i]);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x),
+                              *reinterpret_cast<const __half2*>(&y));
+    l[i] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&r));
   }
   q_hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   q_lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
@@ -386,7 +392,7 @@ __device__ __forceinline__ void to_f16(const uint4& x, uint32_t (&h)[4]) {
 // tile (72-byte rows) and of the operand spread over all banks.
 template <int KV>
 struct Chunk {
-  static constexpr bool kBf16 = KV == MSA_KV_BF16, kE4m3 = KV == MSA_KV_FP8_E4M3;
+  static constexpr bool kBf16 = KV == MSA_KV_BF16;
   static constexpr int kOut = kBf16 ? 1 : 2, kChunks = kTileBytes / 16 / kOut / kConvThreads;
   uint4 w;                     // as read (NVFP4: 8 bytes, and the scale)
   int key, c;                  // row, and chunk of the row (of kOut operand chunks)
@@ -396,7 +402,7 @@ struct Chunk {
       key = (x >> 3) & (kBlock - 1);
       c = (x & 7) ^ (key & 7) | (x >> 10) << 3;
       w = *reinterpret_cast<const uint4*>(raw + x * 16);
-    } else if constexpr (kE4m3) {
+    } else if constexpr (KV == MSA_KV_FP8_E4M3) {
       key = (x & 7) | ((x >> 6) << 3);
       c = (x >> 3) & 7;
       w = *reinterpret_cast<const uint4*>(raw + key * 128 + ((c ^ (key & 7)) << 4));
@@ -414,7 +420,7 @@ struct Chunk {
   __device__ __forceinline__ void convert(int k, uint32_t (&h)[4]) const {
     if constexpr (kBf16) {
       to_f16(w, h);
-    } else if constexpr (kE4m3) {
+    } else if constexpr (KV == MSA_KV_FP8_E4M3) {
       const uint32_t u[2] = {k ? w.z : w.x, k ? w.w : w.y};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -884,7 +890,8 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
       bool ovf = false;
       const int first = wk.pair * kPairRows + t * kTile, rows = wk.rows - t * kTile;
       uint8_t* dst = smem + b * kTileBytes;
-      constexpr int kN = kTile * 16 / kConvThreads, kBatch = F::kFp4 ? 4 : 8;
+      constexpr int kN = kTile * 16 / kConvThreads, kBatch = F::kBf16 ? 8 : 4;
+#pragma unroll 1
       for (int i0 = 0; i0 < kN; i0 += kBatch) {                  // a batch's loads in flight
         uint4 v[kBatch];
 #pragma unroll
@@ -921,8 +928,8 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
     };
     while (wk.next(ws, a)) {
       if (!F::kFp4 || keys) {
-        load_q(0, wk.tiles == 2 ? 0 : qsel);
-        if (wk.tiles == 2) load_q(1, 1);
+#pragma unroll 1
+        for (int t = 0; t < wk.tiles; ++t) load_q(t, wk.tiles == 2 ? t : qsel);
       }
       if (wk.tiles == 1) qsel ^= 1;
       if (!keys && ct == 0) sh.bad[(seg + kBads / 2) & (kBads - 1)] = 0;
@@ -1004,7 +1011,7 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
           const uint4* q = reinterpret_cast<const uint4*>(
               a.q + a.q_row(wk.q.t0, wk.h, wk.pair * kPairRows + n) * kHeadDim);
           uint32_t top = 0;
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < 16; ++c) top = __vmaxu2(top, largest(q[c]));
           sc = a.scale_log2 * exp2_of(row_exponent(top));
         }
@@ -1023,7 +1030,7 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
         mbar_wait(&sh.s_ready[wg], (uint32_t)(k >> 1) & 1u, ws.hdr);
         tc_fence_after();
         const bool plain = usable && d >= kBlock;
-        const uint64_t sl = f2(sc, sc), bias = f2(kBias, kBias);
+        const uint64_t sl = f2(sc, sc);
         uint64_t sum0 = 0, sum1 = 0;
         float mx[2];
         auto most = [&](const uint32_t (&x)[kC]) {
@@ -1034,7 +1041,19 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
           }
         };
         uint32_t pk[64];
-        bool good = false;
+        // A row's m, and with it its bits, goes by the row alone: where a warp takes
+        // the slow path for one row, the others keep theirs and compute the same.
+        bool good = false, tried = false, kept = false;
+        if (plain && first) {
+          // a page that begins a row: the maximum of its first columns stands for all
+          uint32_t x[kC];
+          tmem_ld32(ts, x);
+          tmem_wait32(x);
+          mx[0] = mx[1] = -INFINITY;
+          most(x);
+          m = fmaxf(mx[0], mx[1]);
+          fast = __all_sync(0xffffffffu, fabsf(m) * sc < kNear);
+        }
         if (plain && fast) {
           // One pass, with m as it is and -m scale + bias rounded to fp32 (fast: off
           // by less than 2^-18): P stays in registers until its sum says that no
@@ -1079,7 +1098,9 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
           }
           float s0, s1;
           f2_split(add_f2(sum0, sum1), s0, s1);
-          good = __all_sync(0xffffffffu, s0 + s1 < kMaxSum);
+          tried = true;
+          kept = s0 + s1 < kMaxSum;            // (not so for NaN)
+          good = __all_sync(0xffffffffu, kept);
         }
         if (good) {
           tmem_st64(ts, pk);                   // over S
@@ -1098,18 +1119,24 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
             for (int i = 0; i < kC; ++i)
               if (!(vis >> i & 1)) x[i] = 0xff800000u;
           };
-          uint32_t x[kC];
+          uint32_t x[kC], y[kC];
           mx[0] = mx[1] = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < kBlock; c += kC) {
+          for (int c = 0; c < kBlock; c += 2 * kC) {
             tmem_ld32(ts + c, x);
+            tmem_ld32(ts + c + kC, y);
             tmem_wait32(x);
+            tmem_wait32(y);
             see(x, c);
+            see(y, c + kC);
             most(x);
+            most(y);
           }
           const float top = fmaxf(mx[0], mx[1]);
-          if (__any_sync(0xffffffffu, top > m)) {
-            const float mn = fmaxf(m, top);
+          // the difference, exact near m; -inf - -inf is NaN: no move
+          const bool move = tried ? !kept : (top - m) * sc > kSlack;
+          if (__any_sync(0xffffffffu, move)) {
+            const float mn = move ? fmaxf(m, top) : m;
             const float alpha = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sc);
             m = mn;
             l *= alpha;
@@ -1124,26 +1151,29 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
               }
             }
           }
-          // P = 2^((s - m) scale + bias)
-          const float ref = m == -INFINITY ? 0.f : -m;
-          const uint64_t rf = f2(ref, ref);
+          // P = 2^((s - m) scale + bias); m close to 0: as in the one pass
+          const bool near = fabsf(m) * sc < kNear;
+          const float ref = near || m == -INFINITY ? 0.f : -m;
+          const float add = near ? fmaf(-m, sc, kBias) : kBias;
+          const uint64_t rf = f2(ref, ref), ad = f2(add, add);
           sum0 = sum1 = 0;
 #pragma unroll 1
           for (int c = 0; c < kBlock; c += kC) {
             tmem_ld32(ts + c, x);
             tmem_wait32(x);
             see(x, c);
-            uint32_t y[kC / 2];
+            uint32_t p[kC / 2];
 #pragma unroll
             for (int i = 0; i < kC / 2; ++i) {
               float p0, p1;
-              f2_split(fma_f2(add_f2(f2u(x[2 * i], x[2 * i + 1]), rf), sl, bias), p0, p1);
+              f2_split(fma_f2(add_f2(f2u(x[2 * i], x[2 * i + 1]), rf), sl, ad), p0, p1);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
-              sum0 = add_f2(sum0, f2(p0, p1));
-              y[i] = pack_f16(p0, p1);
+              if (i & 1) sum1 = add_f2(sum1, f2(p0, p1));
+              else sum0 = add_f2(sum0, f2(p0, p1));
+              p[i] = pack_f16(p0, p1);
             }
-            tmem_st16(ts + c / 2, y);          // over columns that were read
+            tmem_st16(ts + c / 2, p);          // over columns that were read
           }
         }
         tmem_st_wait();
