@@ -56,6 +56,7 @@
 #include <cfloat>
 
 #include "tcgen05.cuh"
+#include "tree.cuh"
 
 namespace msa {
 namespace {
@@ -73,6 +74,8 @@ struct DenseArgs {
   float scale_log2, v_scale, slack;            // slack: kSlack in unscaled scores
   const __nv_bfloat16* q;
   const uint8_t *k_pool, *v_pool;
+  const int64_t* mask;                         // draft trees: what each token sees of its
+                                               // request's new tokens (NULL: a chain)
   __nv_bfloat16* out;
   float* lse;
   float* o_part;                               // [2 * teams][rows][128]
@@ -413,7 +416,7 @@ struct Shape {
 // Phase parity of the use number t of buffer t & 1.
 __device__ __forceinline__ uint32_t par(int t) { return (uint32_t)(t >> 1) & 1u; }
 
-template <int NG, int TEAMS>
+template <int NG, int TEAMS, bool TREE>
 struct TeamShared {
   using S = Shape<NG, TEAMS>;
   float red[4][S::kN];         // per warp: row maxima, row sums
@@ -427,6 +430,7 @@ struct TeamShared {
   int usable[S::kStages];      // K slots: 0 = the plan flagged the page
   int tok[S::kN];              // token of each row within the request
   unsigned nan[S::kN];         // value blocks that are NaN for the row
+  uint64_t mask[TREE ? S::kN : 1];             // the new tokens that the row sees
 };
 
 template <int N>
@@ -446,13 +450,15 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-template <int NG, int TEAMS>
+// TREE: the new tokens are the nodes of a draft tree; requests of more than q_len of
+// them are another kernel's, which also sees to the tokens of no request.
+template <int NG, int TEAMS, bool TREE>
 __global__ void __launch_bounds__(Shape<NG, TEAMS>::kThreads, 1)
 dense_decode_kernel(WsView ws, DenseArgs a) {
   using S = Shape<NG, TEAMS>;
   constexpr int kN = S::kN, kStages = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(16) TeamShared<NG, TEAMS> shared[S::kTeams];
+  __shared__ __align__(16) TeamShared<NG, TEAMS, TREE> shared[S::kTeams];
   __shared__ uint32_t tmem_base;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
@@ -460,7 +466,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   const int team = extra < 0 ? warp / 4 : (extra < S::kTeams ? extra : extra - S::kTeams);
   const bool keeper = extra == S::kTeams;      // MMA warp 0 keeps the TMEM allocation
   if (tid < S::kTeams) {
-    TeamShared<NG, TEAMS>& st = shared[tid];
+    TeamShared<NG, TEAMS, TREE>& st = shared[tid];
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&st.full_bar[i], 1);
       mbar_init(&st.empty_bar[i], 4);
@@ -490,7 +496,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   constexpr int kDoneCount = S::kTeams * 160;
   if (extra >= 0) regs_down<S::kMiscRegs>();
   if (extra >= 2 * S::kTeams) return;
-  TeamShared<NG, TEAMS>& sh = shared[team];
+  TeamShared<NG, TEAMS, TREE>& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
   // As an argument it stays in a register, which up to three teams have to spare
   // (32 requests of 16384 tokens, 16 rows: 131.6 us, computed here 135.2; verify
@@ -629,7 +635,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     }
     // tokens of no request, and of requests with more tokens than the config's
     const int T = ws.hdr->num_tokens;
-    for (int t = vid; t < T; t += teams) {
+    for (int t = vid; t < T && !TREE; t += teams) {
       const int r = ws.tok_req[t];
       if (r >= 0 && ws.req_qstart[r + 1] - ws.req_qstart[r] <= a.q_len) continue;
       for (int x = lane; x < a.Hq * (kHeadDim / 8); x += 32)
@@ -679,13 +685,17 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   int4 split = make_int4(0, 0, 0, 0);
   for (int seg = 0; any && wk.next(ws, a);) {
     if (wk.nq > a.q_len || wk.nq == 0) {       // more tokens than the config's, or none
-      if (ttid == 0 && wk.nq > 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
+      if (!TREE && ttid == 0 && wk.nq > 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
       continue;
     }
     const int rows = wk.nq * a.G;
     if (ttid < kN) {
       sh.tok[ttid] = min(a.token_of(ttid), wk.nq - 1);
       sh.nan[ttid] = 0u;
+      if constexpr (TREE) {
+        const int i = sh.tok[ttid];
+        sh.mask[ttid] = a.mask ? (uint64_t)a.mask[wk.qs + i] : ~0ull >> (63 - i);
+      }
     }
     named_bar_sync(bar, 128);
 
@@ -700,7 +710,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       // by its MMAs (S^T = K Q^T) while the first half of V is written
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const int ntok = sh.usable[stage] ? wk.L - j * kBlock : 0;   // keys that exist
-      const int all = ntok - wk.nq + 1;                            // and that every row sees
+      const int all = ntok - wk.nq + (TREE ? 0 : 1);               // and that every row sees
       const int kst = stage;
       const uint8_t* kt = ring + kst * kPageBytes + ttid * kFp4Row;
       step();
@@ -727,7 +737,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
             bad |= (vt[ttid * kFp4Row + kHeadDim / 2 + b] & 0x7f) == 0x7f ? 1u << b : 0u;
           if (bad)
             for (int n = 0; n < rows; ++n)
-              if (ttid < all + sh.tok[n]) atomicOr(&sh.nan[n], bad);
+              if (TREE ? sh.mask[TREE ? n : 0] >> (ttid - all) & 1 : ttid < all + sh.tok[n])
+                atomicOr(&sh.nan[n], bad);
         }
       }
       __syncwarp();
@@ -747,8 +758,14 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 #pragma unroll
           for (int e = 0; e < 4 * NG; ++e) {
             const int key = 32 * w + 16 * hf + g + 8 * ((e >> 1) & 1);
-            const int lim = min(ntok, all + sh.tok[8 * (e >> 2) + 2 * c + (e & 1)]);
-            if (key >= lim) x[hf][e] = 0xff800000u;
+            const int n = 8 * (e >> 2) + 2 * c + (e & 1);
+            if constexpr (TREE) {
+              if (key >= ntok || (key >= all && !(sh.mask[n] >> (key - all) & 1)))
+                x[hf][e] = 0xff800000u;
+            } else {
+              const int lim = min(ntok, all + sh.tok[n]);
+              if (key >= lim) x[hf][e] = 0xff800000u;
+            }
           }
       }
       auto xf = [&](int hf, int i, int e) { return __uint_as_float(x[hf][4 * i + e]); };
@@ -1012,14 +1029,14 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
   }
 }
 
-template <int NG, int TEAMS>
+template <int NG, int TEAMS, bool TREE = false>
 msa_status launch_dense(const WsView& v, DenseArgs& a, int64_t units, cudaStream_t s) {
   using S = Shape<NG, TEAMS>;
   static std::atomic<bool> ready[64];          // shared-memory limit raised, per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MSA_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(dense_decode_kernel<NG, TEAMS>,
+    if (cudaFuncSetAttribute(dense_decode_kernel<NG, TEAMS, TREE>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::kSmem) != cudaSuccess)
       return MSA_ERR_CUDA;
@@ -1031,7 +1048,7 @@ msa_status launch_dense(const WsView& v, DenseArgs& a, int64_t units, cudaStream
   if (grid <= 0) return MSA_ERR_CUDA;
   if (grid > units) grid = units;
   const int teams = a.teams = (int)grid * S::kTeams;
-  msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS>, dim3((unsigned)grid),
+  msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS, TREE>, dim3((unsigned)grid),
                              dim3(S::kThreads), S::kSmem, s, v, a);
   if (st != MSA_OK) return st;
   int64_t blocks = (int64_t)teams * ((a.rows + kMergeRows - 1) / kMergeRows);
@@ -1040,21 +1057,70 @@ msa_status launch_dense(const WsView& v, DenseArgs& a, int64_t units, cudaStream
                     teams);
 }
 
+// What both forms of the call share: the config's numbers, the pools and the scratch.
+DenseArgs dense_args(const msa_config& cfg, int q_len, const void* q, const void* k_pages,
+                     const void* v_pages, void* scratch, void* out, float* lse) {
+  DenseArgs a;
+  a.Hkv = cfg.num_kv_heads;
+  a.Hq = cfg.num_q_heads;
+  a.G = a.Hq / a.Hkv;
+  a.q_len = q_len;
+  a.max_blocks = cfg.max_blocks_per_req;
+  a.max_batch = cfg.max_batch;
+  a.rows = a.G * a.q_len;
+  a.scale_log2 = cfg.softmax_scale * cfg.k_scale * kLog2e;
+  a.slack = fminf(kSlack / a.scale_log2, FLT_MAX);
+  a.v_scale = cfg.v_scale;
+  a.q = (const __nv_bfloat16*)q;
+  a.k_pool = (const uint8_t*)k_pages;
+  a.v_pool = (const uint8_t*)v_pages;
+  a.mask = nullptr;
+  a.out = (__nv_bfloat16*)out;
+  a.lse = lse;
+  a.o_part = (float*)scratch;
+  a.g_magic = (65536u + a.G - 1) / a.G;        // exact for rows below 128 and G <= 16
+  a.ml_part = (float2*)((char*)scratch + align_up(2 * (size_t)kTeamsMax * a.rows * kHeadDim * 4));
+  a.split = (int4*)((char*)a.ml_part + align_up(2 * (size_t)kTeamsMax * a.rows * 8));
+  return a;
+}
+
+size_t dense_scratch(int rows) {
+  return align_up(2 * (size_t)kTeamsMax * rows * kHeadDim * 4) +
+         align_up(2 * (size_t)kTeamsMax * rows * 8) + align_up(kTeamsMax * sizeof(int4));
+}
+
 bool dense_supported(const msa_config& c) {
   return !is_prefill(c) && c.kv_dtype == MSA_KV_NVFP4 &&
          (int64_t)c.num_q_heads / c.num_kv_heads * c.q_len <= kMaxRows;
 }
 
 }  // namespace
+
+// Draft trees of up to kTreeDenseRows query rows a KV head over NVFP4 pools
+// (msa_tree_attention): this kernel with the trees' masks.
+size_t tree_dense_scratch(const msa_config& c) {
+  const int G = c.num_q_heads / c.num_kv_heads;
+  return dense_scratch(kTreeDenseRows / G * G);
+}
+
+msa_status tree_dense_attention(const msa_config& c, const WsView& v, const void* q,
+                                const void* k_pages, const void* v_pages, const int64_t* mask,
+                                void* scratch, void* out, float* lse, cudaStream_t s) {
+  static_assert(kTreeDenseRows <= kMaxRows, "rows");
+  DenseArgs a = dense_args(c, kTreeDenseRows / (c.num_q_heads / c.num_kv_heads), q, k_pages,
+                           v_pages, scratch, out, lse);
+  a.mask = mask;
+  // two teams of up to 64 rows: the host does not know the trees' sizes
+  return launch_dense<8, 2, true>(v, a, (int64_t)c.max_batch * c.max_blocks_per_req * a.Hkv, s);
+}
+
 }  // namespace msa
 
 using namespace msa;
 
 extern "C" size_t msa_dense_decode_scratch_bytes(const msa_config* cfg) {
   if (check_config(cfg) != MSA_OK || !dense_supported(*cfg)) return 0;
-  const size_t rows = (size_t)(cfg->num_q_heads / cfg->num_kv_heads) * cfg->q_len;
-  return align_up(2 * (size_t)kTeamsMax * rows * kHeadDim * 4) +
-         align_up(2 * (size_t)kTeamsMax * rows * 8) + align_up(kTeamsMax * sizeof(int4));
+  return dense_scratch(cfg->num_q_heads / cfg->num_kv_heads * cfg->q_len);
 }
 
 extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const void* q,
@@ -1070,27 +1136,9 @@ extern "C" msa_status msa_dense_decode(const msa_config* cfg, void* ws, const vo
     return MSA_ERR_INVALID_ARG;
   const int64_t T = max_tokens_of(*cfg);
   if (T <= 0 || cfg->max_batch == 0) return MSA_OK;
-  DenseArgs a;
-  a.Hkv = cfg->num_kv_heads;
-  a.Hq = cfg->num_q_heads;
-  a.G = a.Hq / a.Hkv;
-  a.q_len = cfg->q_len;
-  a.max_blocks = cfg->max_blocks_per_req;
-  a.max_batch = cfg->max_batch;
-  a.rows = a.G * a.q_len;
-  a.scale_log2 = cfg->softmax_scale * cfg->k_scale * kLog2e;
-  if (!(a.scale_log2 > 0.f && a.scale_log2 < INFINITY)) return MSA_ERR_INVALID_ARG;
-  a.slack = fminf(kSlack / a.scale_log2, FLT_MAX);
-  a.v_scale = cfg->v_scale;
-  a.q = (const __nv_bfloat16*)q;
-  a.k_pool = (const uint8_t*)k_pages;
-  a.v_pool = (const uint8_t*)v_pages;
-  a.out = (__nv_bfloat16*)out;
-  a.lse = lse;
-  a.o_part = (float*)scratch;
-  a.g_magic = (65536u + a.G - 1) / a.G;        // exact for rows below 128 and G <= 16
-  a.ml_part = (float2*)((char*)scratch + align_up(2 * (size_t)kTeamsMax * a.rows * kHeadDim * 4));
-  a.split = (int4*)((char*)a.ml_part + align_up(2 * (size_t)kTeamsMax * a.rows * 8));
+  const float scale_log2 = cfg->softmax_scale * cfg->k_scale * kLog2e;
+  if (!(scale_log2 > 0.f && scale_log2 < INFINITY)) return MSA_ERR_INVALID_ARG;
+  DenseArgs a = dense_args(*cfg, cfg->q_len, q, k_pages, v_pages, scratch, out, lse);
   const WsView v = view_of(*cfg, ws);
   const int64_t units = (int64_t)cfg->max_batch * cfg->max_blocks_per_req * a.Hkv;
   if (units > 0x7fffffff) return MSA_ERR_UNSUPPORTED;   // units are counted in 32 bits

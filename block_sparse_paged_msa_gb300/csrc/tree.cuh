@@ -24,4 +24,12 @@ __device__ __forceinline__ Tree tree_of(const WsView& ws, int r) {
   return t;
 }
 
+// NVFP4 pools: trees of up to that many query rows (nodes x group) a KV head go
+// through the dense decode's kernel (dense_decode.cu).
+constexpr int kTreeDenseRows = 64;
+size_t tree_dense_scratch(const msa_config& c);
+msa_status tree_dense_attention(const msa_config& c, const WsView& v, const void* q,
+                                const void* k_pages, const void* v_pages, const int64_t* mask,
+                                void* scratch, void* out, float* lse, cudaStream_t s);
+
 }  // namespace msa

@@ -32,6 +32,7 @@
 // of a pair of tiles each takes one, of a single tile every second page, whose two
 // results (m, sum, O) are joined at the end of the segment.  While one warpgroup
 // has its softmax, the tensor cores work for the other.
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 
@@ -45,7 +46,7 @@ namespace {
 constexpr int kTile = 128;                     // query rows of an M tile
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kPairRows = 2 * kTile;
-constexpr int kMaxCtas = 320;
+constexpr int kMaxCtas = 192;
 constexpr float kBias = 7.f;                   // exponent offset of the probabilities
 constexpr float kMaxSum = 60000.f;             // a row's sum over a page that fp16 holds
 constexpr float kNear = 64.f;                  // |m| of the fast path, in exponents
@@ -106,8 +107,9 @@ struct Form {
   // 640 x 96 >= 256 x 152 + 256 x 56 + 128 x 56
   static constexpr int kSoftRegs = kFp4 ? 152 : 176, kConvRegs = kFp4 ? 56 : 96,
                        kMiscRegs = kFp4 ? 56 : 64;
-  // weight of a page for a pair of two tiles and of one
-  static constexpr int kW2 = 1, kW1 = 1;
+  // weight of a page for a pair of two tiles and of one, and of a group's beginning and
+  // end (Q, the first S, the last P V, the result)
+  static constexpr int kW2 = 4, kW1 = 3, kHead = 9;
 };
 
 constexpr int at_least(int n) { return n < 1 ? 1 : n; }
@@ -148,7 +150,7 @@ struct Place {
 // Weights.  A request: heads x pairs of tiles x pages.
 struct Req {
   int n, t0, base, L, nb, rows, pairs;
-  uint32_t pw, weight;                         // of a page over all pairs; of the request
+  uint32_t gw, hw, weight;                     // of a group of two tiles; a head; the request
 };
 template <int KV>
 __device__ __forceinline__ Req request(const WsView& ws, const TreeArgs& a, int r) {
@@ -159,12 +161,16 @@ __device__ __forceinline__ Req request(const WsView& ws, const TreeArgs& a, int 
   q.t0 = t.t0;
   q.base = t.base;
   q.L = t.base + t.n;
-  q.nb = t.n > 0 ? (q.L + kBlock - 1) / kBlock : 0;
   q.rows = t.n * a.G;
+  // (small trees over NVFP4 pools are the dense decode's)
+  const bool ours = t.n > 0 && !(F::kFp4 && q.rows <= kTreeDenseRows);
+  q.nb = ours ? (q.L + kBlock - 1) / kBlock : 0;
   const int tiles = (q.rows + kTile - 1) / kTile;
   q.pairs = (tiles + 1) / 2;
-  q.pw = (uint32_t)(tiles / 2 * F::kW2 + (tiles & 1) * F::kW1);
-  q.weight = q.pw * (uint32_t)q.nb * (uint32_t)a.Hkv;
+  q.gw = (uint32_t)(q.nb * F::kW2 + F::kHead);
+  q.hw = q.nb == 0 ? 0
+                   : (uint32_t)(tiles / 2) * q.gw + (tiles & 1) * (uint32_t)(q.nb * F::kW1 + F::kHead);
+  q.weight = q.hw * (uint32_t)a.Hkv;
   return q;
 }
 
@@ -177,7 +183,8 @@ __device__ __forceinline__ uint32_t range_of(uint32_t total, uint32_t ranges, ui
 }
 
 // A role's walk over its CTA's range: one segment per (request, head, pair).  A
-// page belongs to the range in which its weight starts.
+// page belongs to the range in which its weight starts, a group's own weight before
+// its first page.
 template <int KV>
 struct Walk {
   using F = Form<KV>;
@@ -203,17 +210,16 @@ struct Walk {
         wr += q.weight;
         q = request<KV>(ws, a, ++r);
       }
-      const uint32_t hw = q.pw * (uint32_t)q.nb;                 // of a head
       const uint32_t x = w - wr;
-      h = (int)(x / hw);
-      const uint32_t y = x - h * hw, gw = (uint32_t)(F::kW2 * q.nb);
-      pair = min((int)(y / gw), q.pairs - 1);
+      h = (int)(x / q.hw);
+      const uint32_t y = x - h * q.hw;
+      pair = min((int)(y / q.gw), q.pairs - 1);
       rows = min(kPairRows, q.rows - pair * kPairRows);
       tiles = rows > kTile ? 2 : 1;
       const uint32_t step = tiles == 2 ? F::kW2 : F::kW1;
-      const uint32_t g0 = wr + h * hw + pair * gw;               // weight before the group
-      j0 = (int)((w - g0 + step - 1) / step);
-      j1 = (int)min((uint32_t)q.nb, (end - g0 + step - 1) / step);
+      const uint32_t g0 = wr + h * q.hw + pair * q.gw + F::kHead;              // of page 0
+      j0 = w > g0 ? (int)((w - g0 + step - 1) / step) : 0;
+      j1 = end > g0 ? (int)min((uint32_t)q.nb, (end - g0 + step - 1) / step) : 0;
       last = g0 + (q.nb - 1) * step;
       w = g0 + q.nb * step;                    // the next group's start
       if (w > end) w = end;
@@ -249,6 +255,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&r)[64]) {
   asm volatile(
@@ -312,20 +336,14 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint32_t alo, uint32_
 }
 __device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
 
-// Largest magnitudes of the even and of the odd ones of eight bf16 (as their bits),
-// those that are not finite left out.
+// Largest magnitudes of the even and of the odd ones of eight bf16, as their bits.
 __device__ __forceinline__ uint32_t largest(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t m = w[i] & 0x7fff7fffu;
-    top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
-  }
-  return top;
+  return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                  __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
 }
 // The exponent e of a query row's scale from its largest magnitudes: they lie in
-// [2^7, 2^8) of 2^e.  (Not below -107: scales stay normal numbers.)
+// [2^7, 2^8) of 2^e.  (Not below -107: scales stay normal numbers.  A row with an
+// element that is not finite is NaN, whatever its scale.)
 __device__ __forceinline__ int row_exponent(uint32_t top) {
   const int x = (int)max(top & 0xffffu, top >> 16);
   return max((x >> 7) - 127, -100) - 7;
@@ -890,35 +908,39 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
       bool ovf = false;
       const int first = wk.pair * kPairRows + t * kTile, rows = wk.rows - t * kTile;
       uint8_t* dst = smem + b * kTileBytes;
-      constexpr int kN = kTile * 16 / kConvThreads, kBatch = F::kBf16 ? 8 : 4;
-#pragma unroll 1
-      for (int i0 = 0; i0 < kN; i0 += kBatch) {                  // a batch's loads in flight
-        uint4 v[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int x = ct + kConvThreads * (i0 + i), row = x >> 4, ch = x & 15;
-          v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (row < rows)
-            v[i] = *reinterpret_cast<const uint4*>(
-                a.q + a.q_row(wk.q.t0, wk.h, first + row) * kHeadDim + 8 * ch);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int x = ct + kConvThreads * (i0 + i), row = x >> 4, ch = x & 15;
+      // All copies in flight at once, straight to their places as bf16 rows; then, where
+      // the scores are no bf16 products, in place: a warp has two rows at a time, and
+      // the two e4m3 rows of a Q row take the place of its two halves.
+      constexpr int kN = kTile * 16 / kConvThreads;
+#pragma unroll 4
+      for (int i = 0; i < kN; ++i) {
+        const int x = ct + kConvThreads * i, row = x >> 4, ch = x & 15;
+        const bool in = row < rows;
+        cp_async16(smem_u32(dst + kmaj_off(row, ch, kTile)),
+                   a.q + (in ? a.q_row(wk.q.t0, wk.h, first + row) : 0) * kHeadDim + 8 * ch,
+                   in ? 16 : 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      if constexpr (!F::kBf16) {
+        __syncwarp();
+#pragma unroll 2
+        for (int i = 0; i < kN; ++i) {
+          const int x = ct + kConvThreads * i, row = x >> 4, ch = x & 15;
+          uint4* place = reinterpret_cast<uint4*>(dst + kmaj_off(row, ch, kTile));
+          const uint4 v = *place;
           if constexpr (F::kE4m3) {
             uint2 q_hi, q_lo;
-            split_e4m3(v[i], q_hi, q_lo);
+            split_e4m3(v, q_hi, q_lo);
+            __syncwarp();                      // the rows are read
             uint8_t* at = dst + row * 128 + (((ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
             *reinterpret_cast<uint2*>(at) = q_hi;
             *reinterpret_cast<uint2*>(at + kTileBytes / 2) = q_lo;
           } else {
-            if constexpr (F::kFp4) {
-              uint32_t h[4];
-              to_f16(v[i], h);
-              ovf |= any_inf(h);
-              v[i] = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            *reinterpret_cast<uint4*>(dst + kmaj_off(row, ch, kTile)) = v[i];
+            uint32_t h[4];
+            to_f16(v, h);
+            ovf |= any_inf(h);
+            *place = make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
       }
@@ -1193,85 +1215,72 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
       const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.starts ? 1 : 0);
       const int items = pages * wk.tiles, kl = k0 + items - 1;   // the last item, and the one
                                                                  // before it in the other slot
-      auto part = [&](int dim) {               // this row's 4 dims from dim on
-        return a.o_part + ((slot * (kHeadDim / 4) + dim / 4) * a.rows + n) * 4;
-      };
+      float* part = a.o_part + (slot * kHeadDim / 4 * a.rows + n) * 4;       // + dim * rows
       const int64_t out_row = on ? a.q_row(wk.q.t0, wk.h, wk.pair * kPairRows + n) : 0;
-      // 32 dims of the row from dim on
-      auto put = [&](const uint32_t (&o)[32], int dim, float inv) {
-        if (!on) return;
-        if (wk.whole) {
-          __nv_bfloat16* dst = a.out + out_row * kHeadDim + dim;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              h[e] = pack_bf16(__uint_as_float(o[16 * i + 2 * e]) * inv,
-                               __uint_as_float(o[16 * i + 2 * e + 1]) * inv);
-            store32(dst + 16 * i, h, a.out32);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(part(dim + 4 * i)) =
-                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
-      };
-      int dim0 = 0, dims = kHeadDim;           // this thread's part of the row
+      __nv_bfloat16* out = a.out + out_row * kHeadDim;
+      // Two tiles: this warpgroup's O, all dims.  One: both warpgroups' results of a
+      // row, joined, half its dims each.  (A small loop: it runs once a segment, from
+      // a cold instruction cache.)
+      int dim0 = 0, dims = kHeadDim;
+      uint32_t t0 = to, t1 = 0;                // the O's columns; the other O's
+      float f0 = 1.f, f1 = 0.f;
       if (two) {
-        const int mine_l = kl & 1 ? (wg ? kl : kl - 1) : (wg ? kl - 1 : kl);
+        const int mine_l = (kl & 1) == wg ? kl : kl - 1;
         mbar_wait(&sh.o_done[wg], (uint32_t)(mine_l >> 1) & 1u, ws.hdr);
-        tc_fence_after();
-        const float inv = l == 0.f ? 0.f : a.v_scale / l;
-#pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(to + c, o);
-          tmem_wait32(o);
-          put(o, c, inv);
-        }
       } else {
-        // one tile: both warpgroups' results of a row, half its dims each
         sh.ml[wg][row] = make_float2(m, l);
         named_bar_sync(kBar, kCount);
-        const bool both = pages > 1;
         const int wl = kl & 1;                 // the warpgroup of the last item
         mbar_wait(&sh.o_done[wl], (uint32_t)(kl >> 1) & 1u, ws.hdr);
-        if (both) mbar_wait(&sh.o_done[wl ^ 1], (uint32_t)((kl - 1) >> 1) & 1u, ws.hdr);
-        tc_fence_after();
         const float2 ml = sh.ml[wl][row], mo = sh.ml[wl ^ 1][row];
         m = ml.x;
         l = ml.y;
-        float fl = 1.f, fo = 0.f;
-        if (both) {
-          m = fmaxf(ml.x, mo.x);
-          if (m != -INFINITY) {
-            fl = ex2_approx((ml.x - m) * sc);
-            fo = ex2_approx((mo.x - m) * sc);
-          }
-          l = ml.y * fl + mo.y * fo;
-        }
-        const float inv = l == 0.f ? 0.f : a.v_scale / l;
         dim0 = 64 * wg;
         dims = 64;
+        t0 = lanes + 256 + wl * 128;
+        if (pages > 1) {
+          mbar_wait(&sh.o_done[wl ^ 1], (uint32_t)((kl - 1) >> 1) & 1u, ws.hdr);
+          t1 = lanes + 256 + (wl ^ 1) * 128;
+          m = fmaxf(ml.x, mo.x);
+          f1 = 1.f;
+          if (m != -INFINITY) {
+            f0 = ex2_approx((ml.x - m) * sc);
+            f1 = ex2_approx((mo.x - m) * sc);
+          }
+          l = ml.y * f0 + mo.y * f1;
+        }
+      }
+      tc_fence_after();
+      const bool joined = !two && pages > 1;
+      const float inv = !wk.whole ? 1.f : (l == 0.f ? 0.f : a.v_scale / l);
 #pragma unroll 1
-        for (int c = dim0; c < dim0 + 64; c += 32) {
-          uint32_t o[32], q[32];
-          tmem_ld32(lanes + 256 + wl * 128 + c, o);
-          if (both) tmem_ld32(lanes + 256 + (wl ^ 1) * 128 + c, q);
-          tmem_wait32(o);
-          if (both) {
-            tmem_wait32(q);
+      for (int c = dim0; c < dim0 + dims; c += 16) {
+        uint32_t o[16], q[16];
+        tmem_ld16(t0 + c, o);
+        if (joined) tmem_ld16(t1 + c, q);
+        tmem_wait16(o);
+        if (joined) {
+          tmem_wait16(q);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * fl + __uint_as_float(q[i]) * fo);
-          }
-          if (c == dim0 + 32) {                // O and ml may be overwritten from here on
-            tc_fence_before();
-            named_bar_sync(kBar, kCount);
-          }
-          put(o, c, inv);
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + __uint_as_float(q[i]) * f1);
+        }
+        if (!two && c == dim0 + 48) {          // O and ml may be overwritten from here on
+          tc_fence_before();
+          named_bar_sync(kBar, kCount);
+        }
+        if (!on) continue;
+        if (wk.whole) {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            h[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          store32(out + c, h, a.out32);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(part + (int64_t)(c + 4 * i) * a.rows) =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (on && (two || wg == 0)) {
@@ -1291,7 +1300,7 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
             __nv_bfloat16* y = a.out + out_row * kHeadDim + dim;
             *y = __float2bfloat16_rn(__bfloat162float(*y) + v);
           } else {
-            part(dim)[dim & 3] += v;
+            part[(int64_t)(dim & ~3) * a.rows + (dim & 3)] += v;
           }
         }
       }
@@ -1360,12 +1369,15 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
     }
   }
   __syncthreads();
-  const int tiles = (a.rows + 31) / 32, items = n * tiles * 4;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int quarter = item & 3, gi = (item >> 2) / tiles, row0 = ((item >> 2) - gi * tiles) * 32;
+  // the groups of few partials, then the others by quarters of their dims
+  const int tiles = (a.rows + 31) / 32, items = n * tiles;
+  for (int item = blockIdx.x; item < 5 * items; item += gridDim.x) {
+    const bool few = item < items;
+    const int it = few ? item : (item - items) >> 2, quarter = few ? 0 : (item - items) & 3;
+    const int gi = it / tiles, row0 = (it - gi * tiles) * 32;
     const int4 g = list[gi];
     const int rows = g.w & 0xffff, np = g.x, row = row0 + lane;
-    if (row0 >= rows || (np <= kFew && quarter != 0)) continue;  // (the whole block)
+    if (row0 >= rows || few != (np <= kFew)) continue;           // (the whole block)
     const int64_t c0 = owner[gi];
     const bool on = row < rows;
     // partial i: the second slot of c0, the first of c0 + i
@@ -1539,8 +1551,10 @@ using namespace msa;
 extern "C" size_t msa_tree_attention_scratch_bytes(const msa_config* cfg) {
   if (check_config(cfg) != MSA_OK || !tree_supported(*cfg)) return 0;
   const size_t rows = (size_t)part_rows(*cfg);
-  return align_up(2 * (size_t)kMaxCtas * rows * kHeadDim * 4) +
-         align_up(2 * (size_t)kMaxCtas * rows * 8) + align_up(kMaxCtas * sizeof(int4));
+  const size_t n = align_up(2 * (size_t)kMaxCtas * rows * kHeadDim * 4) +
+                   align_up(2 * (size_t)kMaxCtas * rows * 8) + align_up(kMaxCtas * sizeof(int4));
+  // the two kernels of an NVFP4 step run after one another
+  return cfg->kv_dtype == MSA_KV_NVFP4 ? std::max(n, tree_dense_scratch(*cfg)) : n;
 }
 
 extern "C" msa_status msa_tree_attention(const msa_config* cfg, void* ws, const void* q,
@@ -1585,6 +1599,12 @@ extern "C" msa_status msa_tree_attention(const msa_config* cfg, void* ws, const 
   switch (cfg->kv_dtype) {
     case MSA_KV_BF16: return launch_tree<MSA_KV_BF16>(v, a, pool_rows, units, s);
     case MSA_KV_FP8_E4M3: return launch_tree<MSA_KV_FP8_E4M3>(v, a, pool_rows, units, s);
-    default: return launch_tree<MSA_KV_NVFP4>(v, a, pool_rows, units, s);
+    default: break;
   }
+  // NVFP4: the small trees, then the others (either may have none: the host does not
+  // know the trees' sizes)
+  const msa_status st4 =
+      tree_dense_attention(*cfg, v, q, k_pages, v_pages, tree_mask, scratch, out, lse, s);
+  if (st4 != MSA_OK) return st4;
+  return launch_tree<MSA_KV_NVFP4>(v, a, pool_rows, units, s);
 }
