@@ -12,11 +12,11 @@
 //
 // Precision.  A drawn token is a comparison of prefix sums over up to hundreds
 // of thousands of probabilities with a random number: with sums of 24 bits one
-// draw in some tens would take a neighbour.  Weights and their sums per thread
-// are pairs of floats (two-sum, about 48 bits; an fp64 addition has a 60th of
-// the rate here), the few sums of warps fp64.
+// draw in some tens would take a neighbour.  Weights, sums, A and Z are pairs of
+// floats (two-sum, about 47 bits).  fp64 has a 60th of the rate here: with no more
+// than the sums of warps and the walk in it, its pipe was what bounded the kernel.
 //
-// Work split.  A cluster of kC blocks per request: each takes a contiguous part
+// Work split.  A cluster of eight blocks per request: each takes a contiguous part
 // of the vocabulary, its warps contiguous parts of that.  The walk over the tree
 // needs single entries only, fetched for all nodes at once; every block walks by
 // itself.  Sums of warps are written to all blocks of the cluster through
@@ -33,9 +33,10 @@ namespace cg = cooperative_groups;
 namespace msa {
 namespace {
 
-constexpr int kVThreads = 256, kVWarps = kVThreads / 32;
+constexpr int kVThreads = 512, kVWarps = kVThreads / 32;
 constexpr int kMaxC = 8;                       // blocks of a cluster
-constexpr int kMaxParts = kMaxC * kVWarps;     // warps of a cluster
+constexpr int kParts = kMaxC * kVWarps;        // warps of a cluster
+constexpr int kMine = kParts / 32;             // of them a lane looks after
 
 struct VerifyArgs {
   const int32_t *parents, *tokens;
@@ -46,37 +47,59 @@ struct VerifyArgs {
   int32_t *accepted, *num, *out;
 };
 
-// A sum of floats as an unevaluated pair.
+// A number as an unevaluated sum of two floats.
 struct Pair {
   float hi, lo;
-  __device__ __forceinline__ void add(float x) {         // two-sum
+  __device__ __forceinline__ void add(float x) {         // two-sum; lo is left to grow
     const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
     hi = s;
   }
-  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
 };
+__device__ __forceinline__ Pair tidy(float hi, float lo) {         // |lo| to half a step of hi
+  const float s = __fadd_rn(hi, lo);
+  return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  a.add(b.hi);
+  return tidy(a.hi, __fadd_rn(a.lo, b.lo));
+}
+__device__ __forceinline__ Pair operator*(Pair a, float x) {
+  const float h = __fmul_rn(a.hi, x);
+  return tidy(h, __fmaf_rn(a.lo, x, __fmaf_rn(a.hi, x, -h)));
+}
+__device__ __forceinline__ bool operator<(Pair a, Pair b) {
+  return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) < 0.f;
+}
+__device__ __forceinline__ Pair shfl(Pair a, int l) {
+  return {__shfl_sync(0xffffffffu, a.hi, l), __shfl_sync(0xffffffffu, a.lo, l)};
+}
+__device__ __forceinline__ Pair shfl_up(Pair a, int o) {
+  return {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+}
+// The inclusive prefix sums over the lanes.
+__device__ __forceinline__ Pair scan(Pair t, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair y = shfl_up(t, o);
+    if (lane >= o) t = t + y;
+  }
+  return t;
+}
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// max(p - A q, 0) as a pair; A = ah + al.
+// max(p - A q, 0).
 template <bool DRAWN>
-__device__ __forceinline__ void weight(float p, float q, float ah, float al, float& hi, float& lo) {
-  if (!DRAWN) {
-    hi = fmaxf(p, 0.f);
-    if (p != p) hi = p;                        // a NaN shows in the sum
-    lo = 0.f;
-    return;
-  }
-  const float h = __fmul_rn(ah, q), e = __fmaf_rn(ah, q, -h);       // h + e = ah q
+__device__ __forceinline__ Pair weight(float p, float q, Pair A) {
+  if (!DRAWN) return {p != p ? p : fmaxf(p, 0.f), 0.f};              // a NaN shows in the sum
+  const float h = __fmul_rn(A.hi, q), e = __fmaf_rn(A.hi, q, -h);   // h + e = A.hi q
   const float d = __fsub_rn(p, h), b = __fsub_rn(d, p);             // d + f = p - h
   const float f = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(h, b));
-  const float g = __fsub_rn(f, __fmaf_rn(al, q, e));
-  const float s = __fadd_rn(d, g);
-  lo = __fsub_rn(g, __fsub_rn(s, d));
-  hi = s;
-  if (s <= 0.f) hi = lo = 0.f;
+  Pair w = tidy(d, __fsub_rn(f, __fmaf_rn(A.lo, q, e)));
+  if (w.hi <= 0.f) w = {0.f, 0.f};
+  return w;
 }
 
 // Up to V consecutive elements from `at` (V of them where it is 16-byte aligned
@@ -105,17 +128,17 @@ __device__ __forceinline__ void load_vec(const T* row, int64_t at, int vocab, bo
 }
 
 template <typename T, bool DRAWN>
-__global__ void __launch_bounds__(kVThreads) tree_verify_kernel(WsView ws, VerifyArgs a, int C) {
+__global__ void __launch_bounds__(kVThreads) tree_verify_kernel(WsView ws, VerifyArgs a) {
   constexpr int V = 16 / sizeof(T);
-  __shared__ double sums[2][kMaxParts];
+  __shared__ Pair sums[2][kParts];
   __shared__ int par[kTreeNodes], tok[kTreeNodes];
   __shared__ float uni[kTreeNodes], pt[kTreeNodes], qt[kTreeNodes];
   __shared__ unsigned long long kids[kTreeNodes];
   __shared__ int gone[kTreeNodes];             // refused tokens of the last node
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = blockIdx.x / C, rank = blockIdx.x - r * C;
-  const int part = rank * kVWarps + warp, parts = C * kVWarps;
+  const int r = blockIdx.x / kMaxC, rank = blockIdx.x - r * kMaxC;
+  const int part = rank * kVWarps + warp;
   griddep_launch_dependents();
   griddep_wait();
   if (r >= ws.hdr->batch) return;              // (the whole cluster, as below)
@@ -150,18 +173,18 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(WsView ws, Verif
   }
   __syncthreads();
 
-  // A pass over row x: this warp's part of sum w, with A = ah + al, then all
+  // A pass over row x: this warp's part of sum w, then all
   // parts' to all blocks; `buf` alternates.
   int buf = 0;
   const int NVmax = a.vocab / V + 2;           // vectors of a row, its ragged ends included
-  const int per = ((NVmax + parts - 1) / parts + 31) & ~31;      // of a warp, whole rounds
+  const int per = ((NVmax + kParts - 1) / kParts + 31) & ~31;    // of a warp, whole rounds
   auto span = [&](const T* row) { return (int)(((uintptr_t)row / sizeof(T)) & (V - 1)); };
-  auto pass = [&](int x, float ah, float al, int ngone) {
+  auto pass = [&](int x, Pair A, int ngone) {
     const T *p = target(x), *q = DRAWN ? draft(x) : nullptr;
     const int sh = span(p);                    // vector v: elements V v - sh ..
     const bool qa = DRAWN && span(q) == sh;
     Pair s = {0.f, 0.f};
-#pragma unroll 4
+#pragma unroll (DRAWN ? 4 : 8)
     for (int v0 = part * per; v0 < (part + 1) * per; v0 += 32) {
       const int64_t at = (int64_t)(v0 + lane) * V - sh;
       if ((int64_t)v0 * V - sh >= a.vocab) break;
@@ -176,71 +199,64 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(WsView ws, Verif
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float hi, lo;
-        weight<DRAWN>(xp[i], DRAWN ? xq[i] : 0.f, ah, al, hi, lo);
-        s.add(hi);
-        if (DRAWN) s.lo += lo;
+        const Pair w = weight<DRAWN>(xp[i], DRAWN ? xq[i] : 0.f, A);
+        s.add(w.hi);
+        if (DRAWN) s.lo += w.lo;
       }
     }
-    double t = s.value();
+    Pair t = tidy(s.hi, s.lo);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    for (int o = 16; o >= 1; o >>= 1)
+      t = t + Pair{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)};
     buf ^= 1;
-    if (lane < C) *cluster.map_shared_rank(&sums[buf][part], lane) = t;
+    if (lane < kMaxC) *cluster.map_shared_rank(&sums[buf][part], lane) = t;
     cluster.sync();
   };
-  // Inclusive prefix sums of the parts, the same numbers in every warp: this
-  // lane's parts are 2 lane, 2 lane + 1.
-  auto prefix = [&](double& s0, double& s1, double& total) {
-    const double a0 = 2 * lane < parts ? sums[buf][2 * lane] : 0.0;
-    const double a1 = 2 * lane + 1 < parts ? sums[buf][2 * lane + 1] : 0.0;
-    double t = a0 + a1;
+  // Inclusive prefix sums of the parts, the same numbers in every warp: this lane's
+  // are kMine from kMine * lane on.
+  auto prefix = [&](Pair (&s)[kMine], Pair& total) {
+    s[0] = sums[buf][kMine * lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
+    for (int i = 1; i < kMine; ++i) s[i] = s[i - 1] + sums[buf][kMine * lane + i];
+    const Pair inc = scan(s[kMine - 1], lane), before = shfl_up(inc, 1);
+    total = shfl(inc, 31);
+    if (lane > 0) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) s[i] = before + s[i];
     }
-    total = __shfl_sync(0xffffffffu, t, 31);
-    const double before = __shfl_up_sync(0xffffffffu, t, 1);
-    s0 = (lane ? before : 0.0) + a0;
-    s1 = t;
   };
 
   int x = 0, len = 1, ngone = 0;
-  double A = 0.0, Z = 1.0, s0, s1, total = 0.0;
+  Pair A = {0.f, 0.f}, Z = {1.f, 0.f}, s[kMine], total = {0.f, 0.f};
   unsigned long long path = 1;
   bool have = false;                           // sums of the current residual are there
   for (;;) {
     unsigned long long m = kids[x];
     int next = -1;
-    A = 0.0;
-    Z = 1.0;
+    A = {0.f, 0.f};
+    Z = {1.f, 0.f};
     ngone = 0;
     have = false;
     while (m) {
       const int c = __ffsll((long long)m) - 1;
       m &= m - 1;
-      double w;
-      if (DRAWN) {
-        w = fmax((double)pt[c] - A * (double)qt[c], 0.0);
-      } else {
-        w = pt[c];
+      Pair w = weight<DRAWN>(pt[c], qt[c], A);
+      if (!DRAWN) {
         for (int k = 0; k < ngone; ++k)
-          if (gone[k] == tok[c]) w = 0.0;
+          if (gone[k] == tok[c]) w = {0.f, 0.f};
       }
-      if ((double)uni[c] * (double)qt[c] * Z < w) {
+      if (Z * qt[c] * uni[c] < w) {
         next = c;
         break;
       }
       if (DRAWN) {
-        A += Z;
-        const float ah = (float)A;
-        pass(x, ah, (float)(A - (double)ah), 0);
-        prefix(s0, s1, total);
+        A = A + Z;
+        pass(x, A, 0);
+        prefix(s, total);
         Z = total;
         have = true;
       } else {
-        Z -= w;
+        Z = Z + Pair{-w.hi, -w.lo};
         __syncthreads();
         if (tid == 0) gone[ngone] = tok[c];
         ++ngone;
@@ -252,32 +268,47 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(WsView ws, Verif
     path |= 1ull << x;
     ++len;
   }
-  float ah = (float)A, al = (float)(A - (double)ah);
   if (!have) {
-    pass(x, ah, al, ngone);
-    prefix(s0, s1, total);
+    pass(x, A, ngone);
+    prefix(s, total);
   }
-  if (total == 0.0 && (A != 0.0 || ngone > 0)) {                 // nothing left: the target itself
-    ah = al = 0.f;
+  if (total.hi == 0.f && (A.hi != 0.f || ngone > 0)) {           // nothing left: the target itself
+    A = {0.f, 0.f};
     ngone = 0;
-    pass(x, 0.f, 0.f, 0);
-    prefix(s0, s1, total);
+    pass(x, A, 0);
+    prefix(s, total);
   }
-  const bool sound = total > 0.0 && total < INFINITY;
+  const bool sound = total.hi > 0.f && total.hi < INFINITY;
 
   // ---- whose part holds the token, and where in it
-  const double aim = (double)a.uniform_final[r] * total;
-  const unsigned b0 = __ballot_sync(0xffffffffu, s0 > aim && 2 * lane < parts);
-  const unsigned b1 = __ballot_sync(0xffffffffu, s1 > aim && 2 * lane + 1 < parts);
-  int owner = parts;
-  if (b0 | b1) {
-    const int i0 = b0 ? 2 * (__ffs(b0) - 1) : parts, i1 = b1 ? 2 * (__ffs(b1) - 1) + 1 : parts;
-    owner = min(i0, i1);
-  } else {                                     // uniform_final near 1: the last part with weight
-    const unsigned w0 = __ballot_sync(0xffffffffu, 2 * lane < parts && sums[buf][2 * lane] > 0.0);
-    const unsigned w1 =
-        __ballot_sync(0xffffffffu, 2 * lane + 1 < parts && sums[buf][2 * lane + 1] > 0.0);
-    owner = max(w0 ? 2 * (31 - __clz(w0)) : 0, w1 ? 2 * (31 - __clz(w1)) + 1 : 0);
+  const Pair aim = total * a.uniform_final[r];
+  // the first part whose prefix passes the aim; uniform_final near 1: the last one
+  // with weight
+  int mine = kMine, weighty = -1;
+  Pair e0 = {0.f, 0.f};                        // the prefix before that part
+#pragma unroll
+  for (int i = kMine - 1; i >= 0; --i) {
+    if (aim < s[i]) mine = i;
+    if (weighty < 0 && sums[buf][kMine * lane + i].hi > 0.f) weighty = i;
+  }
+  const unsigned past = __ballot_sync(0xffffffffu, mine < kMine);
+  const unsigned any = __ballot_sync(0xffffffffu, weighty >= 0);
+  int owner;
+  if (past) {
+    const int l = __ffs(past) - 1;
+    owner = kMine * l + __shfl_sync(0xffffffffu, mine, l);
+  } else {
+    const int l = any ? 31 - __clz(any) : 0;
+    owner = kMine * l + max(__shfl_sync(0xffffffffu, weighty, l), 0);
+  }
+  {
+    const int before = max(owner - 1, 0);
+    Pair v = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (before % kMine == i) v = s[i];
+    v = shfl(v, before / kMine);
+    if (owner > 0) e0 = v;
   }
   if (rank == 0 && warp == 0) {
     // the path, from the root; its nodes' tokens, then the drawn one
@@ -298,16 +329,14 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(WsView ws, Verif
     }
   }
   if (!sound || part != owner) return;
-  const double e0 = __shfl_sync(0xffffffffu, owner & 1 ? s0 : s1, owner & 1 ? owner / 2
-                                                                             : max(owner / 2 - 1, 0));
-  double run = owner == 0 ? 0.0 : e0;          // sum of the parts before
+  // This warp's part once more, from L2: a lane sums the vectors of a stretch of its
+  // own, then the stretch that holds the token is gone through, a lane a vector at a
+  // time.
   const T *p = target(x), *q = DRAWN ? draft(x) : nullptr;
   const int sh = span(p);
   const bool qa = DRAWN && span(q) == sh;
-  int got = -1, last = -1;
-  for (int v0 = part * per; v0 < (part + 1) * per; v0 += 32) {
-    const int64_t at = (int64_t)(v0 + lane) * V - sh;
-    if ((int64_t)v0 * V - sh >= a.vocab) break;
+  auto weights = [&](int v, Pair (&w)[V], int& top) {          // of vector v; its last weighty
+    const int64_t at = (int64_t)v * V - sh;
     float xp[V], xq[V];
     load_vec<T, V>(p, at, a.vocab, true, xp);
     if (DRAWN) load_vec<T, V>(q, at, a.vocab, qa, xq);
@@ -317,70 +346,82 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(WsView ws, Verif
       for (int i = 0; i < V; ++i)
         if (d == i) xp[i] = 0.f;
     }
-    double w[V], t = 0.0;
-    int top = -1;
+    Pair t = {0.f, 0.f};
+    top = -1;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float hi, lo;
-      weight<DRAWN>(xp[i], DRAWN ? xq[i] : 0.f, ah, al, hi, lo);
-      w[i] = (double)hi + (double)lo;
-      t += w[i];
-      if (hi > 0.f) top = i;
+      w[i] = weight<DRAWN>(xp[i], DRAWN ? xq[i] : 0.f, A);
+      t.add(w[i].hi);
+      t.lo += w[i].lo;
+      if (w[i].hi > 0.f) top = i;
     }
-    double inc = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, run + inc > aim);
-    const unsigned pos = __ballot_sync(0xffffffffu, top >= 0);
-    if (pos) {
-      const int l = 31 - __clz(pos);
-      const int i = __shfl_sync(0xffffffffu, top, l);
-      last = (int)((int64_t)(v0 + l) * V - sh + i);
-    }
+    return tidy(t.hi, t.lo);
+  };
+  const int each = per / 32;                   // vectors of a lane's stretch
+  Pair w[V], t = {0.f, 0.f};
+  int top, last = -1;                          // last: the last vector with weight
+#pragma unroll 4
+  for (int k = 0; k < each; ++k) {
+    const int v = part * per + lane * each + k;
+    t = t + weights(v, w, top);
+    if (top >= 0) last = v;
+  }
+  Pair inc = scan(t, lane);
+  unsigned hit = __ballot_sync(0xffffffffu, aim < e0 + inc);
+  unsigned heavy = __ballot_sync(0xffffffffu, last >= 0);
+  int l = hit ? __ffs(hit) - 1 : (heavy ? 31 - __clz(heavy) : 0);
+  // the sum before stretch l, and its vectors 32 at a time
+  Pair run = shfl(inc, max(l - 1, 0));
+  run = l > 0 ? e0 + run : e0;
+  const int v_last = __shfl_sync(0xffffffffu, last, l);
+  const int v0 = part * per + l * each;
+  int got = -1;
+  for (int k = 0; k < each && got < 0; k += 32) {
+    const bool on = k + lane < each;
+    t = on ? weights(v0 + k + lane, w, top) : Pair{0.f, 0.f};
+    inc = scan(t, lane);
+    hit = __ballot_sync(0xffffffffu, on && aim < run + inc);
     if (hit) {
-      const int l = __ffs(hit) - 1;
-      const double before = __shfl_up_sync(0xffffffffu, inc, 1);
+      const int f = __ffs(hit) - 1;
+      const Pair b = shfl_up(inc, 1);
       int i_hit = -1;
-      if (lane == l) {
-        double c = run + (lane ? before : 0.0);
-        int i = 0;
+      if (lane == f) {
+        Pair c = lane ? run + b : run;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {          // the first that passes; else the last with weight
-          c += w[k];
-          if (i_hit < 0 && c > aim) i_hit = k;
+        for (int i = 0; i < V; ++i) {          // the first that passes; else the last with weight
+          c = c + w[i];
+          if (i_hit < 0 && aim < c) i_hit = i;
         }
-        (void)i;
         if (i_hit < 0) i_hit = top;
       }
-      i_hit = __shfl_sync(0xffffffffu, i_hit, l);
-      got = i_hit >= 0 ? (int)((int64_t)(v0 + l) * V - sh + i_hit) : last;
+      i_hit = __shfl_sync(0xffffffffu, i_hit, f);
+      if (i_hit >= 0) got = (int)((int64_t)(v0 + k + f) * V - sh + i_hit);
       break;
     }
-    run += __shfl_sync(0xffffffffu, inc, 31);
+    run = run + shfl(inc, 31);
   }
-  if (got < 0) got = last;
+  if (got < 0 && v_last >= 0) {                // rounding, or uniform_final near 1
+    weights(v_last, w, top);
+    got = (int)((int64_t)v_last * V - sh + top);
+  }
   if (lane == 0) a.out[(int64_t)r * kTreeNodes + len - 1] = got;
 }
 
 template <typename T, bool DRAWN>
 msa_status launch_verify(const WsView& v, const VerifyArgs& a, int batch, cudaStream_t s) {
-  const int C = kMaxC;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.x = kMaxC;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)batch * C);
+  lc.gridDim = dim3((unsigned)batch * kMaxC);
   lc.blockDim = dim3(kVThreads);
   lc.stream = s;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, tree_verify_kernel<T, DRAWN>, v, a, C) == cudaSuccess
+  return cudaLaunchKernelEx(&lc, tree_verify_kernel<T, DRAWN>, v, a) == cudaSuccess
              ? MSA_OK
              : MSA_ERR_CUDA;
 }
