@@ -63,13 +63,20 @@ tree_plan_kernel(WsView ws, const int32_t* __restrict__ parents, int64_t* __rest
 // ascends, so the row j is read from is never below j: a thread that loads a
 // batch of rows before it stores them, batch after batch, never reads a row that
 // it has overwritten, and no other thread touches its column.
-constexpr int kMoveThreads = 128, kDeep = 8, kMoveLayers = 48, kDistinctLayers = 1024;
+//
+// What bounds it is the chain of dependent loads ahead of a block's rows (header,
+// tree, path, block table: some 2 us) and, for many requests, the rows' traffic in
+// sectors of 32 bytes.  So the grid is one wave of the SMs' resident blocks, a block
+// walks the chain once and then takes one pool after the other.
+constexpr int kMoveThreads = 128, kDeep = 8, kMovePools = 192, kDistinctLayers = 1024;
+constexpr int kMoveBlocks = 16 * 152;          // resident at a time
 
 struct Move {
   int32_t src_page, src_row, dst_page, dst_row;
 };
 struct MoveArgs {
-  void* pool[kMoveLayers * 4];                 // [layer][K, V, index K, index V]
+  void* pool[kMovePools];
+  uint8_t kind[kMovePools];                    // K, V, index K, index V
   int32_t pools, heads, max_blocks;            // pools: of the array
   int32_t bytes[4];                            // of a row of each kind
   int32_t slots[4], first[4];                  // slots of a page and head, the kind's own
@@ -147,8 +154,7 @@ tree_commit_kernel(WsView ws, const __grid_constant__ MoveArgs a,
   const int n = moves;
   for (int p = blockIdx.y; n > 0 && p < a.pools; p += gridDim.y) {
     uint8_t* pool = static_cast<uint8_t*>(a.pool[p]);
-    const int kind = p & 3, bytes = a.bytes[kind];
-    if (pool == nullptr) continue;
+    const int kind = a.kind[p], bytes = a.bytes[kind];
     if (bytes % 16 == 0)
       move_rows<uint4>(pool, mv, n, a.heads, a.slots[kind], a.first[kind], bytes);
     else                                       // NVFP4: 72 bytes
@@ -190,18 +196,18 @@ extern "C" msa_status msa_tree_commit(const msa_config* cfg, void* ws, const int
   for (int32_t l = 0; l < num_layers; ++l)
     for (int k = 0; k < 4; ++k)
       if (kinds[k] && (!kinds[k][l] || !aligned16(kinds[k][l]))) return MSA_ERR_INVALID_ARG;
-  // a pool that stood twice in a list would be moved by two blocks at once
+  // a pool that stood twice in the lists would be moved by two blocks at once; an
+  // NVFP4 pool is its layer's K and its V
   if (num_layers > kDistinctLayers) return MSA_ERR_UNSUPPORTED;
-  for (int k = 0; k < 4; ++k) {
-    if (!kinds[k] || num_layers < 2) continue;
-    void* sorted[kDistinctLayers];
-    std::copy(kinds[k], kinds[k] + num_layers, sorted);
-    std::sort(sorted, sorted + num_layers);
-    if (std::adjacent_find(sorted, sorted + num_layers) != sorted + num_layers)
-      return MSA_ERR_INVALID_ARG;
-  }
-  MoveArgs a;
   const bool fp4 = cfg->kv_dtype == MSA_KV_NVFP4;
+  uintptr_t sorted[4 * kDistinctLayers];
+  int all = 0;
+  for (int k = 0; k < 4; ++k)
+    for (int32_t l = 0; kinds[k] && l < num_layers; ++l)
+      sorted[all++] = (uintptr_t)kinds[k][l] | (fp4 && k == 1 ? 1 : 0);
+  std::sort(sorted, sorted + all);
+  if (std::adjacent_find(sorted, sorted + all) != sorted + all) return MSA_ERR_INVALID_ARG;
+  MoveArgs a;
   const int32_t row = fp4 ? kFp4Row : (cfg->kv_dtype == MSA_KV_BF16 ? 2 * kHeadDim : kHeadDim);
   a.heads = cfg->num_kv_heads;
   a.max_blocks = cfg->max_blocks_per_req;
@@ -210,15 +216,20 @@ extern "C" msa_status msa_tree_commit(const msa_config* cfg, void* ws, const int
     a.slots[k] = k < 2 && fp4 ? 2 : 1;
     a.first[k] = k == 1 && fp4 ? 1 : 0;
   }
-  for (int32_t l0 = 0; l0 < num_layers; l0 += kMoveLayers) {
-    const int32_t n = num_layers - l0 < kMoveLayers ? num_layers - l0 : kMoveLayers;
-    a.pools = 4 * n;
-    for (int32_t l = 0; l < n; ++l)
-      for (int k = 0; k < 4; ++k) a.pool[4 * l + k] = kinds[k] ? kinds[k][l0 + l] : nullptr;
-    const msa_status s2 =
-        launch_pdl(tree_commit_kernel, dim3(cfg->max_batch, a.pools), dim3(kMoveThreads), 0,
-                   (cudaStream_t)stream, view_of(*cfg, ws), a, accepted, num_accepted);
+  a.pools = 0;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    for (int k = 0; k < 4; ++k) {
+      if (!kinds[k]) continue;
+      a.pool[a.pools] = kinds[k][l];
+      a.kind[a.pools++] = (uint8_t)k;
+    }
+    if (a.pools <= kMovePools - 4 && l + 1 < num_layers) continue;
+    const int share = (kMoveBlocks + cfg->max_batch - 1) / cfg->max_batch;
+    const msa_status s2 = launch_pdl(
+        tree_commit_kernel, dim3(cfg->max_batch, a.pools < share ? a.pools : share),
+        dim3(kMoveThreads), 0, (cudaStream_t)stream, view_of(*cfg, ws), a, accepted, num_accepted);
     if (s2 != MSA_OK) return s2;
+    a.pools = 0;
   }
   return MSA_OK;
 }

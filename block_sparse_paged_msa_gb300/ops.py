@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from array import array
 from typing import Optional
 
 import torch
@@ -804,18 +805,21 @@ def tree_commit(cfg, ws, accepted, num_accepted, k_pages, v_pages, idx_k_pages=N
         pools = [pools] if isinstance(pools, _Tensor) else pools
         if n is not None and len(pools) != n:
             raise ValueError(f"{name} has {len(pools)} layers, k_pages has {n}")
-        return (ctypes.c_void_p * len(pools))(*[_expect(p, name, dtypes, shape, dev)
-                                                for p in pools])
+        return array("Q", [_expect(p, name, dtypes, shape, dev) for p in pools])
+
+    def at(pools):                                       # (the array outlives the call)
+        return None if pools is None else pools.buffer_info()[0]
 
     k = pointers(k_pages, "k_pages", y.kv_dtypes, y.pool)
     n = len(k)
+    v = pointers(v_pages, "v_pages", y.kv_dtypes, y.pool, n)
+    idx_k = pointers(idx_k_pages, "idx_k_pages", _BF16, y.idx_pool, n)
+    idx_v = pointers(idx_v_pages, "idx_v_pages", _BF16, y.idx_pool, n)
     st = _call(lib().msa_tree_commit, dev, stream, ctypes.byref(cfg),
                _expect(ws, "ws", _U8, y.ws, dev),
                _expect(accepted, "accepted", _I32, y.paths, dev),
-               _expect(num_accepted, "num_accepted", _I32, y.batch, dev), n, k,
-               pointers(v_pages, "v_pages", y.kv_dtypes, y.pool, n),
-               pointers(idx_k_pages, "idx_k_pages", _BF16, y.idx_pool, n),
-               pointers(idx_v_pages, "idx_v_pages", _BF16, y.idx_pool, n))
+               _expect(num_accepted, "num_accepted", _I32, y.batch, dev), n, at(k), at(v), at(idx_k),
+               at(idx_v))
     if st:
         _check("msa_tree_commit", st)
 
