@@ -80,6 +80,22 @@ def test_commit_refused_on_the_host():
         msa.tree_commit(cfg, None, None, None, [], [])
 
 
+def test_lists_of_pools_that_do_not_fit():
+    """The lists' tensors are checked together where they are alike, else one by
+    one: the same tensors pass, and the others are named."""
+    good = [torch.zeros((3, 2, 4, 8), dtype=torch.bfloat16) for _ in range(5)]
+    more = torch.zeros((4, 2, 4, 8), dtype=torch.bfloat16)
+    args = "pools", (torch.bfloat16, torch.int16), (3, 2, 4, 8), -1
+    for pools in (good, tuple(good), good[:1], good + [more], good + [more.view(torch.int16)]):
+        assert ops._expect_all(pools, *args).tolist() == [x.data_ptr() for x in pools]
+    for bad in (good + [more[:2]], good + [good[0].float()], [good[0].float()], good + [None],
+                [None], ["x"], good + [more.transpose(2, 3)], good + [more[:3, :, :, :4]]):
+        with pytest.raises(ValueError, match="pools"):
+            ops._expect_all(bad, *args)
+    with pytest.raises(ValueError, match="pools"):
+        ops._expect_all(good, *args[:3], 0)
+
+
 # ------------------------------------------------------------ oracle pins (CPU)
 def test_oracle_masks_by_hand():
     #       0
@@ -266,6 +282,23 @@ def test_verify_many_requests(drawn):
     assert msa.check_device_error(d.ws) == 0
     p.check(s, got)
     assert int(got[1].max()) > 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("drawn", [False, True])
+@pytest.mark.parametrize("batch", [37, 39, 75, 79, 200])
+@pytest.mark.parametrize("vocab,dtype,pad", [(5003, torch.float32, 2), (20011, torch.bfloat16, 5),
+                                             (66000, torch.float32, 0)])
+def test_verify_batches_of_every_cluster_size(batch, vocab, dtype, pad, drawn):
+    """Fewer blocks a request take more rounds each, the last ones ragged."""
+    rng = np.random.default_rng(batch)
+    nodes = rng.integers(1, 6, size=batch).tolist()
+    s = Step(8, 1, [n + 5 for n in nodes], nodes, width=2, seed=batch)
+    p = Probs(s, vocab, drawn, dtype, pad, seed=vocab)
+    p.uf[::5] = float(np.nextafter(np.float32(1), np.float32(0)))
+    d, got = p.run(s)
+    assert msa.check_device_error(d.ws) == 0
+    p.check(s, got)
 
 
 @pytest.mark.gpu
