@@ -52,6 +52,7 @@
 // 64 of them a page and warp.  16 requests of 32772 tokens with 4 new ones each
 // (32 rows): 149 us, 4.1 TB/s, against 295 us by mma.sync.  Two requests of
 // 1.5k tokens, one head: 8 us, the chain of one tile and two launches.
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
 
@@ -416,7 +417,7 @@ struct Shape {
 // Phase parity of the use number t of buffer t & 1.
 __device__ __forceinline__ uint32_t par(int t) { return (uint32_t)(t >> 1) & 1u; }
 
-template <int NG, int TEAMS, bool TREE>
+template <int NG, int TEAMS>
 struct TeamShared {
   using S = Shape<NG, TEAMS>;
   float red[4][S::kN];         // per warp: row maxima, row sums
@@ -430,7 +431,6 @@ struct TeamShared {
   int usable[S::kStages];      // K slots: 0 = the plan flagged the page
   int tok[S::kN];              // token of each row within the request
   unsigned nan[S::kN];         // value blocks that are NaN for the row
-  uint64_t mask[TREE ? S::kN : 1];             // the new tokens that the row sees
 };
 
 template <int N>
@@ -450,15 +450,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// TREE: the new tokens are the nodes of a draft tree; requests of more than q_len of
-// them are another kernel's, which also sees to the tokens of no request.
-template <int NG, int TEAMS, bool TREE>
+template <int NG, int TEAMS>
 __global__ void __launch_bounds__(Shape<NG, TEAMS>::kThreads, 1)
 dense_decode_kernel(WsView ws, DenseArgs a) {
   using S = Shape<NG, TEAMS>;
   constexpr int kN = S::kN, kStages = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(16) TeamShared<NG, TEAMS, TREE> shared[S::kTeams];
+  __shared__ __align__(16) TeamShared<NG, TEAMS> shared[S::kTeams];
   __shared__ uint32_t tmem_base;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
@@ -466,7 +464,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   const int team = extra < 0 ? warp / 4 : (extra < S::kTeams ? extra : extra - S::kTeams);
   const bool keeper = extra == S::kTeams;      // MMA warp 0 keeps the TMEM allocation
   if (tid < S::kTeams) {
-    TeamShared<NG, TEAMS, TREE>& st = shared[tid];
+    TeamShared<NG, TEAMS>& st = shared[tid];
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&st.full_bar[i], 1);
       mbar_init(&st.empty_bar[i], 4);
@@ -496,7 +494,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   constexpr int kDoneCount = S::kTeams * 160;
   if (extra >= 0) regs_down<S::kMiscRegs>();
   if (extra >= 2 * S::kTeams) return;
-  TeamShared<NG, TEAMS, TREE>& sh = shared[team];
+  TeamShared<NG, TEAMS>& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
   // As an argument it stays in a register, which up to three teams have to spare
   // (32 requests of 16384 tokens, 16 rows: 131.6 us, computed here 135.2; verify
@@ -635,7 +633,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
     }
     // tokens of no request, and of requests with more tokens than the config's
     const int T = ws.hdr->num_tokens;
-    for (int t = vid; t < T && !TREE; t += teams) {
+    for (int t = vid; t < T; t += teams) {
       const int r = ws.tok_req[t];
       if (r >= 0 && ws.req_qstart[r + 1] - ws.req_qstart[r] <= a.q_len) continue;
       for (int x = lane; x < a.Hq * (kHeadDim / 8); x += 32)
@@ -685,17 +683,13 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   int4 split = make_int4(0, 0, 0, 0);
   for (int seg = 0; any && wk.next(ws, a);) {
     if (wk.nq > a.q_len || wk.nq == 0) {       // more tokens than the config's, or none
-      if (!TREE && ttid == 0 && wk.nq > 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
+      if (ttid == 0 && wk.nq > 0) set_error(ws.hdr, MSA_DEVERR_SEQ_LEN);
       continue;
     }
     const int rows = wk.nq * a.G;
     if (ttid < kN) {
       sh.tok[ttid] = min(a.token_of(ttid), wk.nq - 1);
       sh.nan[ttid] = 0u;
-      if constexpr (TREE) {
-        const int i = sh.tok[ttid];
-        sh.mask[ttid] = a.mask ? (uint64_t)a.mask[wk.qs + i] : ~0ull >> (63 - i);
-      }
     }
     named_bar_sync(bar, 128);
 
@@ -710,7 +704,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       // by its MMAs (S^T = K Q^T) while the first half of V is written
       mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
       const int ntok = sh.usable[stage] ? wk.L - j * kBlock : 0;   // keys that exist
-      const int all = ntok - wk.nq + (TREE ? 0 : 1);               // and that every row sees
+      const int all = ntok - wk.nq + 1;                            // and that every row sees
       const int kst = stage;
       const uint8_t* kt = ring + kst * kPageBytes + ttid * kFp4Row;
       step();
@@ -737,8 +731,7 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
             bad |= (vt[ttid * kFp4Row + kHeadDim / 2 + b] & 0x7f) == 0x7f ? 1u << b : 0u;
           if (bad)
             for (int n = 0; n < rows; ++n)
-              if (TREE ? sh.mask[TREE ? n : 0] >> (ttid - all) & 1 : ttid < all + sh.tok[n])
-                atomicOr(&sh.nan[n], bad);
+              if (ttid < all + sh.tok[n]) atomicOr(&sh.nan[n], bad);
         }
       }
       __syncwarp();
@@ -758,14 +751,8 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 #pragma unroll
           for (int e = 0; e < 4 * NG; ++e) {
             const int key = 32 * w + 16 * hf + g + 8 * ((e >> 1) & 1);
-            const int n = 8 * (e >> 2) + 2 * c + (e & 1);
-            if constexpr (TREE) {
-              if (key >= ntok || (key >= all && !(sh.mask[n] >> (key - all) & 1)))
-                x[hf][e] = 0xff800000u;
-            } else {
-              const int lim = min(ntok, all + sh.tok[n]);
-              if (key >= lim) x[hf][e] = 0xff800000u;
-            }
+            const int lim = min(ntok, all + sh.tok[8 * (e >> 2) + 2 * c + (e & 1)]);
+            if (key >= lim) x[hf][e] = 0xff800000u;
           }
       }
       auto xf = [&](int hf, int i, int e) { return __uint_as_float(x[hf][4 * i + e]); };
@@ -922,6 +909,544 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   named_bar_arrive(kDone, kDoneCount);
 }
 
+// ---------------------------------------------------------------- draft trees
+// Trees of up to 64 query rows a KV head (msa_tree_attention): two teams a CTA as
+// above, whose new tokens see what their masks say.  With 64 rows the softmax of a
+// page costs a warp as much as its dequantisation, and two teams of four warps that do
+// one after the other leave the schedulers idle half the time.  So a team has four
+// warps each for keys, values and the softmax: S of a page is computed while the one
+// before it has its softmax (K has its whole page in TMEM, 64 columns), and its values
+// are converted as soon as P V has read the last ones.
+//
+// What bounds it: the softmax warps' chain of a page, from 5 nodes of 8 heads on; below,
+// the converters'.  32 requests of 8k-32k tokens, 8 KV heads (755 MB), 6 nodes, 48
+// rows: 273 us; 1 node 203, 4 nodes 241, 8 nodes 288.  Measured against it: one group
+// of four warps for everything 317 us (6 nodes); four warps that dequantise and four for
+// the softmax 297; four and twice four, of 32 rows each, 281 (1 node 241).  Unrolling
+// the two halves of a conversion costs 20 us: the roles' loops share the instruction
+// cache.
+struct TreeShape {
+  static constexpr int kNG = 8, kN = 8 * kNG, kTeams = 2;
+  static constexpr int kWarps = 12;                              // of a team: K, V, softmax
+  static constexpr int kThreads = kTeams * kWarps * 32 + 128;    // and loaders, MMA warps
+  // 896 x 72 = 512 x 64 + 256 x 104 + 128 x 40
+  static constexpr int kConvRegs = 64, kSoftRegs = 104, kMiscRegs = 40;
+  static constexpr int kCols = 128 + 2 * kN;                     // TMEM of a team: K | V | S | O
+  static constexpr int kOperand = kN * kHeadDim * 2;             // a Q buffer, and P
+  static constexpr int kStages = (218 * 1024 / kTeams - 3 * kOperand) / kPageBytes;
+  static constexpr int kTeamSmem = 3 * kOperand + kStages * kPageBytes;
+  static constexpr int kSmem = kTeams * kTeamSmem;
+  static_assert(kTeams * kCols <= 512 && kStages % 2 == 0 && kN == kTreeDenseRows, "shape");
+};
+
+// The loader of a team: the pages of a segment 32 at a time (a lane each), one bulk
+// copy per K and V slot; of the last page only the rows that exist.
+template <int kStages, typename Shared>
+__device__ __forceinline__ void load_pages(const WsView& ws, const DenseArgs& a, Shared& sh,
+                                           uint8_t* ring, int vid, int teams, int lane) {
+  Tiles tl;
+  const bool any = tl.open(ws, a, vid, teams, lane);
+  int arms = 0, stage = 0, mine = 0;
+  uint32_t phase = 0;
+  while (any && tl.next<true>(ws, a, lane)) {
+    const Walk& wk = tl.wk;
+    const int at = (tl.j - wk.j0) & 31;
+    if (tl.first)
+      mine = wk.page;
+    else if (at == 0)
+      mine = tl.j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + tl.j + lane] : -1;
+    const int page = __shfl_sync(0xffffffffu, mine, at);
+    const int rows = min(kBlock, wk.L - tl.j * kBlock);
+    const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;         // a multiple of 16
+    const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2;
+    for (int kind = 0; kind < 2; ++kind) {
+      mbar_wait(&sh.empty_bar[stage], phase ^ 1u, ws.hdr);
+      __syncwarp();
+      if (elect_one()) {
+        sh.usable[stage] = page >= 0;
+        if (page >= 0) {
+          mbar_arrive_expect_tx(&sh.full_bar[stage], bytes);
+          bulk_load(ring + stage * kPageBytes,
+                    (kind ? a.v_pool : a.k_pool) + (slot + kind) * kPageBytes, bytes,
+                    &sh.full_bar[stage]);
+        } else {
+          mbar_arrive(&sh.full_bar[stage]);
+        }
+      }
+      __syncwarp();
+      ++arms;
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+    }
+  }
+  // Normally the consumers wait for every copy issued here.  After a wait gave up they
+  // may not have: let the copies in flight land.
+  if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
+    for (int i = 0; i < kStages && i < arms; ++i)
+      mbar_drain(&sh.full_bar[i], (uint32_t)(((arms - 1 - i) / kStages) & 1));
+}
+
+struct TreeShared {
+  using S = TreeShape;
+  float red[4][S::kN], alpha[S::kN], ref[S::kN];
+  uint32_t pairs[4][64];
+  uint64_t full_bar[S::kStages], empty_bar[S::kStages];
+  uint64_t q_free[2];          // Q buffer free again
+  uint64_t k_ready, v_ready;   // written (K: and the segment's Q)
+  uint64_t s_ready, s_free;    // S written, K read; S read
+  uint64_t p_ready, o_ready;   // P written; O updated and P and V read
+  int usable[S::kStages];
+  unsigned nan[S::kN];
+  uint64_t mask[S::kN];        // the nodes that the row sees
+};
+
+__global__ void __launch_bounds__(TreeShape::kThreads, 1)
+dense_tree_kernel(WsView ws, DenseArgs a) {
+  using S = TreeShape;
+  constexpr int kN = S::kN, kNG = S::kNG, kStages = S::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(16) TreeShared shared[S::kTeams];
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);         // uniform
+  const int extra = warp - S::kWarps * S::kTeams;      // loaders, then MMA warps
+  const int team = extra < 0 ? warp / S::kWarps : extra & 1;
+  if (tid < S::kTeams) {
+    TreeShared& st = shared[tid];
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&st.full_bar[i], 1);
+      mbar_init(&st.empty_bar[i], 4);
+    }
+    mbar_init(&st.q_free[0], 4);
+    mbar_init(&st.q_free[1], 4);
+    mbar_init(&st.k_ready, 4);
+    mbar_init(&st.v_ready, 4);
+    mbar_init(&st.s_ready, 1);
+    mbar_init(&st.s_free, 4);
+    mbar_init(&st.p_ready, 4);
+    mbar_init(&st.o_ready, 1);
+    fence_barrier_init();
+  }
+  const bool keeper = extra == S::kTeams;      // MMA warp 0 keeps the TMEM allocation
+  if (keeper) {
+    tmem_alloc(&tmem_base, 512);               // before the wait, as above
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int kDone = 15;                    // named barrier: every consumer and MMA warp
+  constexpr int kDoneCount = S::kTeams * (S::kWarps + 1) * 32;
+  TreeShared& sh = shared[team];
+  const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
+  const int teams = S::kTeams * (int)gridDim.x;
+  uint8_t* qbuf = smem + team * S::kTeamSmem;  // Q x 2 and P: K-major, 128-byte swizzle
+  uint8_t* pbuf = qbuf + 2 * S::kOperand;
+  uint8_t* ring = pbuf + S::kOperand;
+
+  if (extra >= S::kTeams) {
+    // ------------------------------------------------------------------ MMAs
+    // S of a page and P V of the page before it, whichever can go first.
+    regs_down<S::kMiscRegs>();
+    constexpr uint32_t idesc = idesc_f16(0, 128, kN);
+    const uint64_t dq = kstep_desc(smem_u32(qbuf), 0, kN), dp = kstep_desc(smem_u32(pbuf), 0, kN);
+    const uint32_t plo = (uint32_t)dp, hi = (uint32_t)(dq >> 32);
+    Tiles tl;
+    bool more = tl.open(ws, a, vid, teams, lane) && tl.next(ws, a);
+    const uint32_t tk = __shfl_sync(0xffffffffu, tmem_base, 0) + team * S::kCols, tv = tk + 64,
+                   ts = tk + 128, to = ts + kN;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      mbar_wait(bar, parity, ws.hdr);
+      __syncwarp();
+    };
+    auto ready = [&](uint64_t* bar, uint32_t parity) {
+      return __shfl_sync(0xffffffffu, (int)mbar_test_wait(bar, parity), 0) != 0;
+    };
+    auto issue_s = [&](int t) {                // S^T = K Q^T (128 keys x rows)
+      wait(&sh.k_ready, t & 1);
+      if (t > 0) wait(&sh.s_free, (t - 1) & 1);
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t qlo = (uint32_t)dq + (tl.seg & 1) * (S::kOperand >> 4);
+        umma_ts<false>(ts, tk, qlo, hi, idesc);
+#pragma unroll
+        for (int ks = 1; ks < 8; ++ks)
+          umma_ts<true>(ts, tk + 8 * ks, qlo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, hi, idesc);
+        umma_commit(&sh.s_ready);
+      }
+      __syncwarp();
+    };
+    auto issue_o = [&](int t, bool first) {    // O^T += V^T P (128 dims x rows)
+      wait(&sh.p_ready, t & 1);
+      wait(&sh.v_ready, t & 1);
+      tc_fence_after();
+      if (elect_one()) {
+        if (first) umma_ts<false>(to, tv, plo, hi, idesc);
+        else umma_ts<true>(to, tv, plo, hi, idesc);
+#pragma unroll
+        for (int ks = 1; ks < 8; ++ks)
+          umma_ts<true>(to, tv + 8 * ks, plo + (ks >> 2) * (kN * 8) + (ks & 3) * 2, hi, idesc);
+        umma_commit(&sh.o_ready);
+      }
+      __syncwarp();
+    };
+    const bool issued = more;
+    int t = 0;
+    if (more) issue_s(0);
+    for (; more; ++t) {
+      const bool first = tl.first;             // of tile t
+      more = tl.next(ws, a);
+      bool s_first = false;
+      // (all phases before the ones that are asked for are over)
+      for (int i = 0; more && i < (1 << 20); ++i) {
+        if (ready(&sh.k_ready, (t + 1) & 1) && ready(&sh.s_free, t & 1)) {
+          s_first = true;
+          break;
+        }
+        if (ready(&sh.p_ready, t & 1) && ready(&sh.v_ready, t & 1)) break;
+        if ((i & 255) == 255 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
+          break;
+      }
+      if (s_first) issue_s(t + 1);
+      issue_o(t, first);
+      if (more && !s_first) issue_s(t + 1);
+    }
+    // Normally the consumers have waited for the last MMAs.  After a wait gave
+    // up they may not have: let them finish before TMEM goes.
+    if (issued && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
+      mbar_drain(&sh.s_ready, (t - 1) & 1);
+      mbar_drain(&sh.o_ready, (t - 1) & 1);
+    }
+    __syncwarp();
+    if (keeper) {
+      named_bar_sync(kDone, kDoneCount);
+      tc_fence_after();
+      tmem_dealloc(tmem_base, 512);
+    } else {
+      named_bar_arrive(kDone, kDoneCount);
+    }
+    return;
+  }
+
+  if (extra >= 0) {
+    // ---------------------------------------------------------------- loader
+    regs_down<S::kMiscRegs>();
+    load_pages<kStages>(ws, a, sh, ring, vid, teams, lane);
+    return;
+  }
+
+  const int w = warp & 3, ttid = tid & 127;    // within four warps; ttid = key of a tile
+  const uint32_t lanes = (uint32_t)(32 * w) << 16;
+  const uint32_t tk = tmem_base + team * S::kCols + lanes, tv = tk + 64, ts = tk + 128,
+                 to = ts + kN;
+  auto written = [&](uint64_t* bar_) {         // this warp's TMEM accesses are done
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_);
+  };
+  Walk wk;
+  const bool any = wk.open(ws, a, vid, teams, lane);
+
+  const int role = (warp % S::kWarps) >> 2;    // keys, values, softmax
+  if (role < 2) {
+    // ------------------------------------------------------- dequantisation
+    // Keys (and the segment's Q) and values by four warps each; a page's K slot in the
+    // ring is an even one, its V slot the next.
+    regs_down<S::kConvRegs>();
+    int stage = role, t = 0;
+    uint32_t phase = 0;
+    for (int seg = 0; any && wk.next(ws, a);) {
+      if (wk.nq > a.q_len || wk.nq == 0) continue;
+      if (role == 0) {
+        // bf16 -> fp16 rows of the B operand, zero past the last
+        const int rows = wk.nq * a.G, b = seg & 1;
+        if (seg >= 2) mbar_wait(&sh.q_free[b], par(seg - 2), ws.hdr);
+        bool ovf = false;
+#pragma unroll 4
+        for (int x = ttid; x < kN * 16; x += 128) {
+          const int n = x >> 4, ch = x & 15;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (n < rows)
+            v = *reinterpret_cast<const uint4*>(a.q + a.q_row(wk.qs, wk.h, n) * kHeadDim + 8 * ch);
+          v.x = bf16x2_to_f16x2(v.x);
+          v.y = bf16x2_to_f16x2(v.y);
+          v.z = bf16x2_to_f16x2(v.z);
+          v.w = bf16x2_to_f16x2(v.w);
+          ovf |= f16x2_has_inf(v.x) | f16x2_has_inf(v.y) | f16x2_has_inf(v.z) |
+                 f16x2_has_inf(v.w);
+          *reinterpret_cast<uint4*>(qbuf + b * S::kOperand + kmaj_off(n, ch, kN)) = v;
+        }
+        if (__any_sync(0xffffffffu, ovf) && lane == 0) set_error(ws.hdr, MSA_DEVERR_FP16_RANGE);
+        fence_proxy_async_smem();
+      }
+      for (int j = wk.j0; j < wk.j1; ++j, ++t) {
+        mbar_wait(&sh.full_bar[stage], phase, ws.hdr);
+        const int ntok = sh.usable[stage] ? wk.L - j * kBlock : 0;   // keys that exist
+        const uint8_t* slot = ring + stage * kPageBytes;
+        if (t > 0) {                           // the last S has read K, the last P V V
+          mbar_wait(role == 0 ? &sh.s_ready : &sh.o_ready, (t - 1) & 1, ws.hdr);
+          tc_fence_after();
+        }
+        if (role == 0) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) key_half(slot + ttid * kFp4Row, tk + 32 * half, half);
+        } else {
+          const int all = ntok - wk.nq;        // keys that every row sees
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            value_half(slot, tv + 32 * half, half, sh.pairs[w], w, lane, ntok, all);
+            __syncwarp();
+          }
+        }
+        tmem_st_wait();
+        written(role == 0 ? &sh.k_ready : &sh.v_ready);
+        if (lane == 0) mbar_arrive(&sh.empty_bar[stage]);
+        if ((stage += 2) >= kStages) {
+          stage = role;
+          phase ^= 1u;
+        }
+      }
+      ++seg;
+    }
+    named_bar_arrive(kDone, kDoneCount);
+    return;
+  }
+
+  // ---------------------------------------------------------------- softmax
+  // Control flow depends on the plan's data alone (never on what a wait saw),
+  // so that the team's named barriers match even after a wait gave up.
+  regs_up<S::kSoftRegs>();
+  const int g = lane >> 2, c = lane & 3;
+  const int bar = 1 + team;                    // the team's named barrier
+  // this lane's address for the transposed store of P (as above)
+  const int pchunk = 4 * w + (lane >> 3);
+  const uint32_t paddr = smem_u32(pbuf) + (pchunk >> 3) * kN * 128 + (lane & 7) * 128 +
+                         (((pchunk & 7) ^ (lane & 7)) << 4);
+  uint32_t ph = 0, o_phase = 0;                // of the tile's S; of the O to wait for
+  int4 split = make_int4(0, 0, 0, 0);
+  for (int seg = 0; any && wk.next(ws, a);) {
+    if (wk.nq > a.q_len || wk.nq == 0) continue;
+    const int rows = wk.nq * a.G;
+    if (ttid < kN) {
+      const int i = min(a.token_of(ttid), wk.nq - 1);
+      sh.nan[ttid] = 0u;
+      sh.mask[ttid] = a.mask ? (uint64_t)a.mask[wk.qs + i] : ~0ull >> (63 - i);
+    }
+    named_bar_sync(bar, 128);
+
+    float m[kNG][2], l[kNG][2];                // rows 8 i + 2 c + {0, 1}
+#pragma unroll
+    for (int i = 0; i < kNG; ++i) {
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
+    }
+    int mine = -1;
+    for (int j = wk.j0; j < wk.j1; ++j) {
+      const int at = (j - wk.j0) & 31;
+      if (at == 0)
+        mine = j + lane < wk.j1 ? ws.block_table[(int64_t)wk.r * a.max_blocks + j + lane] : -1;
+      const int page = __shfl_sync(0xffffffffu, mine, at);
+      const int ntok = page >= 0 ? wk.L - j * kBlock : 0;
+      const int all = ntok - wk.nq;
+      mbar_wait(&sh.s_ready, ph, ws.hdr);
+      ph ^= 1u;
+      tc_fence_after();
+      if (all < kBlock && ttid >= all && ttid < ntok) {
+        // NaN scales of values that only some nodes see
+        const uint2 sc = *reinterpret_cast<const uint2*>(
+            a.v_pool + ((((int64_t)page * a.Hkv + wk.h) * 2 + 1) * kBlock + ttid) * kFp4Row +
+            kHeadDim / 2);
+        unsigned bad = 0;
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          bad |= ((b < 4 ? sc.x : sc.y) >> (8 * (b & 3)) & 0x7fu) == 0x7fu ? 1u << b : 0u;
+        if (bad)
+          for (int n = 0; n < rows; ++n)
+            if (sh.mask[n] >> (ttid - all) & 1) atomicOr(&sh.nan[n], bad);
+      }
+      // ---- softmax of S^T, 32 rows at a time: 8 keys (16 hf + g, + 8) of rows 8 i + 2 c
+      // + {0, 1}
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        constexpr int kG = kNG / 2;
+        uint32_t x[2][4 * kG];
+        if (half == 0 || rows > 32) {
+          tmem_ld_16x256<kG>(ts + 32 * half, x[0]);
+          tmem_ld_16x256<kG>(ts + 32 * half + (16u << 16), x[1]);
+          tmem_ld_wait();
+        }
+        if (half == 1) written(&sh.s_free);
+        if (half == 1 && rows <= 32) break;
+        if (all < kBlock) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int e = 0; e < 4 * kG; ++e) {
+              const int key = 32 * w + 16 * hf + g + 8 * ((e >> 1) & 1);
+              const int n = 32 * half + 8 * (e >> 2) + 2 * c + (e & 1);
+              if (key >= ntok || (key >= all && !(sh.mask[n] >> (key - all) & 1)))
+                x[hf][e] = 0xff800000u;
+            }
+        }
+        auto xf = [&](int hf, int i, int e) { return __uint_as_float(x[hf][4 * i + e]); };
+        bool move = false;
+        float mx[kG][2];
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mx[i][k] = fmaxf(fmax3(xf(0, i, k), xf(0, i, k + 2), xf(1, i, k)), xf(1, i, k + 2));
+            move |= mx[i][k] - m[kG * half + i][k] > a.slack;    // (as above)
+          }
+        if (half == 0 && j > wk.j0) {          // P V of the last page: P and O are free
+          mbar_wait(&sh.o_ready, o_phase, ws.hdr);
+          o_phase ^= 1u;
+          tc_fence_after();
+        }
+        if (named_bar_any(bar, 128, move)) {
+          // new references: the row maxima over the team's keys
+#pragma unroll
+          for (int i = 0; i < kG; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1)
+                mx[i][k] = fmaxf(mx[i][k], __shfl_xor_sync(0xffffffffu, mx[i][k], o));
+              if (g == 0) sh.red[w][8 * i + 2 * c + k] = mx[i][k];
+            }
+          named_bar_sync(bar, 128);
+#pragma unroll
+          for (int i = 0; i < kG; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int n = 8 * i + 2 * c + k, gi = kG * half + i;
+              const float mn = fmaxf(fmax3(m[gi][k], sh.red[0][n], sh.red[1][n]),
+                                     fmaxf(sh.red[2][n], sh.red[3][n]));
+              const float alpha =
+                  mn == -INFINITY ? 1.f : ex2_approx((m[gi][k] - mn) * a.scale_log2);
+              m[gi][k] = mn;
+              l[gi][k] *= alpha;
+              if (w == 0 && g == 0) sh.alpha[n] = alpha;
+            }
+          named_bar_sync(bar, 128);
+          if (j > wk.j0) {
+#pragma unroll 1
+            for (int n0 = 0; n0 < 32; n0 += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + 32 * half + n0, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * sh.alpha[n0 + e]);
+              tmem_st16(to + 32 * half + n0, o);
+            }
+            tmem_st_wait();
+          }
+          named_bar_sync(bar, 128);            // red and alpha may be overwritten
+        }
+        // ---- P = 2^((s - m) scale + bias) as the B operand [row][key]
+        const uint64_t sl = f2(a.scale_log2, a.scale_log2), bias = f2(kBias, kBias);
+#pragma unroll
+        for (int i = 0; i < kG; ++i) {
+          const int gi = kG * half + i;
+          if (8 * gi >= rows) break;           // (rows past the last have no result)
+          const uint64_t ref = f2(m[gi][0] == -INFINITY ? 0.f : -m[gi][0],
+                                  m[gi][1] == -INFINITY ? 0.f : -m[gi][1]);
+          uint64_t sum = f2(l[gi][0], l[gi][1]);
+          uint32_t p[4];
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {        // keys 8 o + g
+            float p0, p1;
+            const uint64_t s2 =
+                f2u(x[o >> 1][4 * i + 2 * (o & 1)], x[o >> 1][4 * i + 2 * (o & 1) + 1]);
+            f2_split(fma_f2(add_f2(s2, ref), sl, bias), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum = add_f2(sum, f2(p0, p1));
+            p[o] = pack_f16(p0, p1);
+          }
+          f2_split(sum, l[gi][0], l[gi][1]);
+          stsm_x4_t(paddr + gi * 1024, p[0], p[1], p[2], p[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      written(&sh.p_ready);
+    }
+
+    // ---- the segment's result: whole rows, or a partial
+#pragma unroll
+    for (int i = 0; i < kNG; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1)
+          l[i][k] += __shfl_xor_sync(0xffffffffu, l[i][k], o);
+        const int n = 8 * i + 2 * c + k;
+        if (g == 0) sh.red[w][n] = l[i][k];
+        if (w == 0 && g == 0) sh.ref[n] = m[i][k];
+      }
+    mbar_wait(&sh.o_ready, o_phase, ws.hdr);
+    o_phase ^= 1u;
+    tc_fence_after();
+    named_bar_sync(bar, 128);
+    // O^T -> [row][dim] in the segment's Q buffer and in P (S and P V are done)
+    const int dim = 32 * w + 4 * (lane & 7) + (lane >> 3);        // of this thread's TMEM lane
+    uint8_t* qcur = qbuf + (seg & 1) * S::kOperand;
+    auto o_row = [&](int n) {
+      return reinterpret_cast<float*>((n < kN / 2 ? qcur : pbuf) + (n & (kN / 2 - 1)) * 512);
+    };
+#pragma unroll
+    for (int n0 = 0; n0 < 8 * kNG; n0 += 16) {
+      uint32_t o[16];
+      tmem_ld16(to + n0, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (n0 + e < 8 * kNG) o_row(n0 + e)[dim] = __uint_as_float(o[e]);
+    }
+    tc_fence_before();
+    named_bar_sync(bar, 128);
+    const int64_t slot = 2 * vid + (wk.starts ? 1 : 0);
+#pragma unroll 1
+    for (int x = ttid; x < rows * 16; x += 128) {
+      const int n = x >> 4, part = x & 15;     // 8 dims, half a value block
+      const float sum = sh.red[0][n] + sh.red[1][n] + sh.red[2][n] + sh.red[3][n];
+      const float4* src = reinterpret_cast<const float4*>(o_row(n) + 8 * part);
+      float4 y0 = src[0], y1 = src[1];
+      if ((sh.nan[n] >> (part >> 1)) & 1u) y0 = y1 = make_float4(NAN, NAN, NAN, NAN);
+      if (wk.whole) {
+        const int64_t row = a.q_row(wk.qs, wk.h, n);
+        const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+        *reinterpret_cast<uint4*>(a.out + row * kHeadDim + 8 * part) =
+            make_uint4(pack_bf16(y0.x * inv, y0.y * inv), pack_bf16(y0.z * inv, y0.w * inv),
+                       pack_bf16(y1.x * inv, y1.y * inv), pack_bf16(y1.z * inv, y1.w * inv));
+        if (part == 0)
+          a.lse[row] =
+              sum == 0.f ? -INFINITY : (sh.ref[n] * a.scale_log2 + log2f(sum) - kBias) * kLn2;
+      } else {
+        float4* dst =
+            reinterpret_cast<float4*>(a.o_part + (slot * a.rows + n) * kHeadDim + 8 * part);
+        dst[0] = y0;
+        dst[1] = y1;
+        if (part == 0) a.ml_part[slot * a.rows + n] = make_float2(sh.ref[n], sum);
+      }
+    }
+    if (wk.starts && !wk.whole) {              // the range ends inside this group
+      const uint32_t U = (uint32_t)ws.hdr->total_blocks * a.Hkv;
+      const int c1 = (int)Partition(U, min((uint32_t)teams, U)).owner(wk.last);
+      split = make_int4(c1 - vid + 1, wk.qs, wk.h, wk.nq);
+    }
+    fence_proxy_async_smem();                  // P rows are refilled, and so is Q
+    named_bar_sync(bar, 128);                  // red, ref, tok, nan and P are free again
+    if (lane == 0) mbar_arrive(&sh.q_free[seg & 1]);
+    ++seg;
+  }
+  if (ttid == 0) a.split[vid] = split;
+  tc_fence_before();
+  named_bar_arrive(kDone, kDoneCount);
+}
+
 // Merges the partials of the (request, head) groups that lie in several teams'
 // ranges, in team order.  Every block lists the split groups in order, then
 // takes its share of (group, two rows), four warps a row.  Rows of more than
@@ -1029,32 +1554,35 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(DenseArgs a,
   }
 }
 
-template <int NG, int TEAMS, bool TREE = false>
+msa_status launch_merge(const DenseArgs& a, int teams, cudaStream_t s) {
+  int64_t blocks = (int64_t)teams * ((a.rows + kMergeRows - 1) / kMergeRows);
+  if (blocks > 4 * sm_count()) blocks = 4 * sm_count();
+  return launch_pdl(dense_merge_kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a,
+                    teams);
+}
+
+template <int NG, int TEAMS>
 msa_status launch_dense(const WsView& v, DenseArgs& a, int64_t units, cudaStream_t s) {
   using S = Shape<NG, TEAMS>;
   static std::atomic<bool> ready[64];          // shared-memory limit raised, per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MSA_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(dense_decode_kernel<NG, TEAMS, TREE>,
+    if (cudaFuncSetAttribute(dense_decode_kernel<NG, TEAMS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::kSmem) != cudaSuccess)
       return MSA_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
   }
-  const int sms = sm_count();
-  int64_t grid = sms;                          // one CTA an SM
+  int64_t grid = sm_count();                   // one CTA an SM
   if (grid > kTeamsMax / S::kTeams) grid = kTeamsMax / S::kTeams;
   if (grid <= 0) return MSA_ERR_CUDA;
   if (grid > units) grid = units;
   const int teams = a.teams = (int)grid * S::kTeams;
-  msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS, TREE>, dim3((unsigned)grid),
+  msa_status st = launch_pdl(dense_decode_kernel<NG, TEAMS>, dim3((unsigned)grid),
                              dim3(S::kThreads), S::kSmem, s, v, a);
   if (st != MSA_OK) return st;
-  int64_t blocks = (int64_t)teams * ((a.rows + kMergeRows - 1) / kMergeRows);
-  if (blocks > 4 * sms) blocks = 4 * sms;
-  return launch_pdl(dense_merge_kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a,
-                    teams);
+  return launch_merge(a, teams, s);
 }
 
 // What both forms of the call share: the config's numbers, the pools and the scratch.
@@ -1106,12 +1634,28 @@ size_t tree_dense_scratch(const msa_config& c) {
 msa_status tree_dense_attention(const msa_config& c, const WsView& v, const void* q,
                                 const void* k_pages, const void* v_pages, const int64_t* mask,
                                 void* scratch, void* out, float* lse, cudaStream_t s) {
-  static_assert(kTreeDenseRows <= kMaxRows, "rows");
   DenseArgs a = dense_args(c, kTreeDenseRows / (c.num_q_heads / c.num_kv_heads), q, k_pages,
                            v_pages, scratch, out, lse);
   a.mask = mask;
-  // two teams of up to 64 rows: the host does not know the trees' sizes
-  return launch_dense<8, 2, true>(v, a, (int64_t)c.max_batch * c.max_blocks_per_req * a.Hkv, s);
+  using S = TreeShape;
+  static std::atomic<bool> raised[64];         // shared-memory limit, per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MSA_ERR_CUDA;
+  if (!raised[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(dense_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::kSmem) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    raised[dev].store(true, std::memory_order_release);
+  }
+  const int64_t units = (int64_t)c.max_batch * c.max_blocks_per_req * a.Hkv;
+  int64_t grid = std::min<int64_t>(sm_count(), kTeamsMax / S::kTeams);       // one CTA an SM
+  if (grid <= 0) return MSA_ERR_CUDA;
+  grid = std::min(grid, units);
+  const int teams = a.teams = (int)grid * S::kTeams;
+  const msa_status st =
+      launch_pdl(dense_tree_kernel, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, v, a);
+  if (st != MSA_OK) return st;
+  return launch_merge(a, teams, s);
 }
 
 }  // namespace msa
