@@ -492,3 +492,70 @@ def test_either_mode(mode, kv):
     d = s.attend()
     assert msa.check_device_error(d.ws) == 0
     s.check(d)
+
+
+@pytest.mark.gpu
+def test_small_trees_over_nvfp4_in_graphs_and_at_once():
+    """The kernel of small trees: two graphs on one layer's buffers, and two layers
+    on two streams, with trees on both sides of its limit of 64 rows."""
+    steps = [Step(8, 2, lens, nodes, "nvfp4", seed=x, max_blocks=45, extra_pages=e)
+             for x, lens, nodes, e in ((50, [5000, 40, 700, 3], [9, 16, 1, 3], 3),
+                                       (51, [20, 2900, 0, 2801], [17, 4, 0, 8], 3))]
+    want = [s.attend() for s in steps]
+    for s, w in zip(steps, want):
+        assert msa.check_device_error(w.ws) == 0
+        s.check(w)
+    layers, streams = [s.layer() for s in steps], [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, d, st in zip(steps, layers, streams):
+            s.attend(d, stream=st)
+    torch.cuda.synchronize()
+    for d, w in zip(layers, want):
+        assert msa.check_device_error(d.ws) == 0
+        assert torch.equal(d.out, w.out) and torch.equal(d.lse, w.lse)
+    d, graphs = steps[0].layer(), []
+    other = Step(8, 2, [4100, 77, 650, 128], [8, 2, 5, 14], "nvfp4", seed=52, max_blocks=45,
+                 extra_pages=10)
+    pair = [(steps[0], want[0]), (other, other.attend())]
+    assert bytes(steps[0].cfg) == bytes(other.cfg)
+    for s, _ in pair:
+        s.attend(d)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            s.attend(d)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        d.out.fill_(7.0)
+        graphs[i].replay()
+        assert torch.equal(d.out, pair[i][1].out) and torch.equal(d.lse, pair[i][1].lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("group,hkv", [(16, 2), (3, 4), (1, 8)])
+def test_trees_at_the_limit_of_small_ones(kv, group, hkv):
+    """One node fewer than 64 rows a head, exactly, one more; few and many pages."""
+    n = 64 // group
+    nodes = [n, max(n - 1, 1), min(n + 1, 64), 1, n, min(n + 1, 64)]
+    s = Step(group * hkv, hkv, [n, 400, 3000, 1, 6001, 129], nodes, kv, seed=group, width=5)
+    d = s.attend()
+    assert msa.check_device_error(d.ws) == 0
+    s.check(d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", KV)
+def test_sequences_shorter_than_their_trees_are_flagged(kv):
+    s = Step(8, 1, [200, 90, 300], [3, 12, 4], kv, seed=61)
+    want = s.attend()
+    s.seq_lens[1] = 11
+    d = s.attend()
+    assert msa.check_device_error(d.ws) == 2
+    assert bool((d.out[3:15] == 0).all()) and bool(torch.isneginf(d.lse[3:15]).all())
+    for part in (slice(0, 3), slice(15, 19)):
+        tol = 2.0 ** -7 * float(want.out[part].float().abs().max())
+        assert float((d.out[part].float() - want.out[part].float()).abs().max()) <= tol
+    msa.tree_plan(s.cfg, d.ws, s.parents, d.tree_mask, d.positions)
+    assert d.tree_mask[3:15].eq(0).all() and d.positions[3:15].eq(-1).all()
+    assert d.tree_mask[:3].tolist() == s.masks[:3]
