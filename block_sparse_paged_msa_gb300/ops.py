@@ -481,16 +481,18 @@ _dtype_of, _shape_of = attrgetter("dtype"), attrgetter("shape")
 
 
 def _expect_all(pools, name, dtypes, shape, dev) -> array:
-    """_expect() of every tensor of a list: together where they are alike (a step
-    of 96 pools spends its time here, not on the GPU), one by one otherwise."""
+    """_expect() of every tensor of a list: together where they are many and alike
+    (a step of 96 pools spends its time here, not on the GPU: 32 tensors 10.5 us,
+    one by one 12.4; 4 tensors 2.1 and 1.6), else one by one."""
     n = len(pools)
     try:
-        dt, shapes = list(map(_dtype_of, pools)), list(map(_shape_of, pools))
-        if (dt.count(dt[0]) == n and dt[0] in dtypes and shapes.count(shape) == n
-                and list(map(_Tensor.get_device, pools)).count(dev) == n
-                and all(map(_Tensor.is_contiguous, pools))):
-            return array("Q", map(_Tensor.data_ptr, pools))
-    except (AttributeError, IndexError, TypeError):
+        if n >= 8:
+            dt, shapes = list(map(_dtype_of, pools)), list(map(_shape_of, pools))
+            if (dt.count(dt[0]) == n and dt[0] in dtypes and shapes.count(shape) == n
+                    and list(map(_Tensor.get_device, pools)).count(dev) == n
+                    and all(map(_Tensor.is_contiguous, pools))):
+                return array("Q", map(_Tensor.data_ptr, pools))
+    except (AttributeError, TypeError):
         pass                                             # not tensors: _expect() says so
     return array("Q", [_expect(p, name, dtypes, shape, dev) for p in pools])
 

@@ -80,10 +80,11 @@ def test_commit_refused_on_the_host():
         msa.tree_commit(cfg, None, None, None, [], [])
 
 
-def test_lists_of_pools_that_do_not_fit():
+@pytest.mark.parametrize("n", [5, 12])
+def test_lists_of_pools_that_do_not_fit(n):
     """The lists' tensors are checked together where they are alike, else one by
     one: the same tensors pass, and the others are named."""
-    good = [torch.zeros((3, 2, 4, 8), dtype=torch.bfloat16) for _ in range(5)]
+    good = [torch.zeros((3, 2, 4, 8), dtype=torch.bfloat16) for _ in range(n)]
     more = torch.zeros((4, 2, 4, 8), dtype=torch.bfloat16)
     args = "pools", (torch.bfloat16, torch.int16), (3, 2, 4, 8), -1
     for pools in (good, tuple(good), good[:1], good + [more], good + [more.view(torch.int16)]):
