@@ -948,7 +948,8 @@ __device__ __forceinline__ void load_pages(const WsView& ws, const DenseArgs& a,
   const bool any = tl.open(ws, a, vid, teams, lane);
   int arms = 0, stage = 0, mine = 0;
   uint32_t phase = 0;
-  while (any && tl.next<true>(ws, a, lane)) {
+  bool going = true;                           // after a wait gave up nothing more is copied
+  while (going && any && tl.next<true>(ws, a, lane)) {
     const Walk& wk = tl.wk;
     const int at = (tl.j - wk.j0) & 31;
     if (tl.first)
@@ -960,8 +961,8 @@ __device__ __forceinline__ void load_pages(const WsView& ws, const DenseArgs& a,
     const uint32_t bytes = (uint32_t)((rows + 1) & ~1) * kFp4Row;         // a multiple of 16
     const int64_t slot = ((int64_t)page * a.Hkv + wk.h) * 2;
     for (int kind = 0; kind < 2; ++kind) {
-      mbar_wait(&sh.empty_bar[stage], phase ^ 1u, ws.hdr);
-      __syncwarp();
+      going = __all_sync(0xffffffffu, mbar_wait(&sh.empty_bar[stage], phase ^ 1u, ws.hdr));
+      if (!going) break;
       if (elect_one()) {
         sh.usable[stage] = page >= 0;
         if (page >= 0) {
