@@ -24,7 +24,8 @@
 // and in a pass the refused tokens are looked for once in several rounds of loads
 // (compared with every element they cost as much as the sums).  Sums of warps are
 // written to all blocks of the cluster through distributed shared memory, one cluster
-// barrier a pass; the first warp finds whose part holds the drawn token, and that warp
+// barrier a pass, and one before the first (blocks that have not started have no shared
+// memory yet; its latency lies behind the nodes' loads); the first warp finds whose part holds the drawn token, and that warp
 // goes through its part again (from L2) for the token itself.
 //
 // What bounds it.  One request of 4 nodes, 32000 tokens: 6.5 us on the GPU, the chain
@@ -93,6 +94,14 @@ __device__ __forceinline__ Pair scan(Pair t, int lane) {
   return t;
 }
 
+// The two halves of a cluster barrier: every thread of the cluster's blocks, once each.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
@@ -153,11 +162,17 @@ __global__ void __launch_bounds__(kVThreads, 2) tree_verify_kernel(WsView ws, Ve
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = blockIdx.x / kC, rank = blockIdx.x - r * kC;
   const int part = rank * kVWarps + warp;
+  // this block has started: the others may write to its shared memory
+  cluster_arrive();
   griddep_launch_dependents();
   griddep_wait();
-  if (r >= ws.hdr->batch) return;              // (the whole cluster, as below)
+  if (r >= ws.hdr->batch) {                    // (the whole cluster, as below)
+    cluster_wait();
+    return;
+  }
   const Tree tr = tree_of(ws, r);
   if (tr.n == 0) {
+    cluster_wait();
     if (rank == 0) {
       if (tid < kTreeNodes) {
         a.accepted[(int64_t)r * kTreeNodes + tid] = -1;
@@ -192,6 +207,7 @@ __global__ void __launch_bounds__(kVThreads, 2) tree_verify_kernel(WsView ws, Ve
       if (tok[__ffsll((long long)m) - 1] == tok[tid]) pt[tid] = 0.f;
   }
   __syncthreads();
+  cluster_wait();                              // and so have the others
 
   // A row in vectors of 16 bytes, aligned ones: vector v holds elements V v - sh ..;
   // 32 of them, a lane each, are a round, and a part has `per` vectors, whole rounds.

@@ -304,6 +304,33 @@ def test_verify_batches_of_every_cluster_size(batch, vocab, dtype, pad, drawn):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("drawn", [False, True])
+@pytest.mark.parametrize("max_batch", [11, 60, 140])
+def test_verify_among_requests_that_have_nothing_to_verify(max_batch, drawn):
+    """Clusters of every size that leave at once (no request, an idle one, a tree that
+    is too large) beside others that work, again and again."""
+    nodes = [3, 0, 70, 6, 0, 1, 12, 90, 2, 0]
+    lens = [40, 0, 80, 6, 0, 200, 33, 95, 9, 7]
+    s = Step(8, 1, lens, nodes, masks=[1] * sum(nodes), width=2, seed=max_batch,
+             max_batch=max_batch)
+    p = Probs(s, 40009, drawn, pad=3, seed=max_batch + 1)
+    want = None
+    for _ in range(20):
+        d, got = p.run(s)
+        assert msa.check_device_error(d.ws) == 64
+        if want is None:
+            want = [x.clone() for x in got]
+            for r in (1, 2, 4, 7, 9):
+                assert got[1][r] == 0 and bool((got[0][r] == -1).all())
+                assert bool((got[2][r] == -1).all())
+            few = [0 if n > 64 else L for L, n in zip(lens, nodes)]
+            s.lens = few
+            p.check(s, got)
+            s.lens = lens
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("drawn", [False, True])
 def test_the_same_token_drafted_twice(drawn):
     """Given: the second of two equal siblings has nothing left to stand on.
     Drawn: it is tried against what the first left."""
