@@ -1,0 +1,43 @@
+"""The loaders' ring (csrc/load_ring.cuh) on the host, against modelled barriers."""
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from test_sources import CSRC, _code
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def build(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+
+    def make(*flags):
+        exe = str(tmp_path_factory.mktemp("ring") / "ring")
+        subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-I", CSRC, *flags,
+                        os.path.join(HERE, "load_ring.cpp"), "-o", exe], check=True)
+        return subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    return make
+
+
+def test_no_copy_follows_a_wait_that_gave_up(build):
+    p = build()
+    assert p.returncode == 0, p.stdout
+
+
+def test_the_model_shows_a_loader_that_copies_on(build):
+    p = build("-DCARRY_ON")
+    assert p.returncode == 1, (p.returncode, p.stdout)
+
+
+@pytest.mark.parametrize("name", ["dense_decode.cu"])
+def test_loaders_look_at_what_their_waits_say(name):
+    """A wait for a stage to be free is never a statement of its own."""
+    text = _code(os.path.join(CSRC, name))
+    assert re.search(r"\bLoadRing<", text)
+    assert not re.search(r"(^|[;{})])\s*mbar_wait\(&[\w.]*empty", text)
