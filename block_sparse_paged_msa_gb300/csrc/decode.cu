@@ -49,6 +49,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "load_ring.cuh"
 #include "msa_device.cuh"
 
 namespace msa {
@@ -331,6 +332,7 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
       return (int)gridDim.x + __shfl_sync(0xffffffffu, i, 0);
     };
     const int num_tokens = ws.hdr->num_tokens;
+    bool going = true;
     for (int idx = (int)blockIdx.x; idx < a.n_items; idx = grab()) {
       const int tt = idx / (a.nsplit * a.Hkv);
       const SlotRaw raw = slot_raw(a, tt < num_tokens, tt, (idx / a.nsplit) % a.Hkv,
@@ -338,8 +340,12 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
       const Item it = item_of(ws, a, idx, num_tokens);
       if (!it.active) continue;
       const ItemBlocks bl = item_blocks(ws, a, raw, it.r, it.pos, lane);
-      if (lane == 0) mbar_wait(&item_empty[islot], iphase ^ 1u, ws.hdr);
-      __syncwarp();
+      // (after a wait that gave up no record is written and nothing is copied: the others
+      // may still read the slot, and its barriers count one item a phase)
+      int free = 1;
+      if (lane == 0) free = mbar_wait(&item_empty[islot], iphase ^ 1u, ws.hdr);
+      going = __shfl_sync(0xffffffffu, free, 0) != 0;
+      if (!going) break;
       if ((bl.mask >> lane) & 1u) {
         const int p = __popc(bl.mask & ((1u << lane) - 1u));
         meta[islot].ntok[p] = (uint8_t)bl.ntok;
@@ -364,11 +370,12 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
       if (++islot == kItems) { islot = 0; iphase ^= 1u; }
     }
     if (lane == 0) {                                      // end-of-work record
-      mbar_wait(&item_empty[islot], iphase ^ 1u, ws.hdr);
-      meta[islot].t = -1;
-      mbar_arrive(&meta_full[islot]);
-      mbar_arrive(&item_full[islot]);
-      ++nph[islot];
+      if (going && mbar_wait(&item_empty[islot], iphase ^ 1u, ws.hdr)) {
+        meta[islot].t = -1;
+        mbar_arrive(&meta_full[islot]);
+        mbar_arrive(&item_full[islot]);
+        ++nph[islot];
+      }
       if (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT) {
         // a wait gave up: let this warp's Q copies land before the CTA retires
         for (int s2 = 0; s2 < kItems; ++s2)
@@ -388,18 +395,20 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
     // For every published item, the K and V tile of each block as 2-D TMA
     // loads into the stage ring.  Only lane 0 works.
     if (lane == 0) {
-      int stage = 0, islot = 0;
-      uint32_t phase = 0, iphase = 0;
-      int nload = 0;                 // stage arms (one K or V tile each)
-      for (;;) {
-        mbar_wait(&meta_full[islot], iphase, ws.hdr);
-        if (meta[islot].t < 0) break;
+      int islot = 0;
+      uint32_t iphase = 0;
+      LoadRing<NST> lr;              // a K or V tile each
+      while (lr.going) {
+        // (a record that was not published is not read)
+        if (!mbar_wait(&meta_full[islot], iphase, ws.hdr) || meta[islot].t < 0) break;
         const int nblk = meta[islot].nblk, h = meta[islot].h;
-        for (int bi = 0; bi < nblk; ++bi) {
+        for (int bi = 0; lr.going && bi < nblk; ++bi) {
           const int y = (meta[islot].page[bi] * a.Hkv + h) * kBlock;
 #pragma unroll
           for (int kind = 0; kind < 2; ++kind) {
-            mbar_wait(&empty_bar[stage], phase ^ 1u, ws.hdr);
+            if (!lr.free([&](int s, uint32_t par) { return mbar_wait(&empty_bar[s], par, ws.hdr); }))
+              break;
+            const int stage = lr.stage;
             mbar_arrive_expect_tx(&full_bar[stage], TB);
             uint8_t* dst = ring + stage * TB;
             if (KV == kKvFp4) {
@@ -411,19 +420,17 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
               tma_load_2d(dst, tm, 0, y, &full_bar[stage]);
               if (KV == kKvBf16) tma_load_2d(dst + TB / 2, tm, 64, y, &full_bar[stage]);
             }
-            ++nload;
-            if (++stage == NST) { stage = 0; phase ^= 1u; }
+            lr.armed();
           }
         }
-        mbar_arrive(&item_empty[islot]);
+        if (lr.going) mbar_arrive(&item_empty[islot]);
         if (++islot == kItems) { islot = 0; iphase ^= 1u; }
       }
       // Normally the consumers wait for every tile issued here, so no copy is
       // in flight when the CTA retires.  After a wait gave up they may not
       // have: wait (bounded) for the last phase armed on each stage.
       if (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)
-        for (int s2 = 0; s2 < NST && s2 < nload; ++s2)
-          mbar_drain(&full_bar[s2], (uint32_t)(((nload - 1 - s2) / NST) & 1));
+        lr.drain([&](int s, uint32_t par) { mbar_drain(&full_bar[s], par); });
     }
     return;
   }
@@ -434,9 +441,15 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
   uint32_t phase = 0, iphase = 0;
   uint8_t* my_conv = conv + warp * kConvBytes;
   for (;;) {
-    mbar_wait(&item_full[islot], iphase, ws.hdr);
+    // The last record, or a wait that gave up (then the record is not read: it may not
+    // be there): the four warps agree to stop in the named barrier of the item, which
+    // every one of them reaches.
+    const bool there = __all_sync(0xffffffffu, mbar_wait(&item_full[islot], iphase, ws.hdr));
+    if (!there || meta[islot].t < 0) {
+      named_bar_any(1, kConsumers * 32, true);
+      break;
+    }
     const int it_t = meta[islot].t;
-    if (it_t < 0) break;                                  // end-of-work record
     const int it_h = meta[islot].h, it_s = meta[islot].s;
     const int nblk = meta[islot].nblk;
     const int my_ntok = lane < nblk ? meta[islot].ntok[lane] : 0;
@@ -642,7 +655,8 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
       l_r[i] += __shfl_xor_sync(0xffffffffu, l_r[i], 1);
       l_r[i] += __shfl_xor_sync(0xffffffffu, l_r[i], 2);
     }
-    named_bar_sync(1, kConsumers * 32);            // previous item fully written out
+    // previous item fully written out
+    if (named_bar_any(1, kConsumers * 32, false)) break;
     if (tq == 0) {
       red_m[warp][g] = m_r[0];
       red_m[warp][g + 8] = m_r[1];

@@ -259,20 +259,6 @@ __device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r
                "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                : "memory");
 }
-__device__ __forceinline__ void named_bar_arrive(int id, int count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-// Barrier over `count` threads that also tells whether any of them said so.
-__device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
-  int any;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n"
-      " selp.b32 %0, 1, 0, q;\n}"
-      : "=r"(any)
-      : "r"(id), "r"(count), "r"((int)mine)
-      : "memory");
-  return any != 0;
-}
 
 // ---------------------------------------------------------------- dequantisation
 // K: 64 dims (half 0 or 1) of this thread's key row (72 bytes) -> its TMEM

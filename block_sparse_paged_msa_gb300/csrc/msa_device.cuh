@@ -356,6 +356,20 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void named_bar_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+__device__ __forceinline__ void named_bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+// Barrier over `count` threads that also tells whether any of them said so.
+__device__ __forceinline__ bool named_bar_any(int id, int count, bool mine) {
+  int any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n"
+      " selp.b32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"((int)mine)
+      : "memory");
+  return any != 0;
+}
 
 // Address of 16-byte chunk c (0..15) of row `row` in a 128-row tile of 256-byte
 // rows loaded as two 64-column TMA boxes with 128-byte swizzle: columns 0..63

@@ -35,9 +35,25 @@ def test_the_model_shows_a_loader_that_copies_on(build):
     assert p.returncode == 1, (p.returncode, p.stdout)
 
 
-@pytest.mark.parametrize("name", ["dense_decode.cu"])
+@pytest.mark.parametrize("name", ["dense_decode.cu", "decode.cu"])
 def test_loaders_look_at_what_their_waits_say(name):
     """A wait for a stage to be free is never a statement of its own."""
     text = _code(os.path.join(CSRC, name))
     assert re.search(r"\bLoadRing<", text)
     assert not re.search(r"(^|[;{})])\s*mbar_wait\(&[\w.]*empty", text)
+
+
+def _statements(name, barrier):
+    """Waits for a barrier whose answer is dropped."""
+    return re.findall(r"(?:^|[;{})])\s*mbar_wait\(&%s\b" % barrier, _code(os.path.join(CSRC, name)))
+
+
+@pytest.mark.parametrize("name,barrier", [("decode.cu", b) for b in
+                                          ("item_full", "meta_full", "item_empty")])
+def test_records_are_read_after_a_wait_that_succeeded_only(name, barrier):
+    """A record that was not published holds any bytes: pages and rows of them would be
+    addresses outside every buffer, and warps that read different ones would wait for
+    each other in different barriers."""
+    text = _code(os.path.join(CSRC, name))
+    assert re.search(r"mbar_wait\(&%s\b" % barrier, text)
+    assert not _statements(name, barrier)
