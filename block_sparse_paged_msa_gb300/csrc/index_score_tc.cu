@@ -26,6 +26,7 @@
 //    token's position, and reduce the maxima across the block's 128 rows.
 #include <mutex>
 
+#include "load_ring.cuh"
 #include "tcgen05.cuh"
 
 namespace msa {
@@ -97,7 +98,7 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    uint32_t loaded = 0;         // lane 0: stages whose latest item issued copies
+    LoadRing<C::kStages> lr;     // lane 0
     for (int base = 0; base < n_my; base += 32) {
       // lane l resolves this CTA's item base + l
       TcItem mine;
@@ -139,9 +140,10 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
         it.page = __shfl_sync(0xffffffffu, mine.page, l);
 #pragma unroll
         for (int i = 0; i < 4; ++i) it.lim[i] = __shfl_sync(0xffffffffu, mine.lim[i], l);
-        if (lane == 0) {
-          const int k = base + l, s = k % C::kStages;
-          mbar_wait(&empty[s], (uint32_t)(((k / C::kStages) & 1) ^ 1), ws.hdr);
+        if (lane == 0 && lr.free([&](int s, uint32_t par) {
+              return mbar_wait(&empty[s], par, ws.hdr);
+            })) {
+          const int s = lr.stage;
           meta[s] = it;
           if (it.page >= 0) {
             uint8_t* st = smem + s * C::kStage;
@@ -153,12 +155,11 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
               tma_load_3d(st + C::kTile + x * (C::kQTile / C::kHalves), &tmap_q, 64 * x, it.h,
                           it.qs, &full[s]);
             }
-            loaded |= 1u << s;
           } else {
             // a page the plan flagged: nothing to load, the epilogue writes -inf
             mbar_arrive(&full[s]);
-            loaded &= ~(1u << s);
           }
+          lr.armed();
         }
         __syncwarp();
       }
@@ -166,11 +167,7 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
     if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
       // a wait gave up somewhere: let this CTA's copies land before it retires
       // (the last phase of a stage completes once every copy armed on it has)
-      for (int s = 0; s < C::kStages; ++s)
-        if ((loaded >> s) & 1u) {
-          const int last = (n_my - 1 - s) / C::kStages;   // phase of the stage's last item
-          mbar_drain(&full[s], (uint32_t)(last & 1));
-        }
+      lr.drain([&](int s, uint32_t par) { mbar_drain(&full[s], par); });
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -178,10 +175,10 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
       constexpr uint32_t idesc = idesc_f16(1, 128, kQRows);
       for (int k = 0; k < n_my; ++k) {
         const int s = k % C::kStages, b = k & 1;
-        mbar_wait(&full[s], (uint32_t)((k / C::kStages) & 1), ws.hdr);
+        const bool there = mbar_wait(&full[s], (uint32_t)((k / C::kStages) & 1), ws.hdr);
         mbar_wait(&acc_empty[b], (uint32_t)(((k >> 1) & 1) ^ 1), ws.hdr);
         tc_fence_after();
-        if (meta[s].page >= 0) {
+        if (there && meta[s].page >= 0) {
           const uint32_t as = smem_u32(smem + s * C::kStage);
           const uint32_t bs = as + C::kTile;
 #pragma unroll
@@ -208,10 +205,22 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
     const int q = warp & 3;                         // TMEM lanes 32q .. 32q + 31
     const int row = 32 * q + lane;                  // key row of the block
     const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16);
+    bool there = true;
     for (int k = 0; k < n_my; ++k) {
       const int s = k % C::kStages, b = k & 1;
-      mbar_wait(&full[s], (uint32_t)((k / C::kStages) & 1), ws.hdr);   // meta[s] is published
-      const TcItem it = meta[s];
+      // meta[s] is published: after a wait that gave up it may not be, and its bytes would
+      // be rows outside the scores
+      there = there &&
+              __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)((k / C::kStages) & 1), ws.hdr));
+      TcItem it;
+      if (there) {
+        it = meta[s];
+      } else {
+        it.page = -1;
+        it.qs = it.j = it.h = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) it.lim[i] = 0;
+      }
       mbar_wait(&acc_full[b], (uint32_t)((k >> 1) & 1), ws.hdr);
       tc_fence_after();
       uint32_t acc[4];
