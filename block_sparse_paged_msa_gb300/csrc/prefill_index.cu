@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "load_ring.cuh"
 #include "tcgen05.cuh"
 
 namespace msa {
@@ -111,6 +112,8 @@ prefill_index_tc_kernel(WsView ws, IdxArgs a, const __grid_constant__ CUtensorMa
   const int T = ws.hdr->num_tokens;
   const int n_units = a.Hkv * a.NC * a.MT;
   int pairs = 0, units = 0;   // pairs of blocks / units with work, this CTA so far
+  LoadRing<1> ar;             // the producer's: query tiles, pairs of blocks
+  LoadRing<C::kStages> br;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     const int m = u % a.MT, c = (u / a.MT) % a.NC, h = u / (a.MT * a.NC);
     const int t0 = m * kIdxTile;
@@ -124,16 +127,19 @@ prefill_index_tc_kernel(WsView ws, IdxArgs a, const __grid_constant__ CUtensorMa
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
-        if (units > 0) mbar_wait(&a_empty, (uint32_t)((units - 1) & 1), ws.hdr);
-        mbar_arrive_expect_tx(&a_full, C::kATile);
+        if (br.going &&
+            ar.free([&](int, uint32_t par) { return mbar_wait(&a_empty, par, ws.hdr); })) {
+          mbar_arrive_expect_tx(&a_full, C::kATile);
 #pragma unroll
-        for (int x = 0; x < C::kHalves; ++x)
-          tma_load_3d(At + x * (C::kATile / C::kHalves), &tmap_q, 64 * x, h, t0, &a_full);
-        int it = pairs;
+          for (int x = 0; x < C::kHalves; ++x)
+            tma_load_3d(At + x * (C::kATile / C::kHalves), &tmap_q, 64 * x, h, t0, &a_full);
+          ar.armed();
+        }
         for_segments(ws, t0, t1, c, a.kc, [&](int r, int, int, int jb, int je) {
-          for (int j = jb; j < je; j += 2, ++it) {
-            const int s = it % C::kStages;
-            mbar_wait(&empty[s], (uint32_t)(((it / C::kStages) & 1) ^ 1), ws.hdr);
+          for (int j = jb; ar.going && j < je; j += 2) {
+            if (!br.free([&](int s, uint32_t par) { return mbar_wait(&empty[s], par, ws.hdr); }))
+              break;
+            const int s = br.stage;
             const int np = min(2, je - j);
             mbar_arrive_expect_tx(&full[s], (uint32_t)(np * C::kPage));
             uint8_t* st = Bst + s * C::kStage;
@@ -145,6 +151,7 @@ prefill_index_tc_kernel(WsView ws, IdxArgs a, const __grid_constant__ CUtensorMa
                 tma_load_2d(st + x * (C::kStage / C::kHalves) + p * (C::kPage / C::kHalves),
                             &tmap_k, 64 * x, y, &full[s]);
             }
+            br.armed();
           }
         });
       }
@@ -229,6 +236,15 @@ prefill_index_tc_kernel(WsView ws, IdxArgs a, const __grid_constant__ CUtensorMa
     pairs += npairs;
     ++units;
   }
+  // This CTA's copies and MMAs end before it retires.  (The epilogue has waited for them,
+  // unless a wait gave up.)
+  if (lane == 0 && warp == 0) {
+    ar.drain([&](int, uint32_t par) { mbar_drain(&a_full, par); });
+    br.drain([&](int s, uint32_t par) { mbar_drain(&full[s], par); });
+  } else if (lane == 0 && warp == 1 && units > 0) {
+    mbar_drain(&a_empty, (uint32_t)((units - 1) & 1));           // the last commit
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

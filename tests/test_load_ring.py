@@ -35,7 +35,8 @@ def test_the_model_shows_a_loader_that_copies_on(build):
     assert p.returncode == 1, (p.returncode, p.stdout)
 
 
-@pytest.mark.parametrize("name", ["dense_decode.cu", "decode.cu", "index_score_tc.cu"])
+@pytest.mark.parametrize("name", ["dense_decode.cu", "decode.cu", "index_score_tc.cu",
+                                  "prefill_index.cu"])
 def test_loaders_look_at_what_their_waits_say(name):
     """A wait for a stage to be free is never a statement of its own (one for an
     accumulator may be: no copies go there)."""
