@@ -336,8 +336,11 @@ prefill_tc_kernel(WsView ws, PrefillArgs a, const __grid_constant__ CUtensorMap 
   int kW = 0;                                  // warpgroup: tiles done
   int cur_row = -1;
   int n_kload = 0, n_vload = 0;                // issuer: K / V loads issued (drain on exit)
+  bool going = true;                           // issuer: no wait gave up; else nothing more is
+                                               // loaded (the last load may be in flight)
   // K / V tiles of CSR row rw: K into the K tile, V into V buffer `buf`
   auto load_k = [&](int rw) {
+    if (!going) return;
     ++n_kload;
     const int jj = rw % a.NB, rr = (rw / a.NB) % a.B, hh = rw / (a.NB * a.B);
     const int pg = ws.block_table[(int64_t)rr * a.NB + jj];
@@ -349,6 +352,7 @@ prefill_tc_kernel(WsView ws, PrefillArgs a, const __grid_constant__ CUtensorMap 
   };
   // NVFP4: both slots of CSR row rw into the staging area (on v_full)
   auto load_kv4 = [&](int rw) {
+    if (!going) return;
     ++n_vload;
     const int jj = rw % a.NB, rr = (rw / a.NB) % a.B, hh = rw / (a.NB * a.B);
     const int pg = ws.block_table[(int64_t)rr * a.NB + jj];
@@ -362,6 +366,7 @@ prefill_tc_kernel(WsView ws, PrefillArgs a, const __grid_constant__ CUtensorMap 
       load_kv4(rw);
       return;
     }
+    if (!going) return;
     ++n_vload;
     uint8_t* Vst = Vb(buf);
     const int jj = rw % a.NB, rr = (rw / a.NB) % a.B, hh = rw / (a.NB * a.B);
@@ -466,7 +471,9 @@ prefill_tc_kernel(WsView ws, PrefillArgs a, const __grid_constant__ CUtensorMap 
       for (int t = 0; t < ntiles; ++t) {
         const int w = t & 1;
         const int n = w ? kL1 : kL0;
-        if (n > 0) mbar_wait(&s_ready[w], (uint32_t)((n - 1) & 1), ws.hdr);
+        // (not read after a wait that gave up: armed again once its last copies landed)
+        if (n > 0 && !mbar_wait(&s_ready[w], (uint32_t)((n - 1) & 1), ws.hdr))
+          mbar_drain(&q_full[w], (uint32_t)((n - 1) & 1));
         const int e0 = beg + t * TPT;
         if (w) ++kL1; else ++kL0;
         if (G >= 8) {
@@ -525,7 +532,7 @@ prefill_tc_kernel(WsView ws, PrefillArgs a, const __grid_constant__ CUtensorMap 
         const uint32_t klo = (uint32_t)dk, khi = (uint32_t)(dk >> 32);
         const int nrow = next_row(k, row);
         if (new_row && !FP4) {
-          mbar_wait(&k_full, k_phase, ws.hdr);
+          going = mbar_wait(&k_full, k_phase, ws.hdr) && going;
           k_phase ^= 1u;
         }
         bool vt_ok = !new_row;                   // V of this row converted
@@ -607,16 +614,17 @@ prefill_tc_kernel(WsView ws, PrefillArgs a, const __grid_constant__ CUtensorMap 
             spins = 0;
           } else if (++spins > 16u * kWaitLimit) {  // bounded like every other wait
             atomicOr(&ws.hdr->err, MSA_DEVERR_TIMEOUT);
+            going = false;
             break;
           }
         }
         // k_free completes once per item: consume it (and request K if the
         // loop ended first)
-        mbar_wait(&k_free, kf_phase, ws.hdr);
+        going = mbar_wait(&k_free, kf_phase, ws.hdr) && going;
         kf_phase ^= 1u;
         if (!k_done) load_k(nrow);
         if (!vt_ok) {                            // only on a timeout above
-          mbar_wait(&vt_ready, vt_phase, ws.hdr);
+          going = mbar_wait(&vt_ready, vt_phase, ws.hdr) && going;
           vt_phase ^= 1u;
         }
         if (!v_done) load_v(nrow, vsel ^ 1);
@@ -776,24 +784,19 @@ prefill_tc_kernel(WsView ws, PrefillArgs a, const __grid_constant__ CUtensorMap 
     }
   }
   if (warp < 8) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  // Every MMA and copy has been waited for on the normal path.  After a wait
-  // timed out some may still run: the issuer waits for its MMAs, and the
-  // threads that issued TMA loads wait for the last phase they armed on each
-  // barrier of those loads (bounded, no early exit), before the TMEM is freed
-  // and the shared memory released.
+  // Every MMA and copy has been waited for, unless a wait gave up: then some may still
+  // run.  So the issuer waits for its MMAs, and the threads that issued TMA loads wait
+  // for the last phase they armed on each barrier of those loads (bounded, no early
+  // exit), before the TMEM is freed and the shared memory released.
   if (issuer && lane == 0) {
     umma_commit(&k_free);
     mbar_drain(&k_free, kf_phase);
+    if (n_kload > 0) mbar_drain(&k_full, (uint32_t)((n_kload - 1) & 1));
+    if (n_vload > 0) mbar_drain(&v_full, (uint32_t)((n_vload - 1) & 1));
   }
-  if (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT) {
-    if (issuer && lane == 0) {
-      if (n_kload > 0) mbar_drain(&k_full, (uint32_t)((n_kload - 1) & 1));
-      if (n_vload > 0) mbar_drain(&v_full, (uint32_t)((n_vload - 1) & 1));
-    }
-    if (loader && lw == 0 && lane == 0 && G >= 8) {   // the Q boxes (G < 8 copies completed)
-      if (kL0 > 0) mbar_drain(&q_full[0], (uint32_t)((kL0 - 1) & 1));
-      if (kL1 > 0) mbar_drain(&q_full[1], (uint32_t)((kL1 - 1) & 1));
-    }
+  if (loader && lw == 0 && lane == 0 && G >= 8) {     // the Q boxes (G < 8 copies completed)
+    if (kL0 > 0) mbar_drain(&q_full[0], (uint32_t)((kL0 - 1) & 1));
+    if (kL1 > 0) mbar_drain(&q_full[1], (uint32_t)((kL1 - 1) & 1));
   }
   tc_fence_before();
   __syncthreads();

@@ -60,3 +60,18 @@ def test_records_are_read_after_a_wait_that_succeeded_only(name, barrier):
     text = _code(os.path.join(CSRC, name))
     assert re.search(r"mbar_wait\(&%s\b" % barrier, text)
     assert not _statements(name, barrier)
+
+
+def test_the_prefills_issuer_loads_nothing_after_a_wait_that_gave_up():
+    """Its loads are single: each of their functions asks whether a wait gave up, and
+    every wait of the issuer answers."""
+    text = _code(os.path.join(CSRC, "prefill.cu"))
+    for barrier in ("k_full", "k_free", "vt_ready"):
+        assert re.search(r"mbar_wait\(&%s\b" % barrier, text)
+        assert not _statements("prefill.cu", barrier), barrier
+    loads = re.findall(r"\bauto load_\w+ = \[&\]\([^)]*\) \{(.*?)\n  \};", text, flags=re.S)
+    assert len(loads) == 3
+    for body in loads:
+        assert "if (!going) return;" in body[:body.index("mbar_arrive_expect_tx")]
+    # a buffer of queries is armed again once its last copies are there, come what may
+    assert re.search(r"!mbar_wait\(&s_ready\[w\][^;]*?\)\)\s*mbar_drain\(&q_full\[w\]", text)
