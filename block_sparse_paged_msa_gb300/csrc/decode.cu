@@ -323,7 +323,6 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
     int islot = 0;
     uint32_t iphase = 0;
     int nph[kItems] = {0, 0};       // phases armed on item_full[s]
-    int qlast[kItems] = {-1, -1};   // phase of the last Q copy on item_full[s]
     // the first item of every CTA is its own index (no counter round trip at
     // the start); the rest come from the counter, after the first gridDim.x
     auto grab = [&]() {
@@ -365,7 +364,7 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
         bulk_load(qbuf + islot * qbytes,
                   a.q + ((int64_t)it.t * a.Hq + (int64_t)it.h * a.G) * kHeadDim, qbytes,
                   &item_full[islot]);
-        qlast[islot] = nph[islot]++;
+        ++nph[islot];
       }
       if (++islot == kItems) { islot = 0; iphase ^= 1u; }
     }
@@ -376,17 +375,16 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
         mbar_arrive(&item_full[islot]);
         ++nph[islot];
       }
-      if (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT) {
-        // a wait gave up: let this warp's Q copies land before the CTA retires
-        for (int s2 = 0; s2 < kItems; ++s2)
-          if (qlast[s2] >= 0) mbar_drain(&item_full[s2], (uint32_t)(qlast[s2] & 1));
-      }
       // the last CTA to stop taking items resets the counters for the next
       // launch on this workspace
       if (atomicAdd(&ws.hdr->work_done, 1) == (int)gridDim.x - 1) {
         ws.hdr->work_next = 0;
         ws.hdr->work_done = 0;
       }
+      // this warp's Q copies land before the CTA retires (the consumers wait for them
+      // too, unless a wait gave up)
+      for (int s2 = 0; s2 < kItems; ++s2)
+        if (nph[s2] > 0) mbar_drain(&item_full[s2], (uint32_t)((nph[s2] - 1) & 1));
     }
     return;
   }
@@ -426,11 +424,9 @@ decode_kernel(WsView ws, DecodeArgs a, const __grid_constant__ CUtensorMap tmap_
         if (lr.going) mbar_arrive(&item_empty[islot]);
         if (++islot == kItems) { islot = 0; iphase ^= 1u; }
       }
-      // Normally the consumers wait for every tile issued here, so no copy is
-      // in flight when the CTA retires.  After a wait gave up they may not
-      // have: wait (bounded) for the last phase armed on each stage.
-      if (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)
-        lr.drain([&](int s, uint32_t par) { mbar_drain(&full_bar[s], par); });
+      // No copy is in flight when the CTA retires: the consumers wait for every tile
+      // issued here, and where a wait gave up this does (bounded).
+      lr.drain([&](int s, uint32_t par) { mbar_drain(&full_bar[s], par); });
     }
     return;
   }

@@ -477,8 +477,9 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
   tc_fence_after();
   griddep_launch_dependents();                 // (as this one does)
   griddep_wait();
-  constexpr int kDone = 15;                    // named barrier: every consumer and MMA warp
-  constexpr int kDoneCount = S::kTeams * 160;
+  constexpr int kDone = 15;                    // named barrier: consumers, MMA warps, loaders
+  constexpr int kDoneCount = S::kTeams * 192;
+  constexpr int kGone = 14;                    // MMA warps
   if (extra >= 0) regs_down<S::kMiscRegs>();
   if (extra >= 2 * S::kTeams) return;
   TeamShared<NG, TEAMS>& sh = shared[team];
@@ -564,17 +565,17 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
       __syncwarp();
       more = tl.next(ws, a);
     }
-    // Normally the consumers have waited for the last MMAs.  After a wait gave
-    // up they may not have: let them finish before TMEM goes.
-    if (issued && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
-      mbar_drain(&sh.o_ready, ph ^ 1u);
+    named_bar_sync(kDone, kDoneCount);
+    // The consumers have waited for the last MMAs, unless a wait gave up: then these
+    // finish before TMEM goes.
+    if (issued && timed_out(ws.hdr)) mbar_drain(&sh.o_ready, ph ^ 1u);
     __syncwarp();
     if (keeper) {
-      named_bar_sync(kDone, kDoneCount);
+      named_bar_sync(kGone, S::kTeams * 32);
       tc_fence_after();
       tmem_dealloc(tmem_base, 512);
     } else {
-      named_bar_arrive(kDone, kDoneCount);
+      named_bar_arrive(kGone, S::kTeams * 32);
     }
     return;
   }
@@ -629,9 +630,10 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
         reinterpret_cast<uint4*>(a.out + (int64_t)t * a.Hq * kHeadDim)[x] = make_uint4(0, 0, 0, 0);
       for (int x = lane; x < a.Hq; x += 32) a.lse[(int64_t)t * a.Hq + x] = -INFINITY;
     }
-    // Normally the consumers wait for every copy issued here.  After a wait
-    // gave up they may not have: let the copies in flight land.
-    if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
+    named_bar_sync(kDone, kDoneCount);
+    // The consumers have waited for every copy issued here, unless a wait gave up: then
+    // those in flight land before the CTA retires.
+    if (lane == 0 && timed_out(ws.hdr))
       lr.drain([&](int s, uint32_t par) { mbar_drain(&sh.full_bar[s], par); });
     return;
   }
@@ -930,8 +932,9 @@ struct TreeShape {
 // The loader of a team: the pages of a segment 32 at a time (a lane each), one bulk
 // copy per K and V slot; of the last page only the rows that exist.
 template <int kStages, typename Shared>
-__device__ __forceinline__ void load_pages(const WsView& ws, const DenseArgs& a, Shared& sh,
-                                           uint8_t* ring, int vid, int teams, int lane) {
+__device__ __forceinline__ LoadRing<kStages> load_pages(const WsView& ws, const DenseArgs& a,
+                                                        Shared& sh, uint8_t* ring, int vid,
+                                                        int teams, int lane) {
   Tiles tl;
   const bool any = tl.open(ws, a, vid, teams, lane);
   LoadRing<kStages> lr;
@@ -966,10 +969,7 @@ __device__ __forceinline__ void load_pages(const WsView& ws, const DenseArgs& a,
       if (go) lr.armed();
     }
   }
-  // Normally the consumers wait for every copy issued here.  After a wait gave up they
-  // may not have: let the copies in flight land.
-  if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
-    lr.drain([&](int s, uint32_t par) { mbar_drain(&sh.full_bar[s], par); });
+  return lr;
 }
 
 struct TreeShared {
@@ -1023,8 +1023,9 @@ dense_tree_kernel(WsView ws, DenseArgs a) {
   tc_fence_after();
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kDone = 15;                    // named barrier: every consumer and MMA warp
-  constexpr int kDoneCount = S::kTeams * (S::kWarps + 1) * 32;
+  constexpr int kDone = 15;                    // named barrier: consumers, MMA warps, loaders
+  constexpr int kDoneCount = S::kTeams * (S::kWarps + 2) * 32;
+  constexpr int kGone = 14;                    // MMA warps
   TreeShared& sh = shared[team];
   const int vid = team * (int)gridDim.x + (int)blockIdx.x;        // neighbours on other SMs
   const int teams = S::kTeams * (int)gridDim.x;
@@ -1092,26 +1093,26 @@ dense_tree_kernel(WsView ws, DenseArgs a) {
           break;
         }
         if (ready(&sh.p_ready, t & 1) && ready(&sh.v_ready, t & 1)) break;
-        if ((i & 255) == 255 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT))
+        if ((i & 255) == 255 && timed_out(ws.hdr))
           break;
       }
       if (s_first) issue_s(t + 1);
       issue_o(t, first);
       if (more && !s_first) issue_s(t + 1);
     }
-    // Normally the consumers have waited for the last MMAs.  After a wait gave
-    // up they may not have: let them finish before TMEM goes.
-    if (issued && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
+    named_bar_sync(kDone, kDoneCount);
+    // (as above)
+    if (issued && timed_out(ws.hdr)) {
       mbar_drain(&sh.s_ready, (t - 1) & 1);
       mbar_drain(&sh.o_ready, (t - 1) & 1);
     }
     __syncwarp();
     if (keeper) {
-      named_bar_sync(kDone, kDoneCount);
+      named_bar_sync(kGone, S::kTeams * 32);
       tc_fence_after();
       tmem_dealloc(tmem_base, 512);
     } else {
-      named_bar_arrive(kDone, kDoneCount);
+      named_bar_arrive(kGone, S::kTeams * 32);
     }
     return;
   }
@@ -1119,7 +1120,10 @@ dense_tree_kernel(WsView ws, DenseArgs a) {
   if (extra >= 0) {
     // ---------------------------------------------------------------- loader
     regs_down<S::kMiscRegs>();
-    load_pages<kStages>(ws, a, sh, ring, vid, teams, lane);
+    const auto lr = load_pages<kStages>(ws, a, sh, ring, vid, teams, lane);
+    named_bar_sync(kDone, kDoneCount);
+    if (lane == 0 && timed_out(ws.hdr))        // (as above)
+      lr.drain([&](int s, uint32_t par) { mbar_drain(&sh.full_bar[s], par); });
     return;
   }
 

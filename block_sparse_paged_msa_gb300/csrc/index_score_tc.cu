@@ -96,9 +96,9 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
   const int total = ws.hdr->total_blocks * a.Hkv;
   const int n_my = total > (int)blockIdx.x ? (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
 
+  LoadRing<C::kStages> lr;       // of warp 0's lane 0
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    LoadRing<C::kStages> lr;     // lane 0
     for (int base = 0; base < n_my; base += 32) {
       // lane l resolves this CTA's item base + l
       TcItem mine;
@@ -164,11 +164,6 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
         __syncwarp();
       }
     }
-    if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
-      // a wait gave up somewhere: let this CTA's copies land before it retires
-      // (the last phase of a stage completes once every copy armed on it has)
-      lr.drain([&](int s, uint32_t par) { mbar_drain(&full[s], par); });
-    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -191,12 +186,6 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
           mbar_arrive(&empty[s]);
           mbar_arrive(&acc_full[b]);
         }
-      }
-      // the last accumulators are waited for by the epilogue; after a timeout
-      // wait for this thread's MMAs before TMEM is released
-      if (n_my > 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
-        const int k = n_my - 1;
-        mbar_drain(&acc_full[k & 1], (uint32_t)((k >> 1) & 1));
       }
     }
     __syncwarp();
@@ -249,6 +238,17 @@ index_score_tc_kernel(WsView ws, TcArgs a, const __grid_constant__ CUtensorMap t
   }
   tc_fence_before();
   __syncthreads();
+  // The epilogue has waited for every copy and MMA, unless a wait gave up: then this
+  // CTA's own end before it retires.
+  if (lane == 0 && timed_out(ws.hdr)) {
+    if (warp == 0) {
+      lr.drain([&](int s, uint32_t par) { mbar_drain(&full[s], par); });
+    } else if (warp == 1) {
+      for (int k = max(0, n_my - 2); k < n_my; ++k)
+        mbar_drain(&acc_full[k & 1], (uint32_t)((k >> 1) & 1));
+    }
+  }
+  __syncwarp();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, 32);

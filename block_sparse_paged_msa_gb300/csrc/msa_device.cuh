@@ -207,6 +207,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether a wait of this launch (or of an earlier one on the plan) gave up.
+__device__ __forceinline__ bool timed_out(WsHeader* hdr) {
+  return (*reinterpret_cast<volatile int*>(&hdr->err) & MSA_DEVERR_TIMEOUT) != 0;
+}
+
 // Wait for the phase of `bar` with the given parity; false on timeout (after
 // kLimit polls, recorded as MSA_DEVERR_TIMEOUT in the error word).  Once any
 // waiter has timed out (the error word says so), every other wait gives up
@@ -215,9 +220,7 @@ template <uint32_t kLimit = kWaitLimit>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, WsHeader* hdr) {
   for (uint32_t i = 0; i < kLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u &&
-        (*reinterpret_cast<volatile int*>(&hdr->err) & MSA_DEVERR_TIMEOUT))
-      return false;
+    if ((i & 255u) == 255u && timed_out(hdr)) return false;
   }
   atomicOr(&hdr->err, MSA_DEVERR_TIMEOUT);
   return false;

@@ -721,9 +721,9 @@ tree_attention_kernel(WsView ws, TreeArgs a, const __grid_constant__ CUtensorMap
           ++vals;
         }
       }
-      // Normally the converters and the MMAs wait for every copy issued here.
-      // After a wait gave up they may not have: let the copies in flight land.
-      if (lane == 0 && (*reinterpret_cast<volatile int*>(&ws.hdr->err) & MSA_DEVERR_TIMEOUT)) {
+      // The copies land before the CTA retires (the converters and the MMAs wait for them
+      // too, unless a wait gave up).
+      if (lane == 0) {
         auto drain = [&](uint64_t* bars, int n, int b, uint32_t par, int arms) {
           for (int i = 0; i < n; ++i)          // its last use: of this round before b, else the last
             if (i < arms) mbar_drain(&bars[i], i < b ? par : par ^ 1u);

@@ -75,3 +75,19 @@ def test_the_prefills_issuer_loads_nothing_after_a_wait_that_gave_up():
         assert "if (!going) return;" in body[:body.index("mbar_arrive_expect_tx")]
     # a buffer of queries is armed again once its last copies are there, come what may
     assert re.search(r"!mbar_wait\(&s_ready\[w\][^;]*?\)\)\s*mbar_drain\(&q_full\[w\]", text)
+
+
+@pytest.mark.parametrize("name", ["decode.cu", "dense_decode.cu", "index_score_tc.cu",
+                                  "prefill_index.cu", "prefill.cu", "tree_attention.cu"])
+def test_what_a_block_issued_ends_before_it_retires(name):
+    """A loader or MMA warp that looks for a timeout before the block's other warps are
+    done can miss one that they meet later: it waits for what it issued in any case, or
+    looks after a barrier with them."""
+    text = _code(os.path.join(CSRC, name))
+    assert not re.search(r"&\s*MSA_DEVERR_TIMEOUT", text)
+    drains = [m.start() for m in re.finditer(r"\bmbar_drain\(", text)]
+    assert drains
+    for m in re.finditer(r"\btimed_out\(", text):
+        before, after = text[max(0, m.start() - 250):m.start()], text[m.start():m.start() + 350]
+        if "mbar_drain(" in after:
+            assert re.search(r"__syncthreads\(\);|named_bar_sync\(kDone,", before), before
