@@ -88,6 +88,6 @@ def test_what_a_block_issued_ends_before_it_retires(name):
     drains = [m.start() for m in re.finditer(r"\bmbar_drain\(", text)]
     assert drains
     for m in re.finditer(r"\btimed_out\(", text):
-        before, after = text[max(0, m.start() - 250):m.start()], text[m.start():m.start() + 350]
+        before, after = text[max(0, m.start() - 250):m.start()], text[m.start():m.start() + 150]
         if "mbar_drain(" in after:
             assert re.search(r"__syncthreads\(\);|named_bar_sync\(kDone,", before), before
