@@ -874,9 +874,14 @@ dense_decode_kernel(WsView ws, DenseArgs a) {
 //
 // What bounds it: the softmax warps' chain of a page, from 5 nodes of 8 heads on; below,
 // the converters'.  32 requests of 8k-32k tokens, 8 KV heads (755 MB), 6 nodes, 48
-// rows: 273 us; 1 node 203, 4 nodes 241, 8 nodes 288.  Measured against it: one group
-// of four warps for everything 317 us (6 nodes); four warps that dequantise and four for
-// the softmax 297; four and twice four, of 32 rows each, 281 (1 node 241).  Unrolling
+// rows: 269 us (another draw of lengths 274); 1 node 202, 4 nodes 239, 8 nodes 280.  The
+// dense decode above, which knows chains only, takes 139 us for 1 new token, 161 for 2 and
+// 184 for 4: its shapes of 8, 16 and 32 rows with masks were not tried.  Measured against
+// this form: one group of four warps for everything 317 us (6 nodes); four warps that
+// dequantise and four for the softmax 297; four and twice four, of 32 rows each, 281 (1
+// node 241).  Pages are cut into ranges over all requests, those whose trees are too large
+// for this kernel among them: 4 such requests beside one of 131072 tokens and 40 nodes take
+// 259 us, alone 58 and 190.  Unrolling
 // the two halves of a conversion costs 20 us: the roles' loops share the instruction
 // cache.
 struct TreeShape {

@@ -67,13 +67,14 @@ tree_plan_kernel(WsView ws, const int32_t* __restrict__ parents, int64_t* __rest
 //
 // What bounds it is the chain of dependent loads ahead of a block's rows (header,
 // tree, path, block table: some 2 us) and, for many requests, the rows' traffic in
-// sectors of 32 bytes.  So the grid is one wave of the SMs' resident blocks, a block
-// walks the chain once and then takes one pool after the other.
+// sectors of 32 bytes.  So the grid is bounded (2432 blocks, of which 912 are resident: 78
+// registers let six stand on an SM), and a block walks the chain once and then takes one
+// pool after the other.
 // 64 requests of 16 nodes, 32 layers of three bf16 pools: 21 us with cold caches, 51 MB
 // read and as many written (a block per pool, 96 a request, each with its own walk of
 // the chain: 26 us); one request, 4 NVFP4 layers: 4.4 us.
 constexpr int kMoveThreads = 128, kDeep = 8, kMovePools = 192, kDistinctLayers = 1024;
-constexpr int kMoveBlocks = 16 * 152;          // resident at a time
+constexpr int kMoveBlocks = 16 * 152;          // of a grid, about
 
 struct Move {
   int32_t src_page, src_row, dst_page, dst_row;

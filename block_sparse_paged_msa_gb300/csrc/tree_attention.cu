@@ -5,12 +5,17 @@
 // Mathematics.  For node i and query head q of KV head h's group, over the keys u
 // that the node sees (the cached prefix, and the nodes of its mask):
 //     s_u = scale q . k_u,   out = sum_u 2^(s'_u - m) v_u / sum_u 2^(s'_u - m),
-// s' = s log2 e, in one pass with a running maximum m and sum.  Scores are bf16
-// products (bf16 pools) or fp16 ones (codes and their block scales are exact fp16
-// operands, and so are queries of 2^-14 .. 65504; larger ones are flagged, smaller
-// ones keep the bits of fp16's subnormals), accumulated in fp32.  Values enter P V
-// as fp16: exact for e4m3 and NVFP4, for bf16 within 2^-14 .. 65504 (as in the
-// prefill tiles; larger ones are flagged).  The probabilities are rounded to fp16
+// s' = s log2 e, in one pass with a running maximum m and sum.  Scores are sums in fp32
+// of products of
+//   bf16 pools   bf16 operands, as they are;
+//   e4m3 pools   e4m3 operands: the keys' codes as stored, a query row as two e4m3 rows
+//                times a power of two (split_e4m3: an element is off by at most 2^-17 of
+//                its row's largest; any finite bf16 query, none is flagged);
+//   NVFP4 pools  fp16 operands: codes times block scales are exact, and so are queries
+//                of 2^-14 .. 65504 (larger ones are flagged, smaller ones keep the bits
+//                of fp16's subnormals).
+// Values enter P V as fp16: exact for e4m3 and NVFP4, for bf16 within 2^-14 .. 65504 (as
+// in the prefill tiles; larger ones are flagged).  The probabilities are rounded to fp16
 // (2^-11 relative, below the bf16 rounding of the output), carried as 2^(s' - m +
 // 7) so that fp16's normal range reaches 2^-21 below the maximum; their sum is
 // taken before that rounding.  m is an unscaled score, and the scale is applied to
@@ -24,8 +29,9 @@
 // lengths and trees are; a group that lies in several ranges leaves one fp32
 // partial per CTA in the scratch, which a second kernel merges in CTA order.
 //
-// A CTA: a loader warp (pages by TMA into a ring), four converter warps (Q rows,
-// and the pages' rows as MMA operands), an MMA warp and two softmax warpgroups.  An
+// A CTA: a loader warp (pages by TMA into a ring), four converter warps (Q rows, and the
+// pages' values as MMA operands; four more for the keys of NVFP4 pages), two MMA warps and
+// two softmax warpgroups, and a warp that clears the rows of tokens that have no tree.  An
 // item is one (page, tile): S = Q K^T (128 rows x 128 keys), softmax by a thread a
 // row (its TMEM lane), P over S, O += P V with P as the A operand from TMEM.  Items
 // alternate between the warpgroups, each of which has TMEM of its own for S and O:
@@ -34,14 +40,14 @@
 // has its softmax, the tensor cores work for the other.
 //
 // What bounds it.  16 requests of 8k-32k tokens, 32 nodes, 64 + 8 heads, bf16 (1.31 GB,
-// 333 GFLOP): 277 us, 4.7 TB/s (0.70 of the measured copy bandwidth) and 1.2 PFLOP/s
+// 333 GFLOP): 282 us, 4.7 TB/s (0.69 of the measured copy bandwidth) and 1.2 PFLOP/s
 // together; the tensor pipe is active for 54 % of the time.  One request of 131071
 // tokens, 64 nodes, e4m3: 212 us, 1.3 PFLOP/s (0.67): an item takes an SM 0.93 us, some
 // 1770 cycles, of them 1024 of MMAs and, beside them, 1024 of exponentials at 16 a
-// cycle.  32 requests of 6 nodes (48 rows of a single tile): bf16 394 us, the copy
-// bandwidth; e4m3 263 us, 0.75 of it; NVFP4 of 16 nodes 469 us, the conversions.  61
-// requests of 40-6001 tokens, 1-40 nodes, 16 + 1 heads, e4m3: 68 us, some 30 of them
-// items, the rest the beginnings and ends of 260 segments and the merge.
+// cycle.  32 requests of 8k-32k tokens, 6 nodes (48 rows of a single tile): bf16 390 us,
+// the copy bandwidth; e4m3 258 us, 0.77 of it; NVFP4 of 9 and 16 nodes 386 and 392 us,
+// the conversions.  61 requests of 40-6001 tokens, 1-40 nodes, 16 + 1 heads, e4m3: 67 us,
+// some 30 of them items, the rest the beginnings and ends of 260 segments and the merge.
 #include <algorithm>
 #include <atomic>
 #include <cstring>

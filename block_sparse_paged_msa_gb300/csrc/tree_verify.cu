@@ -24,15 +24,16 @@
 // and in a pass the refused tokens are looked for once in several rounds of loads
 // (compared with every element they cost as much as the sums).  Sums of warps are
 // written to all blocks of the cluster through distributed shared memory, one cluster
-// barrier a pass, and one before the first (blocks that have not started have no shared
-// memory yet; its latency lies behind the nodes' loads); the first warp finds whose part holds the drawn token, and that warp
-// goes through its part again (from L2) for the token itself.
+// barrier a pass, and one before the first (a block that has not started has no shared
+// memory yet; the wait lies behind the nodes' loads, later it costs the same); the first
+// warp finds whose part holds the drawn token, and that warp goes through its part again
+// (from L2) for the token itself.
 //
 // What bounds it.  One request of 4 nodes, 32000 tokens: 6.5 us on the GPU, the chain
 // header - nodes - their entries - row - barrier - owner's part.  64 requests of 16
 // nodes, 131072 tokens (34 MB): 18 us, of them 5 to 7 for the rows (the two-sums' FMA
-// pipe).  24 requests with drawn drafts, 100003 tokens: 26 us, up to five passes of
-// 4.3 us one after the other.
+// pipe).  24 requests with drawn drafts, 100003 tokens: 26 to 29 us, by the paths taken:
+// up to five passes of 4.3 us one after the other.
 #include <cooperative_groups.h>
 
 #include "msa_device.cuh"

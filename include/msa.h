@@ -453,6 +453,12 @@ msa_status msa_dense_decode(const msa_config* cfg, void* ws, const void* q, cons
  * number of nodes per request up to MSA_MAX_TREE_NODES (cu_seqlens_q, or
  * cfg->q_len of them each).  The pages have chains only (vLLM
  * MiniMaxM3SparseMSAMetadataBuilder.build: decode_query_len).
+ *
+ * Trees are for full-attention layers: msa_index_score, msa_sparse_decode and
+ * msa_sparse_prefill see new tokens in causal order by position, in which a node
+ * would see its siblings.  A model with block-sparse layers verifies chains
+ * through them, or attends to its trees there by kernels of its own; the index
+ * pools of such layers can be passed to msa_tree_commit.
  */
 #define MSA_MAX_TREE_NODES 64
 
@@ -483,8 +489,11 @@ msa_status msa_tree_plan(const msa_config* cfg, void* ws, const int32_t* parents
  * A node that sees nothing gets out = 0, lse = -inf; so do idle requests' and
  * those of requests with more than MSA_MAX_TREE_NODES nodes (MSA_DEVERR_TREE).
  * What a node does not see does not reach it, infinities and NaN included.
- * Values beyond the fp16 range (and queries, with e4m3 or NVFP4 pools) set
- * MSA_DEVERR_FP16_RANGE.  Pages that the plan flagged are skipped.  Rows of out
+ * Values beyond the fp16 range (and queries, with NVFP4 pools) set
+ * MSA_DEVERR_FP16_RANGE.  With e4m3 pools a query row enters the scores as two
+ * e4m3 rows times a power of two: an element is off by at most 2^-17 of its row's
+ * largest magnitude.  For chains of up to 4 tokens over NVFP4 pools
+ * msa_dense_decode is the faster call.  Pages that the plan flagged are skipped.  Rows of out
  * and lse from T on are left as they are.  softmax_scale * k_scale has to be a
  * positive finite float; max_batch * max_blocks_per_req * H_kv < 2^27 and
  * num_pages * H_kv < 2^24, else MSA_ERR_UNSUPPORTED.
